@@ -190,7 +190,7 @@ def run(s):
             return dsl.paged_attention(s["q"], s["k_cache"], s["v_cache"], s["page_table"], s["kv_len"], s["cu_q"],
                                        s["max_q"], s["case"]["page"], causal=s["case"]["causal"], scale=s["scale"],
                                        out=s["out"], workspace=s["workspace"])
-        return dsl.prompt_attention(s["q"], s["k"], s["v"], s["cu"], s["max_len"], causal=s["case"]["causal"],
+        return dsl.prompt_attention(s["q"], s["k"], s["v"], s["cu"], causal=s["case"]["causal"],
                                     scale=s["scale"], out=s["out"])
     return {"append": _append_plain, "paged": _paged_plain, "prompt": _prompt_plain}[op](s)
 
