@@ -12,6 +12,11 @@ Stages (names follow the C ABI):
   markov_sample   stage 2, N-step low-rank Markov Gumbel-max loop (in place)
   admit           stage 4, survival by chain rule + pooled top-K admission
   verify          stage 3, lossless rejection-sampling verification
+The layers around them share one key-value cache:
+  context_kv        fills it for context tokens, from the target's hidden states
+  kv_append         a layer's new tokens into it, normed and rotated
+  paged_attention   a round's few query tokens per request over its pages
+  prompt_attention  attention over whole packed prompts
 plus build_inverse_map (reduced vocabulary), philox_blocks and
 race_exponentials (bit-exact access to the random numbers).
 """
@@ -29,6 +34,7 @@ __all__ = [
     "markov_workspace_size", "build_inverse_map", "verify", "verify_workspace_size", "verify_noalloc", "admit",
     "markov_sample_deferred", "verify_deferred", "verify_deferred_workspace_size",
     "context_kv", "context_kv_workspace_size",
+    "kv_append", "paged_attention", "paged_attention_workspace_size", "prompt_attention",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdspark.so")
@@ -69,6 +75,13 @@ _SIGS = {
     "dspark_context_kv_workspace_size": (_c_size, [_c_int] * 5),
     "dspark_context_kv": (_c_int, [_c_void_p] * 11 + [_c_int] * 6 + [_c_i64, ctypes.c_float, ctypes.c_float]
                           + [_c_void_p, _c_size, _c_void_p]),
+    "dspark_kv_append": (_c_int, [_c_void_p, _c_i64] * 3 + [_c_void_p] * 4 + [_c_void_p, _c_i64] * 2 + [_c_void_p] * 2
+                         + [_c_int] * 4 + [_c_i64, ctypes.c_float, ctypes.c_float, _c_void_p]),
+    "dspark_paged_attention_workspace_size": (_c_size, [_c_int] * 6),
+    "dspark_paged_attention": (_c_int, [_c_void_p, _c_i64] + [_c_void_p] * 7 + [_c_int] * 10
+                               + [ctypes.c_float, _c_void_p, _c_size, _c_void_p]),
+    "dspark_prompt_attention": (_c_int, [_c_void_p, _c_i64] * 3 + [_c_void_p] * 3 + [_c_int] * 6
+                                + [ctypes.c_float, _c_void_p]),
     "dspark_verify_deferred": (_c_int, [_c_void_p] * 8 + [_c_int] + [_c_void_p] * 3 + [_c_u64, _c_void_p, _c_void_p]
                                + [_c_int] * 3 + [_c_void_p, _c_size, _c_void_p]),
     "dspark_choose_k": (_c_int, [_c_void_p, _c_int, _c_int, _c_void_p, _c_int, _c_void_p, _c_void_p, _c_void_p]),
@@ -484,3 +497,150 @@ def admit(cond_accept: torch.Tensor, K: int, survival: Optional[torch.Tensor] = 
         _ptr(cond_accept, "cond_accept", _F32, dev), B, N, K, _ptr(survival, "survival", _F32, dev, (B, N)),
         _ptr(admit_len, "admit_len", _I32, dev, (B,)), _stream(cond_accept)))
     return survival, admit_len
+
+
+# ---------------------------------------------------------------- the cache and attention over it
+
+def _rows(t: torch.Tensor, name: str, device, shape) -> int:
+    """Element distance between the tokens of a [tokens, heads, hd] bf16 tensor whose
+    heads lie contiguously: a tensor of its own or a column range of a wider product."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _BF16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {_BF16}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    rows, heads, hd = shape
+    row, head, one = t.stride()
+    if (one != 1 and hd > 1) or (head != hd and heads > 1):
+        raise ValueError(f"{name}: the heads of a token must lie contiguously (strides {t.stride()})")
+    if rows <= 1:
+        return heads * hd
+    return row
+
+
+def _device_of(t: torch.Tensor, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device (cuda/hip) tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, hd], got shape {tuple(t.shape)}")
+    return t.device
+
+
+def _on(dev, name: str, call, *args) -> None:
+    """call(*args, stream) on dev's current stream, with dev the current device."""
+    if dev.index == torch.cuda.current_device():
+        status = call(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = call(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != 0:
+        _check(name, status)
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+              k_cache: torch.Tensor, v_cache: torch.Tensor, q: Optional[torch.Tensor] = None,
+              qnorm_w: Optional[torch.Tensor] = None, knorm_w: Optional[torch.Tensor] = None,
+              q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+              eps: float = 1e-6, rope_theta: float = 1e6) -> Optional[torch.Tensor]:
+    """One layer's new tokens into the cache (dspark_kv_append): head norm (where a weight
+    is given) and rotate-half RoPE at positions [M] int32 on k [M, nkv, hd] and q
+    [M, nh, hd]; k and v into k_cache, v_cache [num_slots, nkv, hd] bf16 at slots [M]
+    int64 (outside the cache: skipped), the rotated q to q_out (new unless given; q itself
+    for in place) and, if given, the rotated k to k_out.  q, k and v may be column ranges
+    of one product.  Returns q_out (None without q)."""
+    dev = _device_of(k, "k")
+    M, nkv, hd = k.shape
+    if k_cache.dim() != 3:
+        raise ValueError(f"k_cache must be [num_slots, nkv, hd], got shape {tuple(k_cache.shape)}")
+    S = k_cache.shape[0]
+    ks, vs = _rows(k, "k", dev, k.shape), _rows(v, "v", dev, k.shape)
+    nh = qs = qos = kos = 0
+    qp = qop = kop = None
+    if q is not None:
+        _device_of(q, "q")
+        nh = q.shape[1]
+        qs = _rows(q, "q", dev, (M, nh, hd))
+        if q_out is None:
+            q_out = torch.empty((M, nh, hd), dtype=q.dtype, device=dev)
+        qos = _rows(q_out, "q_out", dev, (M, nh, hd))
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None or qnorm_w is not None:
+        raise ValueError("q_out and qnorm_w need q")
+    if k_out is not None:
+        kos = _rows(k_out, "k_out", dev, k.shape)
+        kop = k_out.data_ptr()
+    _on(dev, "dspark_kv_append", load().dspark_kv_append,
+        qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(qnorm_w, "qnorm_w", _BF16, dev, (hd,)),
+        _ptr(knorm_w, "knorm_w", _BF16, dev, (hd,)), _ptr(positions, "positions", _I32, dev, (M,)),
+        _ptr(slots, "slots", _I64, dev, (M,)), qop, qos, kop, kos,
+        _ptr(k_cache, "k_cache", _BF16, dev, (S, nkv, hd)), _ptr(v_cache, "v_cache", _BF16, dev, (S, nkv, hd)),
+        M, nh, nkv, hd, S, eps, rope_theta)
+    return q_out
+
+
+def paged_attention_workspace_size(T: int, B: int, max_q: int, nh: int, nkv: int, hd: int) -> int:
+    return load().dspark_paged_attention_workspace_size(T, B, max_q, nh, nkv, hd)
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                    kv_len: torch.Tensor, cu_q: torch.Tensor, max_q: int, page_size: int, causal: bool = True,
+                    scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of each request's few query tokens over its cache (dspark_paged_attention).
+    q [T, nh, hd] bf16, the tokens cu_q[b] .. cu_q[b+1] - 1 (cu_q [B+1] int32) of request b
+    being the last of its kv_len[b] (int32) cached ones; page p of k_cache, v_cache
+    [num_slots, nkv, hd] is the slots p * page_size .. and page_table [B, max_pages] int32
+    lists a request's pages.  scale defaults to hd ** -0.5.  lse [T, nh] float32, if given,
+    receives each row's log sum of exponentials.  Returns out [T, nh, hd]."""
+    dev = _device_of(q, "q")
+    T, nh, hd = q.shape
+    qs = _rows(q, "q", dev, q.shape)
+    if k_cache.dim() != 3 or page_table.dim() != 2:
+        raise ValueError("k_cache must be [num_slots, nkv, hd] and page_table [B, max_pages]")
+    S, nkv = k_cache.shape[0], k_cache.shape[1]
+    B, width = page_table.shape
+    if page_size < 1 or S % page_size:
+        raise ValueError(f"num_slots ({S}) must be a multiple of page_size ({page_size})")
+    if out is None:
+        out = torch.empty((T, nh, hd), dtype=q.dtype, device=dev)
+    lib = load()
+    ws = _workspace(workspace, lib.dspark_paged_attention_workspace_size(T, B, max_q, nh, nkv, hd), dev)
+    if ws.device != dev:
+        raise ValueError(f"workspace is on {ws.device}, expected {dev}")
+    _on(dev, "dspark_paged_attention", lib.dspark_paged_attention,
+        q.data_ptr(), qs, _ptr(k_cache, "k_cache", _BF16, dev, (S, nkv, hd)),
+        _ptr(v_cache, "v_cache", _BF16, dev, (S, nkv, hd)), _ptr(page_table, "page_table", _I32, dev, (B, width)),
+        _ptr(kv_len, "kv_len", _I32, dev, (B,)), _ptr(cu_q, "cu_q", _I32, dev, (B + 1,)),
+        _ptr(out, "out", _BF16, dev, (T, nh, hd)), _ptr(lse, "lse", _F32, dev, (T, nh)), T, B, max_q, nh, nkv, hd,
+        page_size, width, S // page_size, 1 if causal else 0, hd ** -0.5 if scale is None else scale,
+        ws.data_ptr(), ws.numel())
+    return out
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                     causal: bool = True, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention over packed prompts (dspark_prompt_attention): q [T, nh, hd], k and v
+    [T, nkv, hd] bf16 (each may be a column range of one product), sequence b the tokens
+    cu_seqlens[b] .. cu_seqlens[b+1] - 1 (int32 [B+1]).  scale defaults to hd ** -0.5.
+    lse [T, nh] float32, if given, receives each row's log sum of exponentials.
+    Returns out [T, nh, hd]."""
+    dev = _device_of(q, "q")
+    T, nh, hd = q.shape
+    _device_of(k, "k")
+    nkv = k.shape[1]
+    qs = _rows(q, "q", dev, q.shape)
+    ks, vs = _rows(k, "k", dev, (T, nkv, hd)), _rows(v, "v", dev, (T, nkv, hd))
+    B = cu_seqlens.numel() - 1
+    if out is None:
+        out = torch.empty((T, nh, hd), dtype=q.dtype, device=dev)
+    _on(dev, "dspark_prompt_attention", load().dspark_prompt_attention,
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(cu_seqlens, "cu_seqlens", _I32, dev, (B + 1,)),
+        _ptr(out, "out", _BF16, dev, (T, nh, hd)), _ptr(lse, "lse", _F32, dev, (T, nh)), T, B, nh, nkv, hd,
+        1 if causal else 0, hd ** -0.5 if scale is None else scale)
+    return out

@@ -1,0 +1,50 @@
+// Building blocks of the two attention kernels: bf16 packing, the finiteness test of
+// masked tiles, the online-softmax constants.
+#pragma once
+
+#include "device.hpp"
+
+namespace dspark {
+
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef short shortx4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// two floats to packed bf16, round to nearest even (one instruction on gfx950)
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((floatx2{a, b}), bf16x2));
+}
+
+// whether a pair of bf16 holds an infinity or a NaN (exponent bits all set)
+__device__ __forceinline__ bool bf16x2_nonfinite(uint32_t w) {
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
+// transposing LDS read: the 16 lanes of a quarter wave name four rows of 16 bf16 (lane i
+// the 8 bytes i % 4 of row i / 4); lane i gets column i of them, four values
+typedef __attribute__((address_space(3))) shortx4 lds_shortx4;
+__device__ __forceinline__ shortx4 lds_read_tr(const char* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4*)p);
+}
+
+// global -> LDS without registers: lane i's 16 bytes go to lds_base + 16 i
+__device__ __forceinline__ void load_to_lds16(const uint16_t* src, char* lds_base) {
+  __builtin_amdgcn_global_load_lds(src, lds_base, 16, 0, 0);
+}
+
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+// A wave-uniform value as a scalar.  MFMA instructions ignore the execution mask, so a
+// branch around one has to be a scalar branch: its condition goes through here.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// log(sum exp) of a row from its base-2 maximum and sum; -inf for a row that saw nothing
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0.0f ? -INFINITY : l;
+}
+
+}  // namespace dspark

@@ -431,6 +431,194 @@ dspark_status dspark_verify_coupled(const float* target_logits, const int32_t* d
                     "verify_coupled");
 }
 
+dspark_status dspark_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                               const uint16_t* v, int64_t v_stride, const uint16_t* qnorm_w,
+                               const uint16_t* knorm_w, const int32_t* positions, const int64_t* slots,
+                               uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out, int64_t k_out_stride,
+                               uint16_t* k_cache, uint16_t* v_cache, int M, int nh, int nkv, int hd,
+                               int64_t num_slots, float eps, float rope_theta, void* stream) {
+  REQUIRE(M >= 0, DSPARK_ERR_INVALID, "M must be >= 0 (got %d)", M);
+  REQUIRE(M <= (1 << 22), DSPARK_ERR_UNSUPPORTED, "M must be <= 2^22 (got %d)", M);
+  REQUIRE(nkv >= 1, DSPARK_ERR_INVALID, "nkv must be >= 1 (got %d)", nkv);
+  REQUIRE(nkv <= 1024, DSPARK_ERR_UNSUPPORTED, "nkv must be <= 1024 (got %d)", nkv);
+  REQUIRE(hd > 0 && hd % 2 == 0, DSPARK_ERR_INVALID, "hd must be positive and even (got %d)", hd);
+  REQUIRE(hd == 32 || hd == 64 || hd == 128 || hd == 256, DSPARK_ERR_UNSUPPORTED,
+          "hd must be 32, 64, 128 or 256 (got %d)", hd);
+  REQUIRE(num_slots >= 1, DSPARK_ERR_INVALID, "num_slots must be >= 1");
+  REQUIRE(eps >= 0.0f && std::isfinite(eps), DSPARK_ERR_INVALID, "eps must be finite and >= 0");
+  REQUIRE(rope_theta > 0.0f && std::isfinite(rope_theta), DSPARK_ERR_INVALID, "rope_theta must be finite and > 0");
+  REQUIRE((q == nullptr) == (q_out == nullptr), DSPARK_ERR_INVALID, "q and q_out must be both given or both NULL");
+  const int64_t krow = (int64_t)nkv * hd;
+  if (q) {
+    REQUIRE(nh >= 1, DSPARK_ERR_INVALID, "nh must be >= 1 (got %d)", nh);
+    REQUIRE(nh <= 1024, DSPARK_ERR_UNSUPPORTED, "nh must be <= 1024 (got %d)", nh);
+    const int64_t qrow = (int64_t)nh * hd;
+    REQUIRE(q_stride >= qrow && q_stride % 8 == 0 && q_out_stride >= qrow && q_out_stride % 8 == 0,
+            DSPARK_ERR_INVALID, "q_stride and q_out_stride must be multiples of 8 and >= nh * hd");
+    REQUIRE(q != q_out || q_stride == q_out_stride, DSPARK_ERR_INVALID, "q_out in place of q needs q's stride");
+  }
+  REQUIRE(k_stride >= krow && k_stride % 8 == 0 && v_stride >= krow && v_stride % 8 == 0, DSPARK_ERR_INVALID,
+          "k_stride and v_stride must be multiples of 8 and >= nkv * hd");
+  if (k_out) {
+    REQUIRE(k_out_stride >= krow && k_out_stride % 8 == 0, DSPARK_ERR_INVALID,
+            "k_out_stride must be a multiple of 8 and >= nkv * hd");
+    REQUIRE(k != k_out || k_stride == k_out_stride, DSPARK_ERR_INVALID, "k_out in place of k needs k's stride");
+  }
+  if (M == 0) return ok();
+  REQUIRE_PTR16(k, "k");
+  REQUIRE_PTR16(v, "v");
+  REQUIRE(aligned16(q) && aligned16(q_out) && aligned16(k_out), DSPARK_ERR_INVALID,
+          "q, q_out and k_out must be 16-byte aligned");
+  REQUIRE(aligned16(qnorm_w) && aligned16(knorm_w), DSPARK_ERR_INVALID, "norm weights must be 16-byte aligned");
+  REQUIRE_PTR(positions, "positions");
+  REQUIRE_PTR(slots, "slots");
+  REQUIRE_PTR16(k_cache, "k_cache");
+  REQUIRE_PTR16(v_cache, "v_cache");
+  dspark::AppendArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.qnorm_w = qnorm_w;
+  a.knorm_w = knorm_w;
+  a.positions = positions;
+  a.slots = slots;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.q_out_stride = q_out_stride;
+  a.k_out_stride = k_out_stride;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.nh = q ? nh : 0;
+  a.nkv = nkv;
+  a.num_slots = num_slots;
+  a.eps = eps;
+  a.log2_theta = std::log2((double)rope_theta);
+  return hip_status(dspark::launch_kv_append(a, M, hd, (hipStream_t)stream), "kv_append");
+}
+
+size_t dspark_paged_attention_workspace_size(int T, int B, int max_q, int nh, int nkv, int hd) {
+  if (T <= 0 || B <= 0 || max_q <= 0 || nkv <= 0 || nh < nkv || hd <= 0 || nh > 1024 || hd > 256 ||
+      B > DSPARK_MAX_SEQS || max_q > DSPARK_MAX_BLOCK)
+    return 0;
+  return dspark::paged_attention_workspace_bytes(T, B, max_q, nh, nkv, hd);
+}
+
+}  // extern "C"
+
+namespace {
+// what the two attention calls check alike
+dspark_status attention_shape(int T, int B, int nh, int nkv, int hd, float scale) {
+  REQUIRE(T >= 0, DSPARK_ERR_INVALID, "T must be >= 0 (got %d)", T);
+  REQUIRE(B >= 1, DSPARK_ERR_INVALID, "B must be >= 1 (got %d)", B);
+  REQUIRE(B <= DSPARK_MAX_SEQS, DSPARK_ERR_UNSUPPORTED, "B must be <= %d (got %d)", DSPARK_MAX_SEQS, B);
+  REQUIRE(nkv >= 1 && nh >= 1 && nh % nkv == 0, DSPARK_ERR_INVALID,
+          "nh must be a positive multiple of nkv (got nh=%d, nkv=%d)", nh, nkv);
+  REQUIRE(nh <= 1024, DSPARK_ERR_UNSUPPORTED, "nh must be <= 1024 (got %d)", nh);
+  REQUIRE(hd > 0 && hd % 2 == 0, DSPARK_ERR_INVALID, "hd must be positive and even (got %d)", hd);
+  REQUIRE(hd == 64 || hd == 128 || hd == 256, DSPARK_ERR_UNSUPPORTED, "hd must be 64, 128 or 256 (got %d)", hd);
+  REQUIRE(scale > 0.0f && std::isfinite(scale), DSPARK_ERR_INVALID, "scale must be finite and > 0");
+  REQUIRE((int64_t)T * nh < ((int64_t)1 << 30), DSPARK_ERR_UNSUPPORTED, "T * nh must be < 2^30");
+  return DSPARK_OK;
+}
+}  // namespace
+
+extern "C" {
+
+dspark_status dspark_paged_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k_cache,
+                                     const uint16_t* v_cache, const int32_t* page_table, const int32_t* kv_len,
+                                     const int32_t* cu_q, uint16_t* out, float* lse, int T, int B, int max_q,
+                                     int nh, int nkv, int hd, int page_size, int max_pages, int num_pages,
+                                     int causal, float scale, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  const dspark_status st = attention_shape(T, B, nh, nkv, hd, scale);
+  if (st != DSPARK_OK) return st;
+  REQUIRE(q_stride >= (int64_t)nh * hd && q_stride % 8 == 0, DSPARK_ERR_INVALID,
+          "q_stride must be a multiple of 8 and >= nh * hd (got %lld)", (long long)q_stride);
+  REQUIRE(max_q >= 1, DSPARK_ERR_INVALID, "max_q must be >= 1 (got %d)", max_q);
+  REQUIRE(max_q <= DSPARK_MAX_BLOCK, DSPARK_ERR_UNSUPPORTED, "max_q must be <= %d (got %d)", DSPARK_MAX_BLOCK, max_q);
+  REQUIRE(page_size >= 1, DSPARK_ERR_INVALID, "page_size must be >= 1 (got %d)", page_size);
+  REQUIRE((page_size & (page_size - 1)) == 0, DSPARK_ERR_UNSUPPORTED, "page_size must be a power of two (got %d)",
+          page_size);
+  REQUIRE(max_pages >= 1 && num_pages >= 1, DSPARK_ERR_INVALID, "max_pages and num_pages must be >= 1");
+  REQUIRE((int64_t)max_pages * page_size < ((int64_t)1 << 31) && (int64_t)num_pages * page_size < ((int64_t)1 << 31),
+          DSPARK_ERR_UNSUPPORTED, "max_pages * page_size and num_pages * page_size must be < 2^31");
+  REQUIRE(causal == 0 || causal == 1, DSPARK_ERR_INVALID, "causal must be 0 or 1 (got %d)", causal);
+  if (T == 0) return ok();
+  REQUIRE_PTR16(q, "q");
+  REQUIRE_PTR16(k_cache, "k_cache");
+  REQUIRE_PTR16(v_cache, "v_cache");
+  REQUIRE_PTR(page_table, "page_table");
+  REQUIRE_PTR(kv_len, "kv_len");
+  REQUIRE_PTR(cu_q, "cu_q");
+  REQUIRE_PTR16(out, "out");
+  const size_t need = dspark::paged_attention_workspace_bytes(T, B, max_q, nh, nkv, hd);
+  REQUIRE(workspace != nullptr, DSPARK_ERR_WORKSPACE, "workspace must not be NULL (%zu bytes needed)", need);
+  REQUIRE(aligned16(workspace), DSPARK_ERR_INVALID, "workspace must be 16-byte aligned");
+  REQUIRE(workspace_bytes >= need, DSPARK_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", workspace_bytes,
+          need);
+  dspark::PagedArgs a;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.page_table = page_table;
+  a.kv_len = kv_len;
+  a.cu_q = cu_q;
+  a.out = out;
+  a.lse = lse;
+  a.q_stride = q_stride;
+  a.T = T;
+  a.B = B;
+  a.max_q = max_q;
+  a.nh = nh;
+  a.nkv = nkv;
+  a.page_shift = __builtin_ctz((unsigned)page_size);
+  a.width = max_pages;
+  a.num_pages = num_pages;
+  a.causal = causal;
+  a.scale = scale;
+  return hip_status(dspark::launch_paged_attention(a, hd, workspace, (hipStream_t)stream), "paged_attention");
+}
+
+dspark_status dspark_prompt_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                      const uint16_t* v, int64_t v_stride, const int32_t* cu_seqlens, uint16_t* out,
+                                      float* lse, int T, int B, int nh, int nkv, int hd, int causal, float scale,
+                                      void* stream) {
+  const dspark_status st = attention_shape(T, B, nh, nkv, hd, scale);
+  if (st != DSPARK_OK) return st;
+  const int64_t qrow = (int64_t)nh * hd, krow = (int64_t)nkv * hd;
+  REQUIRE(q_stride >= qrow && q_stride % 8 == 0, DSPARK_ERR_INVALID,
+          "q_stride must be a multiple of 8 and >= nh * hd (got %lld)", (long long)q_stride);
+  REQUIRE(k_stride >= krow && k_stride % 8 == 0 && v_stride >= krow && v_stride % 8 == 0, DSPARK_ERR_INVALID,
+          "k_stride and v_stride must be multiples of 8 and >= nkv * hd");
+  REQUIRE(causal == 0 || causal == 1, DSPARK_ERR_INVALID, "causal must be 0 or 1 (got %d)", causal);
+  if (T == 0) return ok();
+  REQUIRE_PTR16(q, "q");
+  REQUIRE_PTR16(k, "k");
+  REQUIRE_PTR16(v, "v");
+  REQUIRE_PTR(cu_seqlens, "cu_seqlens");
+  REQUIRE_PTR16(out, "out");
+  dspark::PromptArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.cu_seqlens = cu_seqlens;
+  a.out = out;
+  a.lse = lse;
+  a.T = T;
+  a.B = B;
+  a.nh = nh;
+  a.nkv = nkv;
+  a.causal = causal;
+  a.scale = scale;
+  return hip_status(dspark::launch_prompt_attention(a, hd, (hipStream_t)stream), "prompt_attention");
+}
+
 dspark_status dspark_admit(const float* cond_accept, int B, int N, int K, float* survival, int32_t* admit_len,
                            void* stream) {
   REQUIRE(B >= 1, DSPARK_ERR_INVALID, "B must be >= 1 (got %d)", B);

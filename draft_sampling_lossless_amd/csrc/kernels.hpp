@@ -134,6 +134,60 @@ hipError_t launch_context_kv(const uint16_t* aux, const uint16_t* fc_w, const ui
                              const int32_t* positions, const int64_t* slots, uint16_t* k_cache, uint16_t* v_cache,
                              int M, int H_in, int Hd, int L, int nkv, int hd, int64_t num_slots, float eps,
                              float theta, void* workspace, hipStream_t stream);
+// ---- a layer's cache and the attention over it
+struct AppendArgs {
+  const uint16_t* q = nullptr;        // [M, nh, hd] bf16, rows q_stride apart (nh == 0: none)
+  const uint16_t* k = nullptr;        // [M, nkv, hd]
+  const uint16_t* v = nullptr;        // [M, nkv, hd]
+  int64_t q_stride = 0, k_stride = 0, v_stride = 0;
+  const uint16_t* qnorm_w = nullptr;  // [hd] or null: no norm
+  const uint16_t* knorm_w = nullptr;
+  const int32_t* positions = nullptr; // [M]
+  const int64_t* slots = nullptr;     // [M]; a slot outside [0, num_slots) is skipped
+  uint16_t* q_out = nullptr;          // may be q itself, at q's stride
+  uint16_t* k_out = nullptr;          // or null; may be k itself, at k's stride
+  int64_t q_out_stride = 0, k_out_stride = 0;
+  uint16_t* k_cache = nullptr;        // [num_slots, nkv, hd]
+  uint16_t* v_cache = nullptr;
+  int nh = 0, nkv = 0;
+  int64_t num_slots = 0;
+  float eps = 0.0f;
+  double log2_theta = 0.0;
+};
+hipError_t launch_kv_append(const AppendArgs& a, int M, int hd, hipStream_t stream);
+
+struct PagedArgs {
+  const uint16_t* q = nullptr;        // [T, nh, hd] bf16, rows q_stride apart
+  const uint16_t* k_cache = nullptr;  // [num_pages << page_shift, nkv, hd]
+  const uint16_t* v_cache = nullptr;
+  const int32_t* page_table = nullptr;  // [B, width]
+  const int32_t* kv_len = nullptr;    // [B]
+  const int32_t* cu_q = nullptr;      // [B + 1]
+  uint16_t* out = nullptr;            // [T, nh, hd]
+  float* lse = nullptr;               // [T, nh] or null
+  int64_t q_stride = 0;
+  int T = 0, B = 0, max_q = 0, nh = 0, nkv = 0;
+  int page_shift = 0, width = 0, num_pages = 0;
+  int causal = 0;
+  float scale = 0.0f;
+};
+size_t paged_attention_workspace_bytes(int T, int B, int max_q, int nh, int nkv, int hd);
+hipError_t launch_paged_attention(const PagedArgs& a, int hd, void* workspace, hipStream_t stream);
+
+struct PromptArgs {
+  const uint16_t* q = nullptr;        // [T, nh, hd] bf16, rows q_stride apart
+  const uint16_t* k = nullptr;        // [T, nkv, hd]
+  const uint16_t* v = nullptr;
+  int64_t q_stride = 0, k_stride = 0, v_stride = 0;
+  const int32_t* cu_seqlens = nullptr;  // [B + 1]
+  uint16_t* out = nullptr;            // [T, nh, hd]
+  float* lse = nullptr;               // [T, nh] or null
+  int T = 0, B = 0, nh = 0, nkv = 0;
+  int causal = 0;
+  float scale = 0.0f;
+};
+hipError_t launch_prompt_attention(const PromptArgs& a, int hd, hipStream_t stream);
+
 // launch_verify with the library's static per-device scratch array as workspace
 constexpr size_t kVerifyScratchBytes = (size_t)4 << 20;
 hipError_t launch_verify_noalloc(int input_kind, const float* target, const float* draft, const float* draft_log_z,

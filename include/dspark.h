@@ -15,6 +15,9 @@
  *                         stages 2 and 3 without storing every processed draft row
  *   dspark_context_kv     the step before the path: draft KV cache of new context
  *                         tokens from the target's hidden states [P1 §4]
+ *   dspark_kv_append      a layer's new tokens into that cache, normed and rotated
+ *   dspark_paged_attention  a round's few query tokens over the pages of that cache
+ *   dspark_prompt_attention attention over whole packed prompts
  *
  * Conventions shared by every call
  *   Memory     Every pointer argument is device memory (HBM) unless stated otherwise.
@@ -79,6 +82,8 @@ enum { DSPARK_INPUT_LOGITS = 0, DSPARK_INPUT_PROBS = 1 };
 #define DSPARK_MAX_RANK 256      /* Markov rank r                                    */
 #define DSPARK_MAX_B 65535       /* requests                                          */
 #define DSPARK_MAX_ADMIT 16384   /* B * N of one admission call                       */
+#define DSPARK_MAX_SEQS 4096     /* sequences of one attention call                   */
+#define DSPARK_MAX_BLOCK 128     /* query tokens per request of dspark_paged_attention */
 
 /* ABI version of the loaded library (== DSPARK_ABI_VERSION of its header). */
 int dspark_abi_version(void);
@@ -395,6 +400,98 @@ dspark_status dspark_context_kv(const uint16_t* aux, const uint16_t* fc_w, const
                                 uint16_t* k_cache, uint16_t* v_cache, int num_ctx, int H_in, int H_d,
                                 int L, int nkv, int hd, int64_t num_slots, float eps, float rope_theta,
                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- cache append
+ * One layer's new tokens into the key-value cache dspark_context_kv fills: the tokens a
+ * round itself runs through the model (the anchor and its drafts), or a prompt's.
+ * For token m, every head x of q[m] and k[m]:
+ *   x = x / sqrt(mean_i x_i^2 + eps) * w       w = qnorm_w / knorm_w; skipped where NULL
+ *   x = rotate-half RoPE: for i < hd/2 the pair (x_i, x_{i+hd/2}) rotated by
+ *       angle positions[m] * rope_theta^(-2i/hd)
+ *   q_out[m] = bf16(q');  k_cache[s] = bf16(k'), v_cache[s] = v[m] with s = slots[m];
+ *   k_out[m] = bf16(k') too where k_out is given (the packed rotated keys that
+ *   dspark_prompt_attention reads).
+ *   q [M, nh, hd], k, v [M, nkv, hd] bf16 bits, device, 16-byte aligned; token m's heads
+ *   lie contiguously at q + m * q_stride elements (k_stride, v_stride alike), so the
+ *   three may be column ranges of one fused projection output.  q NULL (then q_out
+ *   NULL): keys and values only; nh is ignored.
+ *   qnorm_w, knorm_w [hd] bf16 or NULL, 16-byte aligned.  positions [M] int32; slots [M]
+ *   int64; a slot outside [0, num_slots) is skipped (nothing cached for that token, its
+ *   q_out and k_out rows are still written).  Slots inside the cache must be distinct:
+ *   which of two tokens with one slot ends up there, and whether whole, is undefined.
+ *   q_out, k_out: bf16, rows q_out_stride / k_out_stride elements apart, 16-byte
+ *   aligned.  q_out may be q and k_out may be k (same pointer, same stride: in place);
+ *   otherwise outputs must not overlap inputs.
+ *   k_cache, v_cache [num_slots, nkv, hd] bf16 (one layer of dspark_context_kv's
+ *   caches), 16-byte aligned, other slots untouched.
+ *   hd in {32, 64, 128, 256} (else UNSUPPORTED); strides % 8 == 0 and at least one
+ *   token's row; 1 <= nkv, nh <= 1024; eps >= 0, rope_theta > 0; M <= 2^22,
+ *   M == 0 enqueues nothing.
+ *   Norms and rotation in float32, angles reduced in double, one rounding to bf16. */
+dspark_status dspark_kv_append(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                               const uint16_t* v, int64_t v_stride, const uint16_t* qnorm_w,
+                               const uint16_t* knorm_w, const int32_t* positions, const int64_t* slots,
+                               uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out, int64_t k_out_stride,
+                               uint16_t* k_cache, uint16_t* v_cache, int M, int nh, int nkv, int hd,
+                               int64_t num_slots, float eps, float rope_theta, void* stream);
+
+/* ---------------------------------------------------------------- paged attention
+ * Attention of a few new tokens per request over the request's cache: one token (plain
+ * decode), the anchor and its drafts (the verify forward, causal), or the draft's
+ * parallel block (every position sees the whole block, causal = 0) [P2 §3].
+ * Request b has the query tokens cu_q[b] <= t < cu_q[b+1] (n_b of them, at the end of
+ * its kv_len[b] cached tokens, their own keys and values included).  Key s of request b
+ * lies at slot page_table[b, s / page_size] * page_size + s % page_size.  For head h,
+ * with kv head h / (nh / nkv), query t = cu_q[b] + j:
+ *   out[t, h] = sum_s p_s v_s,  p = softmax_s(scale * q[t, h] . k_s)
+ *   over s < kv_len[b], and s <= kv_len[b] - n_b + j where causal is set.
+ *   A row that sees no key gets zeros.  Keys a row does not see have no influence on
+ *   it, whatever their values (NaN and infinities included).
+ *   lse[t, h] (optional, NULL = none) = log sum_s exp(scale * q . k_s), -inf for a row
+ *   that sees no key: what a caller needs to join the result with another part's.
+ *   q [T, nh, hd] bf16 bits, rows q_stride elements apart (% 8 == 0, >= nh * hd), device,
+ *   16-byte aligned; k_cache, v_cache [num_pages * page_size, nkv, hd] bf16, 16-byte
+ *   aligned (a layer of dspark_context_kv's caches; page_size 1: the table holds slots);
+ *   page_table [B, max_pages] int32, kv_len [B] int32, cu_q [B + 1] int32 ascending
+ *   from 0, all device; out [T, nh, hd] bf16, 16-byte aligned; lse [T, nh] float32.
+ *   max_q: at least the largest n_b; tokens of a request beyond it, and rows behind
+ *   cu_q[B], are left as they were.  A page outside [0, num_pages) hides its keys from
+ *   every row; kv_len is taken as at most max_pages * page_size and at least 0.
+ *   page_size a power of two; hd in {64, 128, 256}; nh % nkv == 0; nh <= 1024;
+ *   1 <= B <= DSPARK_MAX_SEQS; 1 <= max_q <= DSPARK_MAX_BLOCK; num_pages * page_size and
+ *   max_pages * page_size < 2^31; T * nh < 2^30; scale > 0 and finite; T == 0
+ *   enqueues nothing.
+ *   Products on bf16 MFMA, accumulated in float32; softmax statistics and sums float32;
+ *   the softmax weights are rounded to bf16 for the second product (its operand type).
+ *   Long caches are split over workgroups and joined in a fixed order: results repeat
+ *   bit for bit.  workspace >= dspark_paged_attention_workspace_size(...) bytes, device,
+ *   16-byte aligned. */
+size_t dspark_paged_attention_workspace_size(int T, int B, int max_q, int nh, int nkv, int hd);
+dspark_status dspark_paged_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k_cache,
+                                     const uint16_t* v_cache, const int32_t* page_table, const int32_t* kv_len,
+                                     const int32_t* cu_q, uint16_t* out, float* lse, int T, int B, int max_q,
+                                     int nh, int nkv, int hd, int page_size, int max_pages, int num_pages,
+                                     int causal, float scale, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/* ---------------------------------------------------------------- prompt attention
+ * Attention over whole prompts, packed: sequence b is the tokens cu_seqlens[b] <= t <
+ * cu_seqlens[b+1].  For head h with kv head h / (nh / nkv), token t of sequence b:
+ *   out[t, h] = sum_s p_s v[s],  p = softmax_s(scale * q[t, h] . k[s])
+ *   over the tokens s of sequence b, s <= t where causal is set.
+ *   lse as dspark_paged_attention's.  Sequences may be empty; rows behind cu_seqlens[B]
+ *   are left as they were; keys a row does not see have no influence on it.
+ *   q [T, nh, hd], k, v [T, nkv, hd] bf16 bits, token rows q_stride, k_stride, v_stride
+ *   elements apart (each % 8 == 0 and at least one row), device, 16-byte aligned;
+ *   cu_seqlens [B + 1] int32 ascending from 0, device; out [T, nh, hd] bf16, 16-byte
+ *   aligned; lse [T, nh] float32 or NULL.
+ *   hd in {64, 128, 256}; nh % nkv == 0; nh <= 1024; 1 <= B <= DSPARK_MAX_SEQS; scale > 0
+ *   and finite; T * nh < 2^30; T == 0 enqueues nothing.  Arithmetic as
+ *   dspark_paged_attention's.  No workspace. */
+dspark_status dspark_prompt_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                      const uint16_t* v, int64_t v_stride, const int32_t* cu_seqlens, uint16_t* out,
+                                      float* lse, int T, int B, int nh, int nkv, int hd, int causal, float scale,
+                                      void* stream);
 
 /* ---------------------------------------------------------------- end of a round
  * The next round's anchors ["DSpark 的实现和测评" §2.1: the anchor of a request is the

@@ -1,0 +1,540 @@
+"""dspark_kv_append, dspark_paged_attention and dspark_prompt_attention against the oracle
+(oracle/attention.py, float64).
+
+Bounds.  A rounding to bf16 is off by at most 2^-8 of the value.
+  * append: one such rounding of the output, and float32 work of a few tens of operations
+    on the pair (x, y): |err| <= 2^-8 |ref| + 2^-18 sqrt(x^2 + y^2).
+  * attention: the output's rounding, 2^-8 |ref|; the weights' rounding, 2^-8 sum p|v|
+    =: 2^-8 A; and float32 errors, each relative to A: a score of magnitude at most
+    D = max scale sum|q||k| is off by e_s <= (hd + 4) 2^-24 D (accumulation and scaling)
+    and moves a weight by e_s, its exponential by 2^-22 (argument and hardware rounding,
+    up to 2^-23 of the argument's magnitude 2 D log2 e), numerator and denominator both; the sums
+    over n keys are off by n 2^-24 each.  Together
+        |err| <= 2^-8 |ref| + A (2^-8 + 2 e_s + 2^-20 (1 + D) + 2 n 2^-24) (1 + 2^-7).
+  * lse: e_s + 2^-21 (1 + D) + n 2^-24 + 2^-22 |ref|.
+"""
+import numpy as np
+import pytest
+import torch
+
+import draft_sampling_lossless_amd as dsl
+import synth
+from oracle import attention as oa
+from oracle import context_kv as ck
+
+from gpu_util import dev, host, say
+
+pytestmark = pytest.mark.gpu
+
+NAN = 0x7FC0
+INF = 0x7F80
+SENT = 0x7E7E
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu(dspark_lib):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield
+    torch.cuda.synchronize()
+
+
+def bits(g, *shape, std=1.0):
+    return synth.bf16_bits(g.normal(0, std, shape).astype(np.float32))
+
+
+def value(t):
+    return ck.bf16_decode(host(t).view(np.uint16))
+
+
+def check_rows(out, lse, ref, hd, label=""):
+    """GPU out [T, nh, hd] (bits) and lse against the oracle's rows, row for row."""
+    w = ref["written"]
+    got = value(out)[w]
+    want, mag, dot = ref["out"][w], ref["mag"][w], ref["dot"][w]
+    n = ref["keys"][w][:, None]
+    es = (hd + 4) * 2.0 ** -24 * dot
+    rel = 2.0 ** -8 + 2 * es + 2.0 ** -20 * (1 + dot) + 2 * n * 2.0 ** -24
+    tol = 2.0 ** -8 * np.abs(want) + mag * rel[..., None] * (1 + 2.0 ** -7)
+    err = np.abs(got - want)
+    bad = ~(err <= tol)
+    assert not bad.any(), (f"{label}: {int(bad.sum())} of {bad.size} outside the bound, first at "
+                           f"{tuple(np.argwhere(bad)[0])}: {got[bad][0]} vs {want[bad][0]} (bound {tol[bad][0]:.3g})")
+    if lse is not None:
+        a, b = host(lse).astype(np.float64)[w], ref["lse"][w]
+        none = np.isneginf(b)
+        assert np.array_equal(none, np.isneginf(a)), f"{label}: rows without keys"
+        ltol = es + 2.0 ** -21 * (1 + dot) + n * 2.0 ** -24 + 2.0 ** -22 * np.where(none, 0, np.abs(b))
+        assert np.all(np.abs(a[~none] - b[~none]) <= ltol[~none]), f"{label}: lse"
+    return float((err / np.maximum(tol, 1e-300)).max()) if err.size else 0.0
+
+
+# ---------------------------------------------------------------- append
+
+@pytest.mark.parametrize("M,nh,nkv,hd,norm,fused,kout", [
+    (1, 1, 1, 128, True, False, False),
+    (9, 32, 8, 128, True, True, True),
+    (37, 20, 4, 128, False, True, False),
+    (5, 16, 2, 64, True, False, True),
+    (3, 8, 2, 256, True, True, True),
+    (4, 3, 3, 32, False, False, False),
+    (301, 0, 8, 128, True, True, False),      # keys and values only
+    (2, 40, 40, 256, True, True, True),       # more heads than one pass of a workgroup
+])
+def test_append(M, nh, nkv, hd, norm, fused, kout):
+    say(f"append M={M} nh={nh} nkv={nkv} hd={hd} norm={norm} fused={fused} k_out={kout}")
+    g = np.random.default_rng(M + hd)
+    S, eps, theta = M + 5, 1e-6, 1e6
+    q, k, v = bits(g, M, max(nh, 1), hd), bits(g, M, nkv, hd), bits(g, M, nkv, hd)
+    qw = synth.bf16_bits((1 + 0.1 * g.normal(size=hd)).astype(np.float32)) if norm else None
+    kw = synth.bf16_bits((1 + 0.1 * g.normal(size=hd)).astype(np.float32)) if norm else None
+    pos = g.integers(0, 1 << 20, M).astype(np.int32)
+    pos[0] = 0 if M > 1 else 2 ** 31 - 1
+    slots = g.permutation(S)[:M].astype(np.int64)
+    kc = torch.full((S, nkv, hd), SENT, dtype=torch.int16, device="cuda")
+    vc = torch.full((S, nkv, hd), SENT, dtype=torch.int16, device="cuda")
+    if fused:
+        wide = dev(np.concatenate([x.reshape(M, -1) for x in (q, k, v)], 1))
+        a, b = q.shape[1] * hd, nkv * hd
+        dq, dk, dv = (wide[:, lo:hi].unflatten(1, (-1, hd)) for lo, hi in ((0, a), (a, a + b), (a + b, a + 2 * b)))
+    else:
+        dq, dk, dv = dev(q), dev(k), dev(v)
+    ko = torch.full((M, nkv, hd), SENT, dtype=torch.int16, device="cuda") if kout else None
+    qo = dsl.kv_append(dk, dv, dev(pos), dev(slots), kc, vc, q=dq if nh else None,
+                       qnorm_w=dev(qw) if norm and nh else None, knorm_w=dev(kw) if norm else None, k_out=ko,
+                       eps=eps, rope_theta=theta)
+
+    def check(t, x, w, label):
+        ref = oa.append(x, w, pos, eps, theta)
+        pair = np.hypot(ref[..., :hd // 2], ref[..., hd // 2:])
+        tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -18 * np.concatenate([pair, pair], -1)
+        assert np.all(np.abs(value(t) - ref) <= tol), label
+
+    if nh:
+        check(qo, q, qw, "q")
+    else:
+        assert qo is None
+    check(kc[dev(slots)], k, kw, "k")
+    assert np.array_equal(host(vc).view(np.uint16)[slots], v)
+    rest = np.setdiff1d(np.arange(S), slots)
+    assert np.all(host(kc)[rest] == SENT) and np.all(host(vc)[rest] == SENT)
+    if kout:
+        assert torch.equal(ko, kc[dev(slots)])
+
+
+def test_append_in_place_and_skipped_slots():
+    g = np.random.default_rng(1)
+    M, nh, nkv, hd, S = 12, 8, 2, 128, 40
+    q, k, v = bits(g, M, nh, hd), bits(g, M, nkv, hd), bits(g, M, nkv, hd)
+    pos = dev(np.arange(100, 100 + M, dtype=np.int32))
+    slots = np.arange(M, dtype=np.int64) * 3
+    slots[[0, 4, 11]] = [-1, S, 1 << 40]
+    out = []
+    for place in (False, True):
+        kc = torch.full((S, nkv, hd), SENT, dtype=torch.int16, device="cuda")
+        vc = torch.full((S, nkv, hd), SENT, dtype=torch.int16, device="cuda")
+        wide = dev(np.concatenate([x.reshape(M, -1) for x in (q, k, v)], 1))
+        dq, dk, dv = (wide[:, lo:hi].unflatten(1, (-1, hd))
+                      for lo, hi in ((0, nh * hd), (nh * hd, (nh + nkv) * hd), ((nh + nkv) * hd, (nh + 2 * nkv) * hd)))
+        qo = dq if place else torch.empty((M, nh, hd), dtype=torch.int16, device="cuda")
+        ko = dk if place else torch.empty((M, nkv, hd), dtype=torch.int16, device="cuda")
+        dsl.kv_append(dk, dv, pos, dev(slots), kc, vc, q=dq, q_out=qo, k_out=ko)
+        assert np.array_equal(host(dv).view(np.uint16), v)
+        out.append([host(x).copy() for x in (qo, ko, kc, vc)])
+    for a, b in zip(*out):
+        assert np.array_equal(a, b)
+    good = np.array([m for m in range(M) if 0 <= slots[m] < S])
+    assert np.all(out[0][2][np.setdiff1d(np.arange(S), slots[good])] == SENT)
+    assert np.array_equal(out[0][2][slots[good]], out[0][1][good])
+    assert not np.any(np.all(out[0][0] == q.view(np.int16), axis=(1, 2)))     # skipped tokens' q is rotated too
+
+
+# ---------------------------------------------------------------- paged attention
+
+def paged_case(g, nh, nkv, hd, page, qlen, kvlen, extra_pages=3, std=2.0, poison=True):
+    """Caches whose unused slots hold NaN, tables whose unused entries are -1."""
+    need = [-(-n // page) for n in kvlen]
+    total = sum(need) + extra_pages
+    order = g.permutation(total)
+    table = np.full((len(kvlen), max(max(need), 1)), -1, np.int32)
+    kc = np.full((total * page, nkv, hd), NAN if poison else 0, np.uint16)
+    vc = np.full((total * page, nkv, hd), NAN if poison else 0, np.uint16)
+    at = 0
+    for b, n in enumerate(kvlen):
+        table[b, :need[b]] = order[at:at + need[b]]
+        at += need[b]
+        slot = table[b, np.arange(n) // page].astype(np.int64) * page + np.arange(n) % page
+        kc[slot], vc[slot] = bits(g, n, nkv, hd), bits(g, n, nkv, hd)
+    cu = np.concatenate([[0], np.cumsum(qlen)]).astype(np.int32)
+    return dict(q=bits(g, int(cu[-1]), nh, hd, std=std), kc=kc, vc=vc, table=table, kv=np.array(kvlen, np.int32), cu=cu,
+                page=page, hd=hd, max_q=max(max(qlen), 1))
+
+
+def run_paged(c, causal, scale=None, lse=True, max_q=None, **kw):
+    T, nh, hd = c["q"].shape
+    out = torch.full((T, nh, hd), SENT, dtype=torch.int16, device="cuda")
+    ls = torch.full((T, nh), 7.0, dtype=torch.float32, device="cuda") if lse else None
+    dsl.paged_attention(dev(c["q"]), dev(c["kc"]), dev(c["vc"]), dev(c["table"]), dev(c["kv"]), dev(c["cu"]),
+                        max_q or c["max_q"], c["page"], causal=causal, scale=scale, out=out, lse=ls, **kw)
+    return out, ls
+
+
+def ref_paged(c, causal, scale=None):
+    return oa.paged(c["q"], c["kc"], c["vc"], c["table"], c["kv"], c["cu"], c["page"], causal,
+                    c["hd"] ** -0.5 if scale is None else scale)
+
+
+@pytest.mark.parametrize("nh,nkv,hd,page,qlen,kvlen,causal", [
+    (4, 1, 128, 16, [1], [1], True),
+    (32, 8, 128, 16, [1], [517], True),
+    (8, 2, 128, 64, [1], [5003], True),                       # split over ranges and joined
+    (8, 2, 128, 1, [3], [3001], True),                        # slots one by one, split
+    (4, 2, 64, 16, [1, 1, 1], [33, 1, 64], True),
+    (4, 2, 256, 32, [2, 1], [95, 700], True),
+    (8, 1, 256, 8, [5, 3], [40, 9], False),
+    (10, 2, 128, 4, [1, 2, 3], [31, 32, 33], True),           # groups of 5
+    (16, 1, 128, 16, [17, 1, 9], [300, 5, 9], True),          # 272 rows: several row blocks
+    (8, 8, 128, 256, [4, 16], [255, 257], False),             # no shared heads
+    (32, 8, 128, 64, [17, 3, 1, 9], [1000, 700, 17, 64], True),
+    (6, 2, 64, 2, [7, 8], [7, 100], True),                    # query tokens are the whole sequence
+    (8, 2, 64, 16, [128, 1], [200, 3], True),                 # the largest block
+    (24, 8, 64, 32, [5, 0, 2], [50, 60, 1100], True),         # a request without query tokens
+    (8, 2, 128, 16, [2, 1, 3], [0, 0, 2], True),              # nothing cached; fewer keys than query tokens
+    (8, 2, 128, 16, [2, 1], [0, 40], False),
+])
+def test_paged(nh, nkv, hd, page, qlen, kvlen, causal):
+    say(f"paged nh={nh} nkv={nkv} hd={hd} page={page} q={qlen} kv={kvlen} causal={causal}")
+    c = paged_case(np.random.default_rng(nh + hd + page), nh, nkv, hd, page, qlen, kvlen)
+    out, lse = run_paged(c, causal)
+    r = check_rows(out, lse, ref_paged(c, causal), hd, "paged")
+    say(f"  worst error at {r:.2f} of its bound")
+    again, _ = run_paged(c, causal)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("B", [64, 65, 130, 1000])
+def test_paged_many_requests(B):
+    g = np.random.default_rng(B)
+    qlen, kvlen = g.integers(0, 4, B).tolist(), g.integers(0, 60, B).tolist()
+    kvlen[B // 2], kvlen[B - 1] = 2100, 1500              # two that are split among many that are not
+    qlen[B // 2] = qlen[B - 1] = 2
+    say(f"paged B={B}, {sum(qlen)} tokens")
+    c = paged_case(g, 4, 2, 64, 16, qlen, kvlen)
+    out, lse = run_paged(c, True)
+    check_rows(out, lse, ref_paged(c, True), 64, "paged")
+
+
+def test_paged_unseen_keys_do_not_matter():
+    """NaN and infinities in keys and values that a row does not see: later tokens of the
+    block (causal), hidden pages, the rest of a page."""
+    g = np.random.default_rng(8)
+    for page, kv in ((16, 45), (1, 45), (64, 700)):
+        c = paged_case(g, 8, 2, 128, page, [6], [kv])
+        clean, _ = run_paged(c, True)
+        slot = lambda s: int(c["table"][0, s // page]) * page + s % page  # noqa: E731
+        for s, kb, vb in ((kv - 1, NAN, NAN), (kv - 2, 0xFF80, INF), (kv - 3, INF, NAN)):
+            c["kc"][slot(s)], c["vc"][slot(s)] = kb, vb
+        out, _ = run_paged(c, True)
+        assert torch.equal(out[:3], clean[:3]), f"page {page}"
+        assert np.isnan(value(out)[5]).all()              # and the rows that see them are not spared
+
+
+def test_paged_values_that_are_not_finite_reach_the_rows_that_see_them():
+    g = np.random.default_rng(9)
+    c = paged_case(g, 4, 1, 128, 16, [4], [40])
+    slot = int(c["table"][0, 37 // 16]) * 16 + 37 % 16
+    c["vc"][slot, 0, 5] = INF                             # seen by tokens 1, 2, 3 (keys <= 37, 38, 39), not by 0
+    got = value(run_paged(c, True)[0])
+    assert np.isposinf(got[1:, :, 5]).all() and np.isfinite(got[0]).all()
+    assert np.isfinite(np.delete(got, 5, axis=2)).all()
+
+
+def test_paged_pages_outside_the_cache_hide_their_keys():
+    g = np.random.default_rng(10)
+    for page in (1, 16, 64):
+        c = paged_case(g, 8, 2, 128, page, [2, 1], [200, 90])
+        pages = c["kc"].shape[0] // page
+        c["table"][0, 0], c["table"][1, 1], c["table"][0, 2] = -1, pages, 2 ** 31 - 1
+        out, lse = run_paged(c, True)
+        check_rows(out, lse, ref_paged(c, True), 128, f"page {page}")
+    c["table"][:] = -7                                    # every page
+    out, lse = run_paged(c, True)
+    assert not value(out).any() and np.isneginf(host(lse)).all()
+
+
+def test_paged_lengths_beyond_the_table_and_rows_behind():
+    g = np.random.default_rng(11)
+    c = paged_case(g, 8, 2, 128, 16, [2, 3], [64, 40])
+    c["q"] = np.concatenate([c["q"], bits(g, 4, 8, 128)])        # four rows behind the last request
+    c["kv"][0] = 1000                                            # the table holds 64 keys a request
+    ref = ref_paged(c, False)
+    out, lse = run_paged(c, False)
+    check_rows(out, lse, ref, 128)
+    assert np.all(host(out)[5:] == SENT) and np.all(host(lse)[5:] == 7.0)
+    c["kv"][:] = -3
+    out, _ = run_paged(c, False)
+    assert not host(out)[:5].any()
+    # tokens beyond max_q are left as they were
+    c = paged_case(g, 8, 2, 128, 16, [5], [64])
+    ref = ref_paged(c, True)
+    out, _ = run_paged(c, True, max_q=2)
+    assert np.all(host(out)[2:] == SENT)
+    ref["written"][2:] = False
+    check_rows(out, None, ref, 128)
+
+
+def test_paged_large_scores_and_scale():
+    g = np.random.default_rng(12)
+    c = paged_case(g, 8, 2, 128, 16, [3], [600], std=60.0)       # scores of hundreds: one weight is all
+    out, lse = run_paged(c, True)
+    check_rows(out, lse, ref_paged(c, True), 128)
+    out, lse = run_paged(c, True, scale=0.003)
+    check_rows(out, lse, ref_paged(c, True, 0.003), 128)
+
+
+def test_paged_offsets_beyond_32_bits():
+    """A cache of 5 GiB a side, its last pages in use: slot offsets pass 2^32 bytes."""
+    g = np.random.default_rng(13)
+    nh, nkv, hd, page = 8, 8, 128, 16
+    pages = 5 * 2 ** 30 // (page * nkv * hd * 2)
+    small = paged_case(g, nh, nkv, hd, page, [2, 1], [100, 650], extra_pages=0)
+    kc = torch.empty((pages * page, nkv, hd), dtype=torch.int16, device="cuda")
+    vc = torch.empty((pages * page, nkv, hd), dtype=torch.int16, device="cuda")
+    n = small["kc"].shape[0]
+    kc[-n:], vc[-n:] = dev(small["kc"]), dev(small["vc"])
+    for p in (16, 1):
+        table = np.where(small["table"] >= 0, small["table"] + pages - n // page, -1).astype(np.int32)
+        if p == 1:
+            table = np.where(np.repeat(table, 16, 1) >= 0, np.repeat(table, 16, 1) * 16 + np.tile(np.arange(16), table.shape[1]),
+                             -1).astype(np.int32)
+        out = dsl.paged_attention(dev(small["q"]), kc, vc, dev(table), dev(small["kv"]), dev(small["cu"]), 2, p)
+        check_rows(out, None, ref_paged(small, True), hd, f"page {p}")
+    # the append reaches the last slot too
+    k, v = bits(g, 1, nkv, hd), bits(g, 1, nkv, hd)
+    dsl.kv_append(dev(k), dev(v), dev(np.zeros(1, np.int32)), dev(np.array([pages * page - 1])), kc, vc)
+    assert np.array_equal(host(kc[-1]).view(np.uint16), k[0]) and np.array_equal(host(vc[-1]).view(np.uint16), v[0])
+
+
+def test_paged_parts_join_by_their_lse():
+    g = np.random.default_rng(14)
+    c = paged_case(g, 8, 2, 128, 16, [4], [320])
+    whole, _ = run_paged(c, False)
+    parts = []
+    for lo, hi in ((0, 8), (8, 20)):
+        d = dict(c, table=np.ascontiguousarray(c["table"][:, lo:hi]), kv=np.array([(hi - lo) * 16], np.int32))
+        out, lse = run_paged(d, False)
+        parts.append((value(out), host(lse).astype(np.float64)))
+    both = np.logaddexp(parts[0][1], parts[1][1])
+    joined = sum(o * np.exp(l - both)[..., None] for o, l in parts)
+    ref = ref_paged(c, False)
+    # each part is within the bound of its own rows; the weighted sum is within theirs together
+    tol = 2.0 ** -7 * 2 * ref["mag"] + 1e-4
+    assert np.all(np.abs(joined - value(whole)) <= tol)
+
+
+def test_paged_strided_queries_streams_and_graph():
+    g = np.random.default_rng(15)
+    c = paged_case(g, 8, 2, 128, 16, [2, 1, 3], [700, 64, 1300])
+    want, _ = run_paged(c, True)
+    T = c["q"].shape[0]
+    wide = torch.zeros((T, 8 * 128 + 512), dtype=torch.int16, device="cuda")
+    wide[:, :1024] = dev(c["q"]).view(T, -1)
+    q = wide[:, :1024].unflatten(1, (8, 128))
+    kc, vc, tb, kv, cu = dev(c["kc"]), dev(c["vc"]), dev(c["table"]), dev(c["kv"]), dev(c["cu"])
+    ws = torch.empty(dsl.paged_attention_workspace_size(T, 3, 3, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    out = torch.empty((T, 8, 128), dtype=torch.int16, device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        dsl.paged_attention(q, kc, vc, tb, kv, cu, 3, 16, out=out, workspace=ws)
+    s.synchronize()
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dsl.paged_attention(q, kc, vc, tb, kv, cu, 3, 16, out=out, workspace=ws)
+    for kvs in ([700, 64, 1300], [10, 70, 1200], [640, 1, 3]):           # lengths change between replays
+        kv.copy_(dev(np.array(kvs, np.int32)))
+        out.fill_(SENT)
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        d = dict(c, kv=np.array(kvs, np.int32))
+        assert torch.equal(out, run_paged(d, True)[0])
+
+
+# ---------------------------------------------------------------- prompt attention
+
+def run_prompt(q, k, v, cu, causal, scale=None):
+    T, nh, hd = q.shape
+    out = torch.full((T, nh, hd), SENT, dtype=torch.int16, device="cuda")
+    lse = torch.full((T, nh), 7.0, dtype=torch.float32, device="cuda")
+    dsl.prompt_attention(dev(q), dev(k), dev(v), dev(np.array(cu, np.int32)), causal=causal, scale=scale, out=out, lse=lse)
+    return out, lse
+
+
+@pytest.mark.parametrize("nh,nkv,hd,lens", [
+    (4, 1, 128, [1]),
+    (8, 2, 128, [63, 64, 65]),
+    (8, 8, 128, [130, 1, 200]),
+    (32, 8, 128, [17, 90]),
+    (10, 2, 128, [5, 0, 77, 2]),            # groups of 5, an empty sequence
+    (16, 1, 128, [33, 40]),
+    (4, 2, 64, [300]),
+    (6, 2, 64, [1, 2, 3, 129]),
+    (4, 2, 256, [150, 31]),
+    (2, 2, 256, [65]),
+    (4, 2, 128, [700]),                     # several key tiles and row tiles
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt(nh, nkv, hd, lens, causal):
+    say(f"prompt nh={nh} nkv={nkv} hd={hd} lens={lens} causal={causal}")
+    g = np.random.default_rng(nh + hd + len(lens))
+    T = sum(lens)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    q, k, v = bits(g, T + 3, nh, hd, std=2.0), bits(g, T + 3, nkv, hd), bits(g, T + 3, nkv, hd)
+    k[T:], v[T:] = NAN, NAN                 # tokens behind the last sequence
+    out, lse = run_prompt(q, k, v, cu, causal)
+    ref = oa.prompt(q, k, v, cu, causal, hd ** -0.5)
+    r = check_rows(out, lse, ref, hd, "prompt")
+    say(f"  worst error at {r:.2f} of its bound")
+    assert np.all(host(out)[T:] == SENT) and np.all(host(lse)[T:] == 7.0)
+    assert torch.equal(out, run_prompt(q, k, v, cu, causal)[0])
+
+
+@pytest.mark.parametrize("B", [64, 65, 200])
+def test_prompt_many_sequences(B):
+    g = np.random.default_rng(B)
+    lens = g.integers(0, 12, B)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    T = int(cu[-1])
+    q, k, v = bits(g, T, 8, 64, std=2.0), bits(g, T, 2, 64), bits(g, T, 2, 64)
+    out, lse = run_prompt(q, k, v, cu, True)
+    check_rows(out, lse, oa.prompt(q, k, v, cu, True, 64 ** -0.5), 64, "prompt")
+
+
+def test_prompt_unseen_keys_do_not_matter():
+    g = np.random.default_rng(21)
+    for hd, lens in ((128, [100, 150]), (64, [70, 80]), (256, [90])):
+        T = sum(lens)
+        cu = np.concatenate([[0], np.cumsum(lens)])
+        q, k, v = bits(g, T, 8, hd, std=2.0), bits(g, T, 2, hd), bits(g, T, 2, hd)
+        clean, _ = run_prompt(q, k, v, cu, True)
+        at = lens[0] - 40                    # in the first sequence: tokens before it, and all others, are untouched
+        k[at], v[at] = NAN, NAN
+        k[at + 2], v[at + 2] = INF, 0xFF80
+        out, _ = run_prompt(q, k, v, cu, True)
+        assert torch.equal(out[:at], clean[:at]) and torch.equal(out[lens[0]:], clean[lens[0]:]), f"hd {hd}"
+        assert np.isnan(value(out)[at:lens[0]]).all()
+        full, _ = run_prompt(q, k, v, cu, False)
+        assert np.isnan(value(full)[:lens[0]]).all() and np.isfinite(value(full)[lens[0]:]).all()
+
+
+def test_prompt_strided_columns_and_graph():
+    g = np.random.default_rng(22)
+    T, nh, nkv, hd = 260, 8, 2, 128
+    q, k, v = bits(g, T, nh, hd, std=2.0), bits(g, T, nkv, hd), bits(g, T, nkv, hd)
+    cu = dev(np.array([0, 100, 260], np.int32))
+    want, _ = run_prompt(q, k, v, [0, 100, 260], True)
+    wide = dev(np.concatenate([x.reshape(T, -1) for x in (q, k, v)], 1))
+    a, b = nh * hd, nkv * hd
+    dq, dk, dv = (wide[:, lo:hi].unflatten(1, (-1, hd)) for lo, hi in ((0, a), (a, a + b), (a + b, a + 2 * b)))
+    out = torch.empty((T, nh, hd), dtype=torch.int16, device="cuda")
+    dsl.prompt_attention(dq, dk, dv, cu, out=out)
+    assert torch.equal(out, want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dsl.prompt_attention(dq, dk, dv, cu, out=out)
+    for mid in (100, 1, 260, 0):
+        cu[1] = mid
+        out.fill_(SENT)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, run_prompt(q, k, v, [0, mid, 260], True)[0])
+
+
+def test_prompt_long_rows_sampled():
+    """4100 tokens: many key tiles; a sample of rows against the oracle."""
+    g = np.random.default_rng(23)
+    T, nh, nkv, hd = 4100, 4, 1, 128
+    q, k, v = bits(g, T, nh, hd, std=2.0), bits(g, T, nkv, hd), bits(g, T, nkv, hd)
+    out, lse = run_prompt(q, k, v, [0, T], True)
+    rows = np.unique(np.concatenate([g.integers(0, T, 40), [0, 63, 64, 4095, 4096, T - 1]]))
+    for t in rows:
+        ref = oa.paged(q[t:t + 1], k[:t + 1], v[:t + 1], np.arange(t + 1)[None], [t + 1], [0, 1], 1, True, hd ** -0.5)
+        check_rows(out[t:t + 1], lse[t:t + 1], ref, hd, f"token {t}")
+
+
+# ---------------------------------------------------------------- as they are used together
+
+def test_prompt_then_rounds_over_one_cache():
+    """A prompt through append and prompt attention, then two verify blocks through append
+    and paged attention on the cache so filled: every block's rows equal the rows prompt
+    attention gives for the whole text, up to the bound."""
+    g = np.random.default_rng(31)
+    nh, nkv, hd, page = 8, 2, 128, 16
+    first, total = [50, 7, 81], [61, 24, 98]
+    pages = 24
+    order = g.permutation(pages)
+    table, at = np.full((3, 8), -1, np.int32), 0
+    for b, n in enumerate(total):
+        table[b, :-(-n // page)] = order[at:at + -(-n // page)]
+        at += -(-n // page)
+    text = [tuple(bits(g, n, h, hd) for h in (nh, nkv, nkv)) for n in total]
+    qw, kw = (synth.bf16_bits((1 + 0.1 * g.normal(size=hd)).astype(np.float32)) for _ in range(2))
+    kc = torch.full((pages * page, nkv, hd), SENT, dtype=torch.int16, device="cuda")
+    vc = torch.full((pages * page, nkv, hd), SENT, dtype=torch.int16, device="cuda")
+
+    def append(lo, hi):
+        parts = [np.concatenate([t[x][a:z] for t, a, z in zip(text, lo, hi)]) for x in range(3)]
+        pos = np.concatenate([np.arange(a, z) for a, z in zip(lo, hi)]).astype(np.int32)
+        slots = np.concatenate([table[b, np.arange(a, z) // page].astype(np.int64) * page + np.arange(a, z) % page
+                                for b, (a, z) in enumerate(zip(lo, hi))])
+        ko = torch.empty(parts[1].shape, dtype=torch.int16, device="cuda")
+        q = dsl.kv_append(dev(parts[1]), dev(parts[2]), dev(pos), dev(slots), kc, vc, q=dev(parts[0]), qnorm_w=dev(qw),
+                          knorm_w=dev(kw), k_out=ko)
+        return q, ko, dev(parts[2]), dev(np.concatenate([[0], np.cumsum([z - a for a, z in zip(lo, hi)])]).astype(np.int32))
+
+    q, k, v, cu = append([0, 0, 0], first)
+    prompt = dsl.prompt_attention(q, k, v, cu)
+    got = [[prompt[cu[b]:cu[b + 1]]] for b in range(3)]
+    for lo, hi in ((first, [55, 16, 82]), ([55, 16, 82], total)):
+        q, _, _, cu = append(lo, hi)
+        out = dsl.paged_attention(q, kc, vc, dev(table), dev(np.array(hi, np.int32)), cu, 16, page)
+        for b in range(3):
+            got[b].append(out[cu[b]:cu[b + 1]])
+    kc2, vc2 = kc, vc
+    kc, vc = torch.empty_like(kc), torch.empty_like(vc)
+    q, k, v, cu = append([0, 0, 0], total)
+    assert torch.equal(dsl.prompt_attention(q, k, v, cu)[:first[0]], torch.cat(got[0])[:first[0]])
+    ref = oa.prompt(host(q).view(np.uint16), host(k).view(np.uint16), host(v).view(np.uint16), host(cu), True, hd ** -0.5)
+    check_rows(torch.cat([torch.cat(x) for x in got]), None, ref, hd, "rounds")
+    used = np.concatenate([table[b, np.arange(n) // page] * page + np.arange(n) % page for b, n in enumerate(total)])
+    assert torch.equal(kc2[dev(used.astype(np.int64))], kc[dev(used.astype(np.int64))])
+    assert torch.equal(vc2[dev(used.astype(np.int64))], vc[dev(used.astype(np.int64))])
+
+
+def test_draft_block_over_a_context_kv_cache():
+    """context_kv fills two layers' caches; a draft block is appended behind the context
+    of each layer and attends to all of it (not causal)."""
+    g = np.random.default_rng(32)
+    M, L, nkv, hd, nh, N = 90, 2, 2, 128, 8, 7
+    H, S = 256, 128
+    kc = torch.zeros((L, S, nkv, hd), dtype=torch.int16, device="cuda")
+    vc = torch.zeros((L, S, nkv, hd), dtype=torch.int16, device="cuda")
+    slot = g.permutation(S).astype(np.int64)
+    w = lambda *s: dev(bits(g, *s, std=0.06))  # noqa: E731
+    ones = dev(synth.bf16_bits(np.ones(H, np.float32)))
+    knorm = dev(synth.bf16_bits(np.ones((L, hd), np.float32)))
+    dsl.context_kv(w(M, H), w(H, H), None, ones, w(L * 2 * nkv * hd, H), w(L * 2 * nkv * hd), knorm,
+                   dev(np.arange(M, dtype=np.int32)), dev(slot[:M]), kc, vc)
+    table = dev(slot[None, :M + N].astype(np.int32))
+    for layer in range(L):
+        q, k, v = bits(g, N, nh, hd), bits(g, N, nkv, hd), bits(g, N, nkv, hd)
+        qr = dsl.kv_append(dev(k), dev(v), dev(np.arange(M, M + N, dtype=np.int32)), dev(slot[M:M + N]), kc[layer],
+                           vc[layer], q=dev(q), knorm_w=knorm[layer])
+        out = dsl.paged_attention(qr, kc[layer], vc[layer], table, dev(np.array([M + N], np.int32)),
+                                  dev(np.array([0, N], np.int32)), N, 1, causal=False)
+        ref = oa.paged(host(qr).view(np.uint16), host(kc[layer]).view(np.uint16), host(vc[layer]).view(np.uint16),
+                       host(table), [M + N], [0, N], 1, False, hd ** -0.5)
+        check_rows(out, None, ref, hd, f"layer {layer}")
