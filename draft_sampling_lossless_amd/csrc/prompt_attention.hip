@@ -72,185 +72,364 @@ __device__ bool find_tile(const Work& w, int u, int rows, int& start, int& n, in
   return false;
 }
 
-template <int HD, int NW, bool kCausal>
-__global__ __launch_bounds__(64 * NW) void prompt_rows(Work w) {
+// RW blocks of 32 rows a wave.  One pass of the loop holds the weights of tile t and the
+// scores of tile t + 1 at once, so that the first product of the next tile (matrix pipe)
+// runs beside the exponentials of this one (vector pipe).  K is read one tile ahead of V;
+// three LDS buffers of K and two of V are filled straight from memory while the others are
+// in use, with one barrier a tile.  The running maximum is raised only when a row's scores exceed it
+// by kRaise (weights up to 2^kRaise, which neither float nor bf16 minds): the accumulators
+// are rescaled on a row's first tile and hardly ever after.
+constexpr float kRaise = 8.0f;
+
+template <int HD, int RW, int NW, bool kCausal>
+__global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
   constexpr int PIECES = HD / 8;            // 16-byte pieces of a row
   constexpr int ROWB = HD * 2;
+  constexpr int TILEB = KT * ROWB;
+  constexpr int WGROWS = 32 * RW * NW;
+  constexpr int LOADS = KT * PIECES / (64 * NW);   // 1 KB loads of a wave for one tile of K (or V)
   const PromptArgs& a = w.a;
-  __shared__ __attribute__((aligned(16))) char kbuf[KT * ROWB];
-  __shared__ __attribute__((aligned(16))) char vbuf[KT * ROWB];
+  extern __shared__ __attribute__((aligned(16))) char smem[];   // three K tiles, two V tiles
 
   const int kvh = blockIdx.x % a.nkv;
   int start, n, tile;
-  if (!find_tile(w, blockIdx.x / a.nkv, 32 * NW, start, n, tile)) return;
+  if (!find_tile(w, blockIdx.x / a.nkv, WGROWS, start, n, tile)) return;
   const int lane = threadIdx.x & 63, col = lane & 31, hh = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r0 = tile * 32 * NW;            // first row of the workgroup
-  const int row = r0 + 32 * wave + col;
-  const int j = row / w.G, h = kvh * w.G + row % w.G;
-  const bool ok = j < n;
-  const int lim = kCausal && ok ? j + 1 : n;                     // keys below lim are seen
-  const int wlow = kCausal ? min(n, (r0 + 32 * wave) / w.G + 1) : n;       // the wave's smallest limit
-  const int whigh = kCausal ? min(n, (r0 + 32 * wave + 31) / w.G + 1) : n; // and its largest
-  const int ghigh = kCausal ? min(n, (r0 + 32 * NW - 1) / w.G + 1) : n;
-  const bool idle = (r0 + 32 * wave) / w.G >= n;                 // no row of this wave exists
+  const int wave = uniform(threadIdx.x >> 6);
+  const int r0 = tile * WGROWS, w0 = r0 + 32 * RW * wave;        // first row of the workgroup, of the wave
+  const int ghigh = kCausal ? min(n, (r0 + WGROWS - 1) / w.G + 1) : n;
+  const int nt = (ghigh + KT - 1) / KT;
+  // tiles every row of the wave sees whole, and tiles some row sees at all
+  const int wlow = kCausal ? min(n, w0 / w.G + 1) : n;
+  const int whigh = w0 / w.G >= n ? 0 : kCausal ? min(n, (w0 + 32 * RW - 1) / w.G + 1) : n;
+  const int nsome = (whigh + KT - 1) / KT, nfull = min(wlow / KT, nsome);
 
-  bf16x8 qf[HD / 16];
-  {
-    const uint16_t* src = a.q + (size_t)(start + (ok ? j : 0)) * a.q_stride + (size_t)(ok ? h : 0) * HD;
+  int row_j[RW], row_h[RW], lim[RW];
+  bool ok[RW];
+  bf16x8 qf[RW][HD / 16];
+#pragma unroll
+  for (int b = 0; b < RW; ++b) {
+    const int row = w0 + 32 * b + col;
+    row_j[b] = row / w.G;
+    row_h[b] = kvh * w.G + row % w.G;
+    ok[b] = row_j[b] < n;
+    lim[b] = kCausal && ok[b] ? row_j[b] + 1 : n;                // keys below lim are seen
+    const uint16_t* src = a.q + (size_t)(start + (ok[b] ? row_j[b] : 0)) * a.q_stride + (size_t)(ok[b] ? row_h[b] : 0) * HD;
 #pragma unroll
     for (int kk = 0; kk < HD / 16; ++kk) {
       const uint4 v = *reinterpret_cast<const uint4*>(src + 16 * kk + 8 * hh);
-      qf[kk] = __builtin_bit_cast(bf16x8, ok ? v : make_uint4(0, 0, 0, 0));
+      qf[b][kk] = __builtin_bit_cast(bf16x8, ok[b] ? v : make_uint4(0, 0, 0, 0));
     }
   }
-  floatx16 o[HD / 32];
-#pragma unroll
-  for (int d = 0; d < HD / 32; ++d) o[d] = floatx16{};
-  float m = -INFINITY, l = 0.0f;
 
-  for (int key0 = 0; key0 < ghigh; key0 += KT) {
-    __syncthreads();
-    // stage: LDS slot q of the tile (row q / PIECES) takes the piece swizzled into it;
-    // a key behind the sequence reads its last row
+  // LDS slot q of a tile (row q / PIECES) takes the piece swizzled into it.  The tile's
+  // base is a scalar, a lane's offset into it 32 bits (token strides stay below 2^24); a
+  // key behind the sequence reads its last row
+  uint32_t koffs[LOADS], voffs[LOADS];
 #pragma unroll
-    for (int q = 0; q < KT * PIECES / (64 * NW); ++q) {
-      const int blk = q * NW + wave, slot = blk * 64 + lane;
-      const int r = slot / PIECES, piece = (slot % PIECES) ^ (swizzle<HD>(r));
-      const size_t t = start + min(key0 + r, n - 1);
-      load_to_lds16(a.k + t * a.k_stride + (size_t)kvh * HD + piece * 8, kbuf + blk * 1024);
-      load_to_lds16(a.v + t * a.v_stride + (size_t)kvh * HD + piece * 8, vbuf + blk * 1024);
+  for (int q = 0; q < LOADS; ++q) {
+    const int slot = (q * NW + wave) * 64 + lane, r = slot / PIECES, piece = (slot % PIECES) ^ swizzle<HD>(r);
+    koffs[q] = (uint32_t)r * (uint32_t)(a.k_stride * 2) + piece * 16;
+    voffs[q] = (uint32_t)r * (uint32_t)(a.v_stride * 2) + piece * 16;
+  }
+  auto fetch = [&](const uint16_t* base, int64_t stride, const uint32_t (&offs)[LOADS], int t, char* lds) {
+    const char* tb = reinterpret_cast<const char*>(base + (size_t)t * KT * stride);
+    if (uniform((t + 1) * KT <= n)) {
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q)
+        load_to_lds16(reinterpret_cast<const uint16_t*>(tb + offs[q]), lds + (q * NW + wave) * 1024);
+    } else {
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q) {
+        const int r = ((q * NW + wave) * 64 + lane) / PIECES, over = max(r - (n - 1 - t * KT), 0);
+        load_to_lds16(reinterpret_cast<const uint16_t*>(tb + (offs[q] - (uint32_t)over * (uint32_t)(stride * 2))),
+                      lds + (q * NW + wave) * 1024);
+      }
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (uniform(idle || key0 >= whigh)) continue;
+  };
+  const uint16_t* kbase = a.k + (size_t)start * a.k_stride + (size_t)kvh * HD;
+  const uint16_t* vbase = a.v + (size_t)start * a.v_stride + (size_t)kvh * HD;
 
-    floatx16 sc[2];
+  floatx16 o[RW][HD / 32];
+  float m[RW], mb[RW], l[RW];               // mb: m, or 0 while a row has seen nothing
+#pragma unroll
+  for (int b = 0; b < RW; ++b) {
+    m[b] = -INFINITY;
+    mb[b] = l[b] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < HD / 32; ++d) o[b][d] = floatx16{};
+  }
+
+  // K operand kk of 32 rows: this lane's row, piece 2 kk + hh; the swizzle repeats every 16
+  // rows, so the second 32 rows are a constant further, and kk only flips bits
+  int koff = col * ROWB + ((hh ^ swizzle<HD>(col)) << 4);
+  auto key_frag = [&](const char* kb, int s, int kk) {
+    return *reinterpret_cast<const bf16x8*>(kb + ((koff ^ (kk << 5)) + 32 * s * ROWB));
+  };
+  auto scores = [&](floatx16 (&sc)[RW][2], const char* kb) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      sc[s] = floatx16{};
-      const int r = 32 * s + col;
+#pragma unroll
+      for (int b = 0; b < RW; ++b) sc[b][s] = floatx16{};
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk) {
-        const bf16x8 kf = *reinterpret_cast<const bf16x8*>(kbuf + r * ROWB + (((2 * kk + hh) ^ swizzle<HD>(r)) << 4));
-        sc[s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[kk], sc[s], 0, 0, 0);
+        const bf16x8 kf = key_frag(kb, s, kk);
+#pragma unroll
+        for (int b = 0; b < RW; ++b) sc[b][s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[b][kk], sc[b][s], 0, 0, 0);
       }
     }
-    const bool partial = uniform(key0 + KT > wlow) != 0;
-    float x[32];
+  };
+  auto row_max = [&](const floatx16 (&sc)[2]) {
+    float t0 = sc[0][0], t1 = sc[1][0];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) x[e] = sc[e >> 4][e & 15] * w.c;
-    if (partial) {
+    for (int e = 1; e < 16; ++e) {
+      t0 = fmaxf(t0, sc[0][e]);
+      t1 = fmaxf(t1, sc[1][e]);
+    }
+    uint32_t lo, hi;
+    halves_pair(__float_as_uint(fmaxf(t0, t1)), lo, hi);
+    return fmaxf(__uint_as_float(lo), __uint_as_float(hi)) * w.c;
+  };
+  auto mask = [&](floatx16 (&sc)[RW][2], int t) {
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const int i = 32 * (e >> 4) + 8 * ((e & 15) >> 2) + 4 * hh + (e & 3);
-        if (key0 + i >= lim) x[e] = -INFINITY;
+    for (int b = 0; b < RW; ++b)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (t * KT + 32 * s + 8 * (e >> 2) + 4 * hh + (e & 3) >= lim[b]) sc[b][s][e] = -INFINITY;
+  };
+  // raise the maxima that tile t's scores exceed by too much
+  auto raise = [&](const float (&tm)[RW]) {
+    bool up = false;
+#pragma unroll
+    for (int b = 0; b < RW; ++b) up |= tm[b] > m[b] + kRaise;
+    if (uniform(__any(up))) {
+#pragma unroll
+      for (int b = 0; b < RW; ++b) {
+        const float mn = tm[b] > m[b] + kRaise ? tm[b] : m[b];
+        const float al = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[b] - mn);
+        m[b] = mn;
+        mb[b] = mn == -INFINITY ? 0.0f : mn;
+        l[b] *= al;
+#pragma unroll
+        for (int d = 0; d < HD / 32; ++d) o[b][d] *= al;
       }
     }
-    float tm = x[0];
+  };
+  // weights of keys 16 u .. 16 u + 15 of the tile, rounded to bf16 (the second product's
+  // operand type), and their sum
+  auto weights = [&](const floatx16 (&sc)[2], int b, int u) {
+    float x[8];
 #pragma unroll
-    for (int e = 1; e < 32; ++e) tm = fmaxf(tm, x[e]);
-    {
-      uint32_t lo, hi;
-      halves_pair(__float_as_uint(tm), lo, hi);
-      tm = fmaxf(__uint_as_float(lo), __uint_as_float(hi));
-    }
-    const float mn = fmaxf(m, tm);
-    const float ms = mn == -INFINITY ? 0.0f : mn;     // a row that has seen nothing yet
-    const float al = __builtin_amdgcn_exp2f(m - ms);
-    m = mn;
-    float sum = 0.0f;
+    for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[u >> 1][8 * (u & 1) + e], w.c, -mb[b]));
+    l[b] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+    return __builtin_bit_cast(bf16x8, make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                 pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
+  };
+  union VFrag {
+    shortx4 s[2];
+    uint32_t w[4];
+    bf16x8 v;
+  };
+  // V operand (u, d): keys 16 u + 8 e + 4 hh .. + 3 (e = 0, 1), dim 32 d + col
+  int voff[2];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      x[e] = __builtin_amdgcn_exp2f(x[e] - ms);
-      sum += x[e];
-    }
-    l = l * al + sum;
-    // the weights' rounding to bf16, the second product's operand type
-    bf16x8 p[4];
+  for (int e = 0; e < 2; ++e) {
+    const int r = 8 * e + 4 * hh + ((lane & 15) >> 2), dim = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    voff[e] = r * ROWB + (((dim >> 3) ^ swizzle<HD>(r)) << 4) + ((dim & 4) << 1);
+  }
+  auto value_frag = [&](const char* vb, int u, int d) {
+    VFrag f;
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      p[u] = __builtin_bit_cast(bf16x8, make_uint4(pack_bf16x2(x[8 * u], x[8 * u + 1]), pack_bf16x2(x[8 * u + 2], x[8 * u + 3]),
-                                                   pack_bf16x2(x[8 * u + 4], x[8 * u + 5]), pack_bf16x2(x[8 * u + 6], x[8 * u + 7])));
-    if (__any(al != 1.0f)) {
+    for (int e = 0; e < 2; ++e) f.s[e] = lds_read_tr(vb + ((voff[e] ^ (d << 6)) + 16 * u * ROWB));
+    return f;
+  };
+
+  // K tile t lies in buffer t % 3, V tile t in buffer t % 2; during tile t the loads of
+  // K t + 2 and V t + 1 are in flight
+  char* const vbuf = smem + 3 * TILEB;
+  fetch(kbase, a.k_stride, koffs, 0, smem);
+  fetch(vbase, a.v_stride, voffs, 0, vbuf);
+  if (nt > 1) fetch(kbase, a.k_stride, koffs, 1, smem + TILEB);
+  int t = 0, kslot = 0;                     // kslot: t % 3
+  auto turn = [&]() {                       // open tile t: its operands have landed, its buffers-to-be are free
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    const int k2 = kslot == 0 ? 2 : kslot - 1;
+    if (t + 2 < nt) fetch(kbase, a.k_stride, koffs, t + 2, smem + k2 * TILEB);
+    if (t + 1 < nt) fetch(vbase, a.v_stride, voffs, t + 1, vbuf + ((t + 1) & 1) * TILEB);
+  };
+  // keeps the flipped offsets out of registers across the loop: they are one instruction
+  auto fresh = [&]() { asm volatile("" : "+v"(koff), "+v"(voff[0]), "+v"(voff[1])); };
+  auto next_slot = [&]() { kslot = kslot == 2 ? 0 : kslot + 1; };
+
+  // tiles that every row of the wave sees whole: cur holds tile t's scores, nxt takes the
+  // next tile's (of no use after the last)
+  auto step = [&](floatx16 (&cur)[RW][2], floatx16 (&nxt)[RW][2]) {
+    turn();
+    fresh();
+    next_slot();
+    const char* kb = smem + kslot * TILEB;
+    const char* vb = vbuf + (t & 1) * TILEB;
+    // eight groups of products, each with its operands read one group ahead and the vector
+    // work of other data beside it
+    constexpr int KG = HD / 32, VG = HD / 32;      // operands of a group: half a row's dims; a value row's
+    bf16x8 kf[2][KG], p[RW][4];
+    VFrag vf[2][VG];
 #pragma unroll
-      for (int d = 0; d < HD / 32; ++d) o[d] *= al;
+    for (int i = 0; i < KG; ++i) kf[0][i] = key_frag(kb, 0, i);
+#pragma unroll
+    for (int gq = 0; gq < 4; ++gq) {
+      const int s = gq >> 1, k0 = (gq & 1) * KG;
+      if (gq < 3) {
+#pragma unroll
+        for (int i = 0; i < KG; ++i) kf[(gq + 1) & 1][i] = key_frag(kb, (gq + 1) >> 1, ((gq + 1) & 1) * KG + i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VG; ++i) vf[0][i] = value_frag(vb, 0, i);
+      }
+#pragma unroll
+      for (int b = 0; b < RW; ++b) {
+        if (k0 == 0) nxt[b][s] = floatx16{};
+        if (gq & 1) p[b][gq >> 1] = weights(cur[b], b, gq >> 1);
+      }
+#pragma unroll
+      for (int i = 0; i < KG; ++i)
+#pragma unroll
+        for (int b = 0; b < RW; ++b)
+          nxt[b][s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[gq & 1][i], qf[b][k0 + i], nxt[b][s], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
+      if (u < 3) {
 #pragma unroll
-      for (int d = 0; d < HD / 32; ++d) {
-        // keys 16 u + 4 hh .. + 3 and 8 more on, dim 32 d + col
-        union {
-          shortx4 s[2];
-          uint32_t w[4];
-          bf16x8 v;
-        } vt;
+        for (int i = 0; i < VG; ++i) vf[(u + 1) & 1][i] = value_frag(vb, u + 1, i);
+      }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 16 * u + 8 * e + 4 * hh + ((lane & 15) >> 2);
-          const int dim = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-          const char* at = vbuf + r * ROWB + (((dim >> 3) ^ swizzle<HD>(r)) << 4) + ((dim & 4) << 1);
-          vt.s[e] = lds_read_tr(at);
-        }
-        int odd = 0;
-        if (partial) {
-          // in a tile some row does not see whole, a value that is not finite must not
-          // meet that row's zero weight
-          const bool any =
-              bf16x2_nonfinite(vt.w[0]) || bf16x2_nonfinite(vt.w[1]) || bf16x2_nonfinite(vt.w[2]) ||
-                bf16x2_nonfinite(vt.w[3]);
-          odd = __any(any);
-        }
-        odd = uniform(odd);
-        if (!odd) {
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vt.v, p[u], o[d], 0, 0, 0);
-        } else {
-          // key by key, added only to the rows that see it
-          for (int k = 0; k < 16; ++k) {
-            const int jj = (k & 3) | ((k >> 3) << 2);
-            const uint32_t half = jj & 1 ? 0xFFFF0000u : 0x0000FFFFu;
-            const bool mine = hh == ((k >> 2) & 1);
-            const bf16x8 one = __builtin_bit_cast(
-                bf16x8, make_uint4(mine && jj / 2 == 0 ? vt.w[0] & half : 0u, mine && jj / 2 == 1 ? vt.w[1] & half : 0u,
-                                   mine && jj / 2 == 2 ? vt.w[2] & half : 0u, mine && jj / 2 == 3 ? vt.w[3] & half : 0u));
-            const floatx16 add = __builtin_amdgcn_mfma_f32_32x32x16_bf16(one, p[u], floatx16{}, 0, 0, 0);
-            if (key0 + 16 * u + k < lim) o[d] += add;
+      for (int b = 0; b < RW; ++b)
+        if (u < 2) p[b][u + 2] = weights(cur[b], b, u + 2);
+#pragma unroll
+      for (int d = 0; d < VG; ++d)
+#pragma unroll
+        for (int b = 0; b < RW; ++b)
+          o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[u & 1][d].v, p[b][u], o[b][d], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    ++t;
+    if (uniform(t < nfull)) {
+      float tm[RW];
+#pragma unroll
+      for (int b = 0; b < RW; ++b) tm[b] = row_max(nxt[b]);
+      raise(tm);
+    }
+  };
+  floatx16 sa[RW][2];
+  if (uniform(nfull > 0)) {
+    floatx16 sb[RW][2];
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    float tm[RW];
+    scores(sa, smem);
+#pragma unroll
+    for (int b = 0; b < RW; ++b) tm[b] = row_max(sa[b]);
+    raise(tm);
+    while (true) {
+      step(sa, sb);
+      if (uniform(t >= nfull)) break;
+      step(sb, sa);
+      if (uniform(t >= nfull)) break;
+    }
+  } else {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+  }
+  // tiles that some row sees only in part, one product after the other
+  for (; t < nt; ++t) {
+    turn();
+    if (uniform(t < nsome)) {
+      const char* vb = vbuf + (t & 1) * TILEB;
+      float tm[RW];
+      scores(sa, smem + kslot * TILEB);
+      mask(sa, t);
+#pragma unroll
+      for (int b = 0; b < RW; ++b) tm[b] = row_max(sa[b]);
+      raise(tm);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        bf16x8 p[RW];
+#pragma unroll
+        for (int b = 0; b < RW; ++b) p[b] = weights(sa[b], b, u);
+#pragma unroll
+        for (int d = 0; d < HD / 32; ++d) {
+          const VFrag f = value_frag(vb, u, d);
+          // a value that is not finite must not meet the zero weight of a row that does not see it
+          const bool any = bf16x2_nonfinite(f.w[0]) || bf16x2_nonfinite(f.w[1]) || bf16x2_nonfinite(f.w[2]) ||
+                           bf16x2_nonfinite(f.w[3]);
+          if (!uniform(__any(any))) {
+#pragma unroll
+            for (int b = 0; b < RW; ++b) o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.v, p[b], o[b][d], 0, 0, 0);
+          } else {
+            // key by key, added only to the rows that see it
+#pragma unroll 1
+            for (int k = 0; k < 16; ++k) {
+              const int jj = (k & 3) | ((k >> 3) << 2);
+              const uint32_t half = jj & 1 ? 0xFFFF0000u : 0x0000FFFFu;
+              const bool mine = hh == ((k >> 2) & 1);
+              const bf16x8 one = __builtin_bit_cast(
+                  bf16x8, make_uint4(mine && jj / 2 == 0 ? f.w[0] & half : 0u, mine && jj / 2 == 1 ? f.w[1] & half : 0u,
+                                     mine && jj / 2 == 2 ? f.w[2] & half : 0u, mine && jj / 2 == 3 ? f.w[3] & half : 0u));
+#pragma unroll
+              for (int b = 0; b < RW; ++b) {
+                const floatx16 add = __builtin_amdgcn_mfma_f32_32x32x16_bf16(one, p[b], floatx16{}, 0, 0, 0);
+                if (t * KT + 16 * u + k < lim[b]) o[b][d] += add;
+              }
+            }
           }
         }
       }
     }
+    next_slot();
   }
 
-  {
+#pragma unroll
+  for (int b = 0; b < RW; ++b) {
     uint32_t lo, hi;
-    halves_pair(__float_as_uint(l), lo, hi);
-    l = __uint_as_float(lo) + __uint_as_float(hi);
+    halves_pair(__float_as_uint(l[b]), lo, hi);
+    const float lt = __uint_as_float(lo) + __uint_as_float(hi);
+    if (!ok[b]) continue;
+    const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
+    const size_t at = (size_t)(start + row_j[b]) * a.nh + row_h[b];
+#pragma unroll
+    for (int d = 0; d < HD / 32; ++d)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint2*>(a.out + at * HD + 32 * d + 8 * q + 4 * hh) =
+            lt == 0.0f ? make_uint2(0u, 0u)
+                       : make_uint2(pack_bf16x2(o[b][d][4 * q] * inv, o[b][d][4 * q + 1] * inv),
+                                    pack_bf16x2(o[b][d][4 * q + 2] * inv, o[b][d][4 * q + 3] * inv));
+    if (a.lse && hh == 0) a.lse[at] = row_lse(m[b], lt);
   }
-  if (!ok) return;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const size_t at = (size_t)(start + j) * a.nh + h;
-#pragma unroll
-  for (int d = 0; d < HD / 32; ++d)
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<uint2*>(a.out + at * HD + 32 * d + 8 * q + 4 * hh) =
-          l == 0.0f ? make_uint2(0u, 0u)
-                    : make_uint2(pack_bf16x2(o[d][4 * q] * inv, o[d][4 * q + 1] * inv),
-                                 pack_bf16x2(o[d][4 * q + 2] * inv, o[d][4 * q + 3] * inv));
-  if (a.lse && hh == 0) a.lse[at] = row_lse(m, l);
 }
 
-template <int HD, int NW>
-hipError_t launch(const Work& w, hipStream_t stream) {
+template <int HD, int RW, int NW, bool kCausal>
+hipError_t launch_one(const Work& w, hipStream_t stream) {
   const PromptArgs& a = w.a;
-  const int64_t tiles = ((int64_t)a.T * w.G + 32 * NW - 1) / (32 * NW) + a.B;
-  const dim3 grid((unsigned)(tiles * a.nkv));
-  if (a.causal)
-    hipLaunchKernelGGL((prompt_rows<HD, NW, true>), grid, dim3(64 * NW), 0, stream, w);
-  else
-    hipLaunchKernelGGL((prompt_rows<HD, NW, false>), grid, dim3(64 * NW), 0, stream, w);
+  constexpr int rows = 32 * RW * NW, lds = 5 * KT * HD * 2;
+  const int64_t tiles = ((int64_t)a.T * w.G + rows - 1) / rows + a.B;
+  if (lds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&prompt_rows<HD, RW, NW, kCausal>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((prompt_rows<HD, RW, NW, kCausal>), dim3((unsigned)(tiles * a.nkv)), dim3(64 * NW), lds, stream, w);
   return hipGetLastError();
+}
+
+template <int HD, int RW, int NW>
+hipError_t launch(const Work& w, hipStream_t stream) {
+  return w.a.causal ? launch_one<HD, RW, NW, true>(w, stream) : launch_one<HD, RW, NW, false>(w, stream);
 }
 
 }  // namespace
@@ -261,9 +440,9 @@ hipError_t launch_prompt_attention(const PromptArgs& a, int hd, hipStream_t stre
   w.G = a.nh / a.nkv;
   w.c = a.scale * kLog2e;
   switch (hd) {
-    case 64: return launch<64, 4>(w, stream);
-    case 128: return launch<128, 4>(w, stream);
-    case 256: return launch<256, 4>(w, stream);
+    case 64: return launch<64, 1, 8>(w, stream);
+    case 128: return launch<128, 1, 8>(w, stream);
+    case 256: return launch<256, 1, 4>(w, stream);
     default: return hipErrorInvalidValue;
   }
 }
