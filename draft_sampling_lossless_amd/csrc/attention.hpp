@@ -31,9 +31,16 @@ __device__ __forceinline__ shortx4 lds_read_tr(const char* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4*)p);
 }
 
-// global -> LDS without registers: lane i's 16 bytes go to lds_base + 16 i
-__device__ __forceinline__ void load_to_lds16(const uint16_t* src, char* lds_base) {
-  __builtin_amdgcn_global_load_lds(src, lds_base, 16, 0, 0);
+// global -> LDS without registers: lane i's 16 bytes at base + off go to LDS byte address
+// lds + 16 i (base and lds uniform).  Written in assembly because the compiler otherwise
+// makes every later LDS read wait for every such load; the callers wait themselves
+// (s_waitcnt vmcnt, then a barrier) before a buffer is read.  It has no register result.
+__device__ __forceinline__ void load_to_lds16(const char* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const char* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
 }
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }

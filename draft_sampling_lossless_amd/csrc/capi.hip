@@ -593,6 +593,7 @@ dspark_status dspark_prompt_attention(const uint16_t* q, int64_t q_stride, const
           "q_stride must be a multiple of 8 and >= nh * hd (got %lld)", (long long)q_stride);
   REQUIRE(k_stride >= krow && k_stride % 8 == 0 && v_stride >= krow && v_stride % 8 == 0, DSPARK_ERR_INVALID,
           "k_stride and v_stride must be multiples of 8 and >= nkv * hd");
+  REQUIRE(k_stride < (1 << 24) && v_stride < (1 << 24), DSPARK_ERR_UNSUPPORTED, "k_stride and v_stride must be < 2^24");
   REQUIRE(causal == 0 || causal == 1, DSPARK_ERR_INVALID, "causal must be 0 or 1 (got %d)", causal);
   if (T == 0) return ok();
   REQUIRE_PTR16(q, "q");

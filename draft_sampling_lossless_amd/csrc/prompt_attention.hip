@@ -23,7 +23,9 @@ namespace dspark {
 
 namespace {
 
-constexpr int KT = 64;   // keys per tile
+
+// keys per tile: 16 KB of K and of V (8 KB for heads of 64)
+__host__ __device__ constexpr int tile_keys(int hd) { return hd > 128 ? 32 : 64; }
 
 struct Work {
   PromptArgs a;
@@ -42,16 +44,55 @@ __device__ __forceinline__ void sequence(const PromptArgs& a, int b, int& start,
   n = clampi(a.cu_seqlens[b + 1], start, a.T) - start;
 }
 
-// the sequence and row tile of item u; every wave finds them for itself
+// The sequence and row tile of item u; every wave finds them for itself.  A causal tile
+// costs as much as its index says, and the dearest go first: item u is the u-th of all
+// tiles by falling index (of up to 64 sequences; a longer batch has tiles enough to even
+// out in the order of its sequences, a sequence's last first).
 __device__ bool find_tile(const Work& w, int u, int rows, int& start, int& n, int& tile) {
   const PromptArgs& a = w.a;
   const int lane = threadIdx.x & 63;
+  auto tiles_of = [&](int len) { return (int)(((int64_t)len * w.G + rows - 1) / rows); };
+  if (a.B == 1) {
+    sequence(a, 0, start, n);
+    start = uniform(start);
+    n = uniform(n);
+    tile = uniform(tiles_of(n)) - 1 - u;
+    return tile >= 0;
+  }
+  if (a.causal && a.B <= 64) {
+    int s = 0, len = 0;
+    if (lane < a.B) sequence(a, lane, s, len);
+    const int mine = tiles_of(len);
+    int hi = mine;
+    for (int o = 32; o > 0; o >>= 1) hi = max(hi, __shfl_xor(hi, o));
+    // the level: the largest index that leaves more than u tiles at or above it
+    auto at_least = [&](int level) {
+      int c = max(mine - level, 0);
+      for (int o = 32; o > 0; o >>= 1) c += __shfl_xor(c, o);
+      return uniform(c);
+    };
+    int lo = 0;
+    hi = uniform(hi);
+    if (at_least(0) <= u) return false;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (at_least(mid) > u) lo = mid;
+      else hi = mid;
+    }
+    uint64_t have = __ballot(mine > lo);     // one tile of this index each
+    for (int skip = u - at_least(lo + 1); skip > 0; --skip) have &= have - 1;
+    const int q = __builtin_ctzll(have);
+    start = __builtin_amdgcn_readlane(s, q);
+    n = __builtin_amdgcn_readlane(len, q);
+    tile = lo;
+    return true;
+  }
   int before = 0;
   for (int base = 0; base < a.B; base += 64) {
     int s = 0, len = 0, cnt = 0;
     if (base + lane < a.B) {
       sequence(a, base + lane, s, len);
-      cnt = (int)(((int64_t)len * w.G + rows - 1) / rows);
+      cnt = tiles_of(len);
     }
     int inc = cnt;
 #pragma unroll
@@ -64,7 +105,7 @@ __device__ bool find_tile(const Work& w, int u, int rows, int& start, int& n, in
       const int q = __builtin_ctzll(hit);
       start = __builtin_amdgcn_readlane(s, q);
       n = __builtin_amdgcn_readlane(len, q);
-      tile = before + __builtin_amdgcn_readlane(inc, q) - 1 - u;   // a sequence's last tile first
+      tile = before + __builtin_amdgcn_readlane(inc, q) - 1 - u;
       return true;
     }
     before += __builtin_amdgcn_readlane(inc, 63);
@@ -83,13 +124,15 @@ constexpr float kRaise = 8.0f;
 
 template <int HD, int RW, int NW, bool kCausal>
 __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
+  constexpr int KT = tile_keys(HD);         // keys per tile
+  constexpr int SB = KT / 32, UG = KT / 16; // its score blocks, its groups of 16 keys
   constexpr int PIECES = HD / 8;            // 16-byte pieces of a row
   constexpr int ROWB = HD * 2;
   constexpr int TILEB = KT * ROWB;
   constexpr int WGROWS = 32 * RW * NW;
   constexpr int LOADS = KT * PIECES / (64 * NW);   // 1 KB loads of a wave for one tile of K (or V)
   const PromptArgs& a = w.a;
-  extern __shared__ __attribute__((aligned(16))) char smem[];   // three K tiles, two V tiles
+  extern __shared__ __attribute__((aligned(16))) char smem[];   // four K tiles, two V tiles
 
   const int kvh = blockIdx.x % a.nkv;
   int start, n, tile;
@@ -132,20 +175,22 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
     koffs[q] = (uint32_t)r * (uint32_t)(a.k_stride * 2) + piece * 16;
     voffs[q] = (uint32_t)r * (uint32_t)(a.v_stride * 2) + piece * 16;
   }
-  auto fetch = [&](const uint16_t* base, int64_t stride, const uint32_t (&offs)[LOADS], int t, char* lds) {
-    const char* tb = reinterpret_cast<const char*>(base + (size_t)t * KT * stride);
-    if (uniform((t + 1) * KT <= n)) {
+  // the tile that the sequence ends in: its offsets are cut once, before its load
+  auto cut = [&](uint32_t (&offs)[LOADS], int64_t stride, int t) {
 #pragma unroll
-      for (int q = 0; q < LOADS; ++q)
-        load_to_lds16(reinterpret_cast<const uint16_t*>(tb + offs[q]), lds + (q * NW + wave) * 1024);
-    } else {
-#pragma unroll
-      for (int q = 0; q < LOADS; ++q) {
-        const int r = ((q * NW + wave) * 64 + lane) / PIECES, over = max(r - (n - 1 - t * KT), 0);
-        load_to_lds16(reinterpret_cast<const uint16_t*>(tb + (offs[q] - (uint32_t)over * (uint32_t)(stride * 2))),
-                      lds + (q * NW + wave) * 1024);
-      }
+    for (int q = 0; q < LOADS; ++q) {
+      const int r = ((q * NW + wave) * 64 + lane) / PIECES, over = max(r - (n - 1 - t * KT), 0);
+      offs[q] -= (uint32_t)over * (uint32_t)(stride * 2);
     }
+  };
+  auto fetch_one = [&](const uint16_t* base, int64_t stride, const uint32_t (&offs)[LOADS], int t, char* lds, int q) {
+    const char* tb = reinterpret_cast<const char*>(base + (size_t)t * KT * stride);
+    load_to_lds16(tb, offs[q], uniform(lds_address(lds) + (q * NW + wave) * 1024));
+  };
+  auto fetch = [&](const uint16_t* base, int64_t stride, uint32_t (&offs)[LOADS], int t, char* lds) {
+    if (uniform((t + 1) * KT > n)) cut(offs, stride, t);
+#pragma unroll
+    for (int q = 0; q < LOADS; ++q) fetch_one(base, stride, offs, t, lds, q);
   };
   const uint16_t* kbase = a.k + (size_t)start * a.k_stride + (size_t)kvh * HD;
   const uint16_t* vbase = a.v + (size_t)start * a.v_stride + (size_t)kvh * HD;
@@ -166,9 +211,9 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
   auto key_frag = [&](const char* kb, int s, int kk) {
     return *reinterpret_cast<const bf16x8*>(kb + ((koff ^ (kk << 5)) + 32 * s * ROWB));
   };
-  auto scores = [&](floatx16 (&sc)[RW][2], const char* kb) {
+  auto scores = [&](floatx16 (&sc)[RW][SB], const char* kb) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < SB; ++s) {
 #pragma unroll
       for (int b = 0; b < RW; ++b) sc[b][s] = floatx16{};
 #pragma unroll
@@ -179,22 +224,21 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
       }
     }
   };
-  auto row_max = [&](const floatx16 (&sc)[2]) {
-    float t0 = sc[0][0], t1 = sc[1][0];
+  auto row_max = [&](const floatx16 (&sc)[SB]) {
+    float top = sc[0][0];
 #pragma unroll
-    for (int e = 1; e < 16; ++e) {
-      t0 = fmaxf(t0, sc[0][e]);
-      t1 = fmaxf(t1, sc[1][e]);
-    }
+    for (int s = 0; s < SB; ++s)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[s][e]);
     uint32_t lo, hi;
-    halves_pair(__float_as_uint(fmaxf(t0, t1)), lo, hi);
+    halves_pair(__float_as_uint(top), lo, hi);
     return fmaxf(__uint_as_float(lo), __uint_as_float(hi)) * w.c;
   };
-  auto mask = [&](floatx16 (&sc)[RW][2], int t) {
+  auto mask = [&](floatx16 (&sc)[RW][SB], int t) {
 #pragma unroll
     for (int b = 0; b < RW; ++b)
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int s = 0; s < SB; ++s)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           if (t * KT + 32 * s + 8 * (e >> 2) + 4 * hh + (e & 3) >= lim[b]) sc[b][s][e] = -INFINITY;
@@ -219,14 +263,16 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
   };
   // weights of keys 16 u .. 16 u + 15 of the tile, rounded to bf16 (the second product's
   // operand type), and their sum
-  auto weights = [&](const floatx16 (&sc)[2], int b, int u) {
-    float x[8];
+  auto weights = [&](const floatx16 (&sc)[SB], int b, int u, int half, uint32_t (&p)[4]) {
+    float x[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[u >> 1][8 * (u & 1) + e], w.c, -mb[b]));
-    l[b] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-    return __builtin_bit_cast(bf16x8, make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                 pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
+    for (int e = 0; e < 4; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[u >> 1][8 * (u & 1) + 4 * half + e], w.c, -mb[b]));
+    l[b] += (x[0] + x[1]) + (x[2] + x[3]);
+    p[2 * half] = pack_bf16x2(x[0], x[1]);
+    p[2 * half + 1] = pack_bf16x2(x[2], x[3]);
+    asm volatile("" : "+v"(p[2 * half]), "+v"(p[2 * half + 1]));
   };
+  auto as_frag = [](const uint32_t (&p)[4]) { return __builtin_bit_cast(bf16x8, make_uint4(p[0], p[1], p[2], p[3])); };
   union VFrag {
     shortx4 s[2];
     uint32_t w[4];
@@ -246,151 +292,192 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
     return f;
   };
 
-  // K tile t lies in buffer t % 3, V tile t in buffer t % 2; during tile t the loads of
-  // K t + 2 and V t + 1 are in flight
-  char* const vbuf = smem + 3 * TILEB;
-  fetch(kbase, a.k_stride, koffs, 0, smem);
-  fetch(vbase, a.v_stride, voffs, 0, vbuf);
-  if (nt > 1) fetch(kbase, a.k_stride, koffs, 1, smem + TILEB);
-  int t = 0, kslot = 0;                     // kslot: t % 3
-  auto turn = [&]() {                       // open tile t: its operands have landed, its buffers-to-be are free
+  // K tile t lies in buffer t % 4, V tile t in buffer t % 2; during tile t the loads of
+  // K t + 3 and V t + 1 are in flight
+  char* const vbuf = smem + 4 * TILEB;
+  auto kbuf_of = [&](int t) { return smem + (t & 3) * TILEB; };
+  auto vbuf_of = [&](int t) { return vbuf + (t & 1) * TILEB; };
+  int t = 0;
+  auto open_tile = [&]() {                  // tile t: its operands have landed, its buffers-to-be are free
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    const int k2 = kslot == 0 ? 2 : kslot - 1;
-    if (t + 2 < nt) fetch(kbase, a.k_stride, koffs, t + 2, smem + k2 * TILEB);
-    if (t + 1 < nt) fetch(vbase, a.v_stride, voffs, t + 1, vbuf + ((t + 1) & 1) * TILEB);
   };
   // keeps the flipped offsets out of registers across the loop: they are one instruction
   auto fresh = [&]() { asm volatile("" : "+v"(koff), "+v"(voff[0]), "+v"(voff[1])); };
-  auto next_slot = [&]() { kslot = kslot == 2 ? 0 : kslot + 1; };
+  fetch(kbase, a.k_stride, koffs, 0, kbuf_of(0));
+  if (nt > 1) fetch(kbase, a.k_stride, koffs, 1, kbuf_of(1));
+  if (nt > 2) fetch(kbase, a.k_stride, koffs, 2, kbuf_of(2));
+  fetch(vbase, a.v_stride, voffs, 0, vbuf_of(0));
 
   // tiles that every row of the wave sees whole: cur holds tile t's scores, nxt takes the
-  // next tile's (of no use after the last)
-  auto step = [&](floatx16 (&cur)[RW][2], floatx16 (&nxt)[RW][2]) {
-    turn();
+  // next tile's (of no use after the last).  Four groups of the first product and UG of
+  // the second, each with its operands read one group ahead (the first group's before the
+  // barrier) and an equal share of the vector work
+  constexpr int KG = SB * (HD / 16) / 4, VG = HD / 32;
+  bf16x8 kf[2][KG];
+  auto step = [&](floatx16 (&cur)[RW][SB], floatx16 (&nxt)[RW][SB]) {
+    open_tile();
+    if (uniform((t + 4) * KT > n && t + 3 < nt)) cut(koffs, a.k_stride, t + 3);
+    if (uniform((t + 2) * KT > n && t + 1 < nt)) cut(voffs, a.v_stride, t + 1);
     fresh();
-    next_slot();
-    const char* kb = smem + kslot * TILEB;
-    const char* vb = vbuf + (t & 1) * TILEB;
-    // eight groups of products, each with its operands read one group ahead and the vector
-    // work of other data beside it
-    constexpr int KG = HD / 32, VG = HD / 32;      // operands of a group: half a row's dims; a value row's
-    bf16x8 kf[2][KG], p[RW][4];
+    const char* kb = kbuf_of(t + 1);
+    const char* vb = vbuf_of(t);
+    uint32_t p[RW][UG][4];
+    float tm[RW];
     VFrag vf[2][VG];
 #pragma unroll
-    for (int i = 0; i < KG; ++i) kf[0][i] = key_frag(kb, 0, i);
-#pragma unroll
     for (int gq = 0; gq < 4; ++gq) {
-      const int s = gq >> 1, k0 = (gq & 1) * KG;
       if (gq < 3) {
 #pragma unroll
-        for (int i = 0; i < KG; ++i) kf[(gq + 1) & 1][i] = key_frag(kb, (gq + 1) >> 1, ((gq + 1) & 1) * KG + i);
+        for (int i = 0; i < KG; ++i) {
+          const int f = (gq + 1) * KG + i;
+          kf[(gq + 1) & 1][i] = key_frag(kb, f % SB, f / SB);
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < VG; ++i) vf[0][i] = value_frag(vb, 0, i);
       }
 #pragma unroll
       for (int b = 0; b < RW; ++b) {
-        if (k0 == 0) nxt[b][s] = floatx16{};
-        if (gq & 1) p[b][gq >> 1] = weights(cur[b], b, gq >> 1);
+        if (gq == 0)
+#pragma unroll
+          for (int s = 0; s < SB; ++s) nxt[b][s] = floatx16{};
+        weights(cur[b], b, gq >> 1, gq & 1, p[b][gq >> 1]);
       }
 #pragma unroll
       for (int i = 0; i < KG; ++i)
 #pragma unroll
-        for (int b = 0; b < RW; ++b)
-          nxt[b][s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[gq & 1][i], qf[b][k0 + i], nxt[b][s], 0, 0, 0);
+        for (int b = 0; b < RW; ++b) {
+          const int f = gq * KG + i;
+          nxt[b][f % SB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[gq & 1][i], qf[b][f / SB], nxt[b][f % SB], 0, 0, 0);
+        }
       __builtin_amdgcn_sched_barrier(0);
+      // the loads to come, spread over the tile: all at once they would hold up every wave
+      if (uniform(t + 3 < nt)) {
+#pragma unroll
+        for (int q = 0; q < LOADS; ++q)
+          if (q * 4 / LOADS == gq) fetch_one(kbase, a.k_stride, koffs, t + 3, kbuf_of(t + 3), q);
+      }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (u < 3) {
+    for (int u = 0; u < UG; ++u) {
+      if (u < UG - 1) {
 #pragma unroll
         for (int i = 0; i < VG; ++i) vf[(u + 1) & 1][i] = value_frag(vb, u + 1, i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < KG; ++i) kf[0][i] = key_frag(kbuf_of(t + 2), i % SB, i / SB);
       }
 #pragma unroll
-      for (int b = 0; b < RW; ++b)
-        if (u < 2) p[b][u + 2] = weights(cur[b], b, u + 2);
+      for (int b = 0; b < RW; ++b) {
+        if (UG > 2 && u == 0) {
+          weights(cur[b], b, 2, 0, p[b][2]);
+          weights(cur[b], b, 2, 1, p[b][2]);
+        } else if (UG > 2 && u < 3) {
+          weights(cur[b], b, 3, u - 1, p[b][3]);
+        }
+        if (u == UG - 1) tm[b] = row_max(nxt[b]);
+      }
 #pragma unroll
       for (int d = 0; d < VG; ++d)
 #pragma unroll
         for (int b = 0; b < RW; ++b)
-          o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[u & 1][d].v, p[b][u], o[b][d], 0, 0, 0);
+          o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[u & 1][d].v, as_frag(p[b][u]), o[b][d], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
+      if (uniform(t + 1 < nt)) {
+#pragma unroll
+        for (int q = 0; q < LOADS; ++q)
+          if (q * UG / LOADS == u) fetch_one(vbase, a.v_stride, voffs, t + 1, vbuf_of(t + 1), q);
+      }
     }
     ++t;
-    if (uniform(t < nfull)) {
-      float tm[RW];
-#pragma unroll
-      for (int b = 0; b < RW; ++b) tm[b] = row_max(nxt[b]);
-      raise(tm);
-    }
+    if (uniform(t < nfull)) raise(tm);      // (the scores of a tile seen in part are formed again, masked)
   };
-  floatx16 sa[RW][2];
+  floatx16 sa[RW][SB];
+  open_tile();
   if (uniform(nfull > 0)) {
-    floatx16 sb[RW][2];
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
+    floatx16 sb[RW][SB];
     float tm[RW];
-    scores(sa, smem);
+    scores(sa, kbuf_of(0));
 #pragma unroll
     for (int b = 0; b < RW; ++b) tm[b] = row_max(sa[b]);
     raise(tm);
+#pragma unroll
+    for (int i = 0; i < KG; ++i) kf[0][i] = key_frag(kbuf_of(1), i % SB, i / SB);
     while (true) {
       step(sa, sb);
       if (uniform(t >= nfull)) break;
       step(sb, sa);
       if (uniform(t >= nfull)) break;
     }
-  } else {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
   }
-  // tiles that some row sees only in part, one product after the other
+  // tiles that some row sees only in part, one product after the other; groups of keys
+  // that no row of the wave sees are left out
   for (; t < nt; ++t) {
-    turn();
+    open_tile();
+    if (t + 3 < nt) fetch(kbase, a.k_stride, koffs, t + 3, kbuf_of(t + 3));
+    if (t + 1 < nt) fetch(vbase, a.v_stride, voffs, t + 1, vbuf_of(t + 1));
     if (uniform(t < nsome)) {
-      const char* vb = vbuf + (t & 1) * TILEB;
+      const char* vb = vbuf_of(t);
       float tm[RW];
-      scores(sa, smem + kslot * TILEB);
+      scores(sa, kbuf_of(t));
       mask(sa, t);
 #pragma unroll
       for (int b = 0; b < RW; ++b) tm[b] = row_max(sa[b]);
       raise(tm);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < UG; ++u) {
+        const int first = t * KT + 16 * u;
+        if (uniform(first >= whigh)) continue;
         bf16x8 p[RW];
+        VFrag f[HD / 32];
+        uint32_t top = 0;                   // the largest exponent, in the high half
 #pragma unroll
-        for (int b = 0; b < RW; ++b) p[b] = weights(sa[b], b, u);
+        for (int b = 0; b < RW; ++b) {
+          uint32_t pw[4];
+          weights(sa[b], b, u, 0, pw);
+          weights(sa[b], b, u, 1, pw);
+          p[b] = as_frag(pw);
+        }
 #pragma unroll
-        for (int d = 0; d < HD / 32; ++d) {
-          const VFrag f = value_frag(vb, u, d);
+        for (int d = 0; d < HD / 32; ++d) f[d] = value_frag(vb, u, d);
+        if (uniform(first + 16 > wlow)) {
           // a value that is not finite must not meet the zero weight of a row that does not see it
-          const bool any = bf16x2_nonfinite(f.w[0]) || bf16x2_nonfinite(f.w[1]) || bf16x2_nonfinite(f.w[2]) ||
-                           bf16x2_nonfinite(f.w[3]);
-          if (!uniform(__any(any))) {
 #pragma unroll
-            for (int b = 0; b < RW; ++b) o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.v, p[b], o[b][d], 0, 0, 0);
-          } else {
-            // key by key, added only to the rows that see it
+          for (int d = 0; d < HD / 32; ++d)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t e = f[d].w[k] & 0x7F807F80u;
+              top = max(top, max(e, e << 16));
+            }
+        }
+        if (!uniform(__any(top >= 0x7F800000u))) {
+#pragma unroll
+          for (int d = 0; d < HD / 32; ++d)
+#pragma unroll
+            for (int b = 0; b < RW; ++b) o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[d].v, p[b], o[b][d], 0, 0, 0);
+        } else {
+          // key by key, added only to the rows that see it
 #pragma unroll 1
-            for (int k = 0; k < 16; ++k) {
-              const int jj = (k & 3) | ((k >> 3) << 2);
-              const uint32_t half = jj & 1 ? 0xFFFF0000u : 0x0000FFFFu;
-              const bool mine = hh == ((k >> 2) & 1);
+          for (int k = 0; k < 16; ++k) {
+            const int jj = (k & 3) | ((k >> 3) << 2);
+            const uint32_t half = jj & 1 ? 0xFFFF0000u : 0x0000FFFFu;
+            const uint32_t keep = hh == ((k >> 2) & 1) ? half : 0u;
+#pragma unroll
+            for (int d = 0; d < HD / 32; ++d) {
               const bf16x8 one = __builtin_bit_cast(
-                  bf16x8, make_uint4(mine && jj / 2 == 0 ? f.w[0] & half : 0u, mine && jj / 2 == 1 ? f.w[1] & half : 0u,
-                                     mine && jj / 2 == 2 ? f.w[2] & half : 0u, mine && jj / 2 == 3 ? f.w[3] & half : 0u));
+                  bf16x8, make_uint4(jj / 2 == 0 ? f[d].w[0] & keep : 0u, jj / 2 == 1 ? f[d].w[1] & keep : 0u,
+                                     jj / 2 == 2 ? f[d].w[2] & keep : 0u, jj / 2 == 3 ? f[d].w[3] & keep : 0u));
 #pragma unroll
               for (int b = 0; b < RW; ++b) {
                 const floatx16 add = __builtin_amdgcn_mfma_f32_32x32x16_bf16(one, p[b], floatx16{}, 0, 0, 0);
-                if (t * KT + 16 * u + k < lim[b]) o[b][d] += add;
+                if (first + k < lim[b]) o[b][d] += add;
               }
             }
           }
         }
       }
     }
-    next_slot();
   }
 
 #pragma unroll
@@ -416,7 +503,7 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
 template <int HD, int RW, int NW, bool kCausal>
 hipError_t launch_one(const Work& w, hipStream_t stream) {
   const PromptArgs& a = w.a;
-  constexpr int rows = 32 * RW * NW, lds = 5 * KT * HD * 2;
+  constexpr int rows = 32 * RW * NW, lds = 6 * tile_keys(HD) * HD * 2;
   const int64_t tiles = ((int64_t)a.T * w.G + rows - 1) / rows + a.B;
   if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&prompt_rows<HD, RW, NW, kCausal>),

@@ -482,8 +482,8 @@ dspark_status dspark_paged_attention(const uint16_t* q, int64_t q_stride, const 
  *   lse as dspark_paged_attention's.  Sequences may be empty; rows behind cu_seqlens[B]
  *   are left as they were; keys a row does not see have no influence on it.
  *   q [T, nh, hd], k, v [T, nkv, hd] bf16 bits, token rows q_stride, k_stride, v_stride
- *   elements apart (each % 8 == 0 and at least one row), device, 16-byte aligned;
- *   cu_seqlens [B + 1] int32 ascending from 0, device; out [T, nh, hd] bf16, 16-byte
+ *   elements apart (each % 8 == 0 and at least one row; k_stride, v_stride < 2^24), device,
+ *   16-byte aligned; cu_seqlens [B + 1] int32 ascending from 0, device; out [T, nh, hd] bf16, 16-byte
  *   aligned; lse [T, nh] float32 or NULL.
  *   hd in {64, 128, 256}; nh % nkv == 0; nh <= 1024; 1 <= B <= DSPARK_MAX_SEQS; scale > 0
  *   and finite; T * nh < 2^30; T == 0 enqueues nothing.  Arithmetic as

@@ -90,6 +90,7 @@ def test_prompt_validation(dspark_lib):
     assert _prompt(T=-4) == INVALID and _prompt(B=0) == INVALID and _prompt(B=4097) == UNSUPPORTED
     assert _prompt(hd=80) == UNSUPPORTED and _prompt(nh=7) == INVALID
     assert _prompt(q_stride=512) == INVALID and _prompt(k_stride=260) == INVALID and _prompt(v_stride=128) == INVALID
+    assert _prompt(k_stride=1 << 24) == UNSUPPORTED and _prompt(v_stride=1 << 30) == UNSUPPORTED
     assert _prompt(causal=-1) == INVALID and _prompt(scale=float("inf")) == INVALID
     for name in ("q", "k", "v", "cu_seqlens", "out"):
         assert _prompt(**{name: None}) == INVALID and name in _err()

@@ -429,6 +429,23 @@ def test_prompt_unseen_keys_do_not_matter():
         assert np.isnan(value(full)[:lens[0]]).all() and np.isfinite(value(full)[lens[0]:]).all()
 
 
+def test_prompt_unseen_keys_with_large_scores():
+    """A key that outweighs all others by far, in tiles that some rows see only in part or
+    not at all: rows before it are what they are without it."""
+    g = np.random.default_rng(24)
+    for hd in (64, 128, 256):
+        T = 200
+        q, k, v = bits(g, T, 4, hd, std=2.0), bits(g, T, 2, hd), bits(g, T, 2, hd)
+        clean, _ = run_prompt(q, k, v, [0, T], True)
+        for at in (40, 63, 64, 100, 130, 199):
+            big = k.copy()
+            big[at] = synth.bf16_bits((100 * ck.bf16_decode(q[at - 1, :2])).astype(np.float32))
+            out, lse = run_prompt(q, big, v, [0, T], True)
+            assert torch.equal(out[:at], clean[:at]), f"hd {hd} key {at}"
+            ref = oa.prompt(q, big, v, [0, T], True, hd ** -0.5)
+            check_rows(out, lse, ref, hd, f"hd {hd} key {at}")
+
+
 def test_prompt_strided_columns_and_graph():
     g = np.random.default_rng(22)
     T, nh, nkv, hd = 260, 8, 2, 128
