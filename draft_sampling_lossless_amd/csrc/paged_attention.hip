@@ -30,14 +30,21 @@ namespace dspark {
 
 namespace {
 
+// The running maximum is raised only when a row's scores exceed it by kRaise (weights up
+// to 2^kRaise, which neither float nor bf16 minds): the accumulators are rescaled on a
+// row's first tile and hardly ever after.
+constexpr float kRaise = 8.0f;
+
 constexpr int NW = 4;          // waves per workgroup; they take tiles in turn
 constexpr int KT = 32;         // keys per tile
-constexpr int kTarget = 1024;  // items aimed at
 constexpr int kMinChunk = 512; // keys of a range, at least
+constexpr int kCus = 256;      // compute units of the card
+constexpr int kJoinGroups = 2048;   // workgroups of the joining pass aimed at
 
 struct Work {
   PagedArgs a;
   int G, RB, unit;     // heads per kv head, row blocks, nkv * RB
+  int target;          // items aimed at
   int pid_cap;         // ranges the workspace has room for
   float c;             // scale * log2 e
   float* part_o;       // [pid_cap, unit, 16 RT, hd]
@@ -73,7 +80,7 @@ __device__ bool find_item(const Work& w, int u, Item& it) {
   if (a.B == 1) {
     request(a, 0, it.q0, it.n, it.kv);
     if (it.n == 0) return false;
-    const int64_t per = ((int64_t)it.kv * w.unit + kTarget - 1) / kTarget;
+    const int64_t per = ((int64_t)it.kv * w.unit + w.target - 1) / w.target;
     it.chunk = max(kMinChunk, (int)((per + step - 1) / step * step));
     it.b = 0;
     it.nsplit = max(1, (it.kv + it.chunk - 1) / it.chunk);
@@ -90,7 +97,7 @@ __device__ bool find_item(const Work& w, int u, Item& it) {
     }
   }
   for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o);
-  const int64_t per = (total * w.unit + kTarget - 1) / kTarget;
+  const int64_t per = (total * w.unit + w.target - 1) / w.target;
   const int64_t up = (per + step - 1) / step * step;
   it.chunk = (int)(up < kMinChunk ? kMinChunk : up > (1 << 30) ? (1 << 30) : up);
   int before = 0, pids = 0;
@@ -438,47 +445,359 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
   }
 }
 
-// one workgroup per (request, row block, kv head): the ranges of a split request, joined
-// in their order; HD / 4 threads take a row
+// ------------------------------------------------------------------ many rows
+// The same work for more than 16 rows: a wave takes 16 rows, and all waves of the
+// workgroup share the keys, which pass through three LDS buffers of 32 (one worked on, two
+// filling straight from memory).  Rows lie there in 16-byte pieces permuted (piece p of
+// row r at p ^ swizzle(r)) so that the K reads (16 rows, one piece) and the transposing V
+// reads (8 rows, two pieces) touch every bank once.  The slots of kWindow keys (small
+// pages) or groups of 16 keys are looked up ahead into LDS by the whole workgroup.  Few
+// registers and 52 KB of LDS leave room for three workgroups on a compute unit, which
+// cover each other's waits.
+constexpr int kWindow = 1024;
+constexpr int kStages = 3;
+
+template <int HD>
+__device__ __forceinline__ int swizzle(int r) {
+  if constexpr (HD == 64) return (((r >> 1) & 3) << 1) | ((r >> 3) & 1);
+  return ((r & 7) << 1) | ((r >> 3) & 1);
+}
+
+template <int HD>
+constexpr int shared_lds() {
+  return kStages * 2 * KT * HD * 2 + kWindow * 4;
+}
+
+template <int HD, int RT, bool kSlots>
+__global__ __launch_bounds__(64 * RT, HD > 128 || RT == 2 ? 2 : RT == 8 ? 4 : 3) void paged_shared(Work w) {
+  constexpr int ROWB = HD * 2, TILEB = KT * ROWB, PIECES = HD / 8;
+  constexpr int LOADS = 2 * TILEB / 1024;         // 1 KB loads of one tile, K then V
+  constexpr int LPW = (LOADS + RT - 1) / RT;      // of a wave (the last wave's may repeat the last load)
+  constexpr int LR = 64 / PIECES;                 // rows of one load
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  int32_t* slots = reinterpret_cast<int32_t*>(smem + kStages * 2 * TILEB);
+  const PagedArgs& a = w.a;
+  const int u = blockIdx.x / w.unit, rest = blockIdx.x % w.unit;
+  const int kvh = rest % a.nkv, rb = rest / a.nkv;
+  Item it;
+  if (!find_item(w, u, it)) return;
+  it.b = uniform(it.b);
+  it.q0 = uniform(it.q0);
+  it.n = uniform(it.n);
+  it.kv = uniform(it.kv);
+  it.chunk = uniform(it.chunk);
+  it.split = uniform(it.split);
+  it.nsplit = uniform(it.nsplit);
+  it.pid = uniform(it.pid);
+  if (rest == 0 && it.split == 0 && threadIdx.x == 0) w.req[it.b] = make_int2(it.pid, it.nsplit);
+  const int nq = min(it.n, a.max_q), row0 = rb * 16 * RT;
+  if (nq * w.G <= row0) return;                                 // (no row of this block exists)
+  if (it.nsplit > 1 && it.pid >= w.pid_cap) return;             // (the workspace holds every range)
+
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int wave = uniform(threadIdx.x >> 6);
+  const bool idle = uniform(row0 + 16 * wave >= nq * w.G) != 0;  // a wave without rows only loads
+  const int row = row0 + 16 * wave + c, j = row / w.G, h = kvh * w.G + row % w.G;
+  const bool ok = j < nq;
+  const int lim = ok && a.causal ? it.kv - it.n + j + 1 : it.kv;        // keys below lim are seen
+  const int minlim = a.causal ? it.kv - it.n + 1 + (row0 + 16 * wave) / w.G : it.kv;
+  bf16x8 qf[HD / 32];
+  {
+    const uint16_t* src = a.q + (size_t)(it.q0 + (ok ? j : 0)) * a.q_stride + (size_t)(ok ? h : 0) * HD;
+#pragma unroll
+    for (int kk = 0; kk < HD / 32; ++kk) {
+      const uint4 v = *reinterpret_cast<const uint4*>(src + 32 * kk + 8 * g);
+      qf[kk] = __builtin_bit_cast(bf16x8, ok ? v : make_uint4(0, 0, 0, 0));
+    }
+  }
+  floatx4 o[HD / 16];                             // dims 16 d + 4 g + i of row c
+#pragma unroll
+  for (int d = 0; d < HD / 16; ++d) o[d] = floatx4{0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, mb = 0.0f, l = 0.0f;       // mb: m, or 0 while the row has seen nothing
+
+  const int k0 = it.split * it.chunk, k1 = min(it.kv, k0 + it.chunk);
+  const int32_t* table = a.page_table + (size_t)it.b * a.width;
+  const int64_t rbytes = (int64_t)a.nkv * ROWB;   // bytes between slots
+  const int pmask = (1 << a.page_shift) - 1;
+  const char* kbase = reinterpret_cast<const char*>(a.k_cache + kvh * HD);
+  const char* vbase = reinterpret_cast<const char*>(a.v_cache + kvh * HD);
+  const int lrow = lane / PIECES, lslot = lane % PIECES;
+  const uint32_t lds0 = lds_address(smem);
+
+  // this wave's loads of a tile; a key that does not exist reads an existing row
+  auto issue = [&](int key0, int win0, int stage) {
+#pragma unroll
+    for (int q = 0; q < LPW; ++q) {
+      const int f = min(q * RT + wave, LOADS - 1), fk = f % (LOADS / 2);
+      const char* base = f < LOADS / 2 ? kbase : vbase;
+      const int r = fk * LR + lrow;               // row of the tile
+      const uint32_t piece = (uint32_t)(lslot ^ swizzle<HD>(r)) << 4;
+      const uint32_t lds = lds0 + stage * 2 * TILEB + f * 1024;
+      if constexpr (kSlots) {
+        const int64_t slot = max(slots[min(key0 + r, it.kv - 1) - win0], 0);
+        load_to_lds16(base + slot * rbytes + piece, uniform(lds));
+      } else {
+        const int ks = key0 + (fk * LR & 16);     // the 16 keys of one page it falls in
+        const int first = uniform(slots[(min(ks, it.kv - 1) - win0) >> 4]);
+        const int last = first < 0 ? 0 : clampi(it.kv - 1 - ks, 0, 15);
+        load_to_lds16(base + (int64_t)max(first, 0) * rbytes, (uint32_t)min(r & 15, last) * (uint32_t)rbytes + piece,
+                      uniform(lds));
+      }
+    }
+  };
+
+  int koff = c * ROWB + ((g ^ swizzle<HD>(c)) << 4);   // K operand (s, kk): piece 4 kk + g of row 16 s + c
+  int voff[2];                                    // V operand d: keys 16 e + 4 g .. + 3, dim 16 d + c
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = 16 * e + 4 * g + (c >> 2), dim = 4 * (c & 3);
+    voff[e] = r * ROWB + (((dim >> 3) ^ swizzle<HD>(r)) << 4) + ((dim & 4) << 1);
+  }
+  union VFrag {
+    shortx4 s[2];
+    uint32_t w[4];
+    bf16x8 v;
+  };
+  auto value_frag = [&](const char* vb, int d) {
+    VFrag f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) f.s[e] = lds_read_tr(vb + (voff[e] ^ (d << 5)));
+    return f;
+  };
+
+  auto work_on = [&](const char* kb, int key0, int win0) {
+    const char* vb = kb + TILEB;
+    asm volatile("" : "+v"(koff), "+v"(voff[0]), "+v"(voff[1]));   // (flipped offsets are cheaper than registers)
+    bool there = key0 + (lane & 31) < it.kv;
+    if (there) {
+      const int e = key0 + (lane & 31) - win0;
+      there = slots[kSlots ? e : e >> 4] >= 0;
+    }
+    floatx4 sc[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      sc[s] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kk = 0; kk < HD / 32; ++kk) {
+        const bf16x8 kf = *reinterpret_cast<const bf16x8*>(kb + ((koff ^ (kk << 6)) + 16 * s * ROWB));
+        sc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[kk], sc[s], 0, 0, 0);
+      }
+    }
+    const uint32_t held = (uint32_t)uniform((int)(uint32_t)__ballot(there));   // bit i: key key0 + i exists
+    const bool partial = uniform(held != 0xFFFFFFFFu || key0 + KT > minlim) != 0;
+    uint32_t top = 0;                             // the largest exponent of a value, in the high half
+    if (partial) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = 16 * (e >> 2) + 4 * g + (e & 3);
+        if (!((held >> i) & 1u) || key0 + i >= lim) sc[e >> 2][e & 3] = -INFINITY;
+      }
+      for (int q = 0; q < TILEB / 1024; ++q) {
+        const uint4 v = *reinterpret_cast<const uint4*>(vb + q * 1024 + lane * 16);
+        const uint32_t x[4] = {v.x & 0x7F807F80u, v.y & 0x7F807F80u, v.z & 0x7F807F80u, v.w & 0x7F807F80u};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = max(top, max(x[k], x[k] << 16));
+      }
+    }
+    float hi = sc[0][0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) hi = fmaxf(hi, sc[e >> 2][e & 3]);
+    const float tm = groups_max(hi) * w.c;
+    if (uniform(__any(tm > m + kRaise))) {
+      const float mn = tm > m + kRaise ? tm : m;
+      const float al = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      mb = mn == -INFINITY ? 0.0f : mn;
+      l *= al;
+#pragma unroll
+      for (int d = 0; d < HD / 16; ++d) o[d] *= al;
+    }
+    // weights, rounded to bf16 (the second product's operand type), and their sum
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[e >> 2][e & 3], w.c, -mb));
+    l += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+    const bf16x8 p = __builtin_bit_cast(bf16x8, make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                           pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
+    // in a tile some row does not see whole, a value that is not finite must not meet
+    // that row's zero weight
+    if (!uniform(__any(top >= 0x7F800000u))) {
+#pragma unroll
+      for (int d = 0; d < HD / 16; ++d) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(value_frag(vb, d).v, p, o[d], 0, 0, 0);
+    } else {
+      // key by key, added only to the rows that see it
+#pragma unroll 1
+      for (int k = 0; k < KT; ++k) {
+        if (!((held >> k) & 1u)) continue;
+        const int jj = (k & 3) | ((k >> 4) << 2);
+        const uint32_t half = jj & 1 ? 0xFFFF0000u : 0x0000FFFFu;
+        const uint32_t keep = g == ((k >> 2) & 3) ? half : 0u;
+#pragma unroll
+        for (int d = 0; d < HD / 16; ++d) {
+          const VFrag f = value_frag(vb, d);
+          const bf16x8 va = __builtin_bit_cast(
+              bf16x8, make_uint4(jj / 2 == 0 ? f.w[0] & keep : 0u, jj / 2 == 1 ? f.w[1] & keep : 0u,
+                                 jj / 2 == 2 ? f.w[2] & keep : 0u, jj / 2 == 3 ? f.w[3] & keep : 0u));
+          const floatx4 add = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, p, (floatx4{0.f, 0.f, 0.f, 0.f}), 0, 0, 0);
+          if (key0 + k < lim) o[d] += add;
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+  };
+
+  constexpr int wkeys = kSlots ? kWindow : kWindow * 16;
+  for (int win0 = k0; win0 < k1; win0 += wkeys) {
+    const int win1 = min(k1, win0 + wkeys);
+    __syncthreads();
+    const int entries = kSlots ? win1 - win0 : (win1 - win0 + 15) >> 4;
+    for (int e = threadIdx.x; e < entries; e += 64 * RT) {
+      const int key = win0 + (kSlots ? e : e << 4);
+      const int page = table[key >> a.page_shift];
+      slots[e] = page >= 0 && page < a.num_pages ? (page << a.page_shift) + (key & pmask) : -1;
+    }
+    __syncthreads();
+    issue(win0, win0, 0);
+    if (win0 + KT < win1) issue(win0 + KT, win0, 1);
+    int stage = 0;
+    for (int key0 = win0; key0 < win1; key0 += KT) {
+      // this wave's loads of the tile have landed; after the barrier everyone's have, and
+      // everyone is done with the tile before
+      if (uniform(key0 + KT < win1)) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LPW) : "memory");
+      else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      lds_barrier();
+      if (uniform(key0 + 2 * KT < win1)) issue(key0 + 2 * KT, win0, stage == 0 ? 2 : stage - 1);
+      if (!idle) work_on(smem + stage * 2 * TILEB, key0, win0);
+      stage = stage == 2 ? 0 : stage + 1;
+    }
+  }
+
+  l = groups_sum(l);
+  if (idle || !ok) return;
+  if (it.nsplit == 1) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const size_t at = (size_t)(it.q0 + j) * a.nh + h;
+#pragma unroll
+    for (int d = 0; d < HD / 16; ++d)
+      *reinterpret_cast<uint2*>(a.out + at * HD + 16 * d + 4 * g) =
+          l == 0.0f ? make_uint2(0u, 0u)
+                    : make_uint2(pack_bf16x2(o[d][0] * inv, o[d][1] * inv), pack_bf16x2(o[d][2] * inv, o[d][3] * inv));
+    if (a.lse && g == 0) a.lse[at] = row_lse(m, l);
+  } else {
+    const size_t at = ((size_t)it.pid * w.unit + rest) * (16 * RT) + 16 * wave + c;
+#pragma unroll
+    for (int d = 0; d < HD / 16; ++d) *reinterpret_cast<floatx4*>(w.part_o + at * HD + 16 * d + 4 * g) = o[d];
+    if (g == 0) {
+      w.part_ml[2 * at] = m;
+      w.part_ml[2 * at + 1] = l;
+    }
+  }
+}
+
+// The ranges of split requests, joined in their order.  A workgroup takes `step` rows of one
+// (request, row block, kv head); hd / 4 threads take a row, four dims each.  Up to kFew
+// ranges they do so alone, every row of the workgroup at once; of more ranges the
+// 256 / (hd / 4) groups take every so many each, row after row, and LDS joins the groups.
+constexpr int kFew = 16;
+
+struct Joined {
+  float m, l;
+  floatx4 acc;
+};
+
+// ranges first, first + hop, .. of row at0 (partials `stride` rows apart)
+__device__ __forceinline__ Joined join_ranges(const Work& w, size_t at0, size_t stride, int ns, int first, int hop, int hd, int d) {
+  Joined t{-INFINITY, 0.0f, floatx4{0.f, 0.f, 0.f, 0.f}};
+  for (int s0 = first; s0 < ns; s0 += 4 * hop) {
+    floatx2 ml[4];
+    floatx4 v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int s = s0 + q * hop;
+      const size_t at = at0 + (size_t)min(s, ns - 1) * stride;
+      ml[q] = *reinterpret_cast<const floatx2*>(w.part_ml + 2 * at);
+      v[q] = *reinterpret_cast<const floatx4*>(w.part_o + at * hd + 4 * d);
+      if (s >= ns) ml[q] = floatx2{-INFINITY, 0.0f};
+    }
+    float mn = t.m;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) mn = fmaxf(mn, ml[q][0]);
+    const float ms = mn == -INFINITY ? 0.0f : mn;
+    const float f0 = __builtin_amdgcn_exp2f(t.m - ms);
+    t.l *= f0;
+    t.acc *= f0;
+    t.m = mn;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float f = __builtin_amdgcn_exp2f(ml[q][0] - ms);
+      if (f != 0.0f) {                            // (a range behind the last has weight 0, whatever lies there)
+        t.l += ml[q][1] * f;
+        t.acc += v[q] * f;
+      }
+    }
+  }
+  return t;
+}
+
 template <int HD, int RT>
-__global__ __launch_bounds__(256) void paged_join(Work w) {
+__global__ __launch_bounds__(256) void paged_join(Work w, int step) {
   const PagedArgs& a = w.a;
   const int b = blockIdx.x / w.unit, rest = blockIdx.x % w.unit;
   const int kvh = rest % a.nkv, rb = rest / a.nkv;
   int q0, n, kv;
   request(a, b, q0, n, kv);
-  const int rows = min(16 * RT, min(n, a.max_q) * w.G - rb * 16 * RT);
-  if (rows <= 0) return;
+  const int rows = min(16 * RT, min(n, a.max_q) * w.G - rb * 16 * RT), first = blockIdx.y * step;
+  if (first >= rows) return;
   const int2 rq = w.req[b];
-  const int ns = min(rq.y, w.pid_cap - rq.x);
   if (rq.y <= 1) return;
-  constexpr int TPR = HD / 4;
-  const int d = 4 * (threadIdx.x % TPR);
-  for (int r = threadIdx.x / TPR; r < rows; r += 256 / TPR) {
-    const size_t at0 = ((size_t)rq.x * w.unit + rest) * (16 * RT) + r, step = (size_t)w.unit * (16 * RT);
-    float mm = -INFINITY;
-    for (int s = 0; s < ns; ++s) mm = fmaxf(mm, w.part_ml[2 * (at0 + s * step)]);
-    const float ms = mm == -INFINITY ? 0.0f : mm;
-    float ll = 0.0f;
-    floatx4 acc = floatx4{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < ns; ++s) {
-      const float* ml = w.part_ml + 2 * (at0 + s * step);
-      const float f = __builtin_amdgcn_exp2f(ml[0] - ms);
-      ll += ml[1] * f;
-      acc += *reinterpret_cast<const floatx4*>(w.part_o + (at0 + s * step) * HD + d) * f;
-    }
+  const int ns = min(rq.y, w.pid_cap - rq.x), last = min(rows, first + step);
+  constexpr int TPR = HD / 4, GR = 256 / TPR;
+  __shared__ floatx4 part[GR][TPR];
+  __shared__ float gm[GR], gl[GR];
+  const int d = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  const size_t stride = (size_t)w.unit * (16 * RT), base = ((size_t)rq.x * w.unit + rest) * (16 * RT);
+  auto finish = [&](int r, const Joined& t) {
     const int R = rb * 16 * RT + r;
     const size_t at = (size_t)(q0 + R / w.G) * a.nh + kvh * w.G + R % w.G;
-    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+    const float inv = t.l == 0.0f ? 0.0f : 1.0f / t.l;
     uint2 pk = make_uint2(0u, 0u);
-    if (ll != 0.0f) pk = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-    *reinterpret_cast<uint2*>(a.out + at * HD + d) = pk;
-    if (a.lse && d == 0) a.lse[at] = row_lse(mm, ll);
+    if (t.l != 0.0f) pk = make_uint2(pack_bf16x2(t.acc[0] * inv, t.acc[1] * inv), pack_bf16x2(t.acc[2] * inv, t.acc[3] * inv));
+    *reinterpret_cast<uint2*>(a.out + at * HD + 4 * d) = pk;
+    if (a.lse && d == 0) a.lse[at] = row_lse(t.m, t.l);
+  };
+  if (ns <= kFew) {
+    for (int r = first + grp; r < last; r += GR) finish(r, join_ranges(w, base + r, stride, ns, 0, 1, HD, d));
+    return;
+  }
+  for (int r = first; r < last; ++r) {
+    Joined t = join_ranges(w, base + r, stride, ns, grp, GR, HD, d);
+    __syncthreads();
+    part[grp][d] = t.acc;
+    if (d == 0) {
+      gm[grp] = t.m;
+      gl[grp] = t.l;
+    }
+    __syncthreads();
+    if (grp == 0) {
+      t.m = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < GR; ++q) t.m = fmaxf(t.m, gm[q]);
+      const float ms = t.m == -INFINITY ? 0.0f : t.m;
+      t.l = 0.0f;
+      t.acc = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < GR; ++q) {
+        const float f = __builtin_amdgcn_exp2f(gm[q] - ms);
+        t.l += gl[q] * f;
+        t.acc += part[q][d] * f;
+      }
+      finish(r, t);
+    }
   }
 }
 
 struct Shape {
-  int RT, RB, G, unit, pid_cap;
+  int RT, RB, G, unit, target, pid_cap;
   size_t off_o, off_ml, off_req, bytes;
 };
 
@@ -487,13 +806,16 @@ Shape shape_of(int B, int max_q, int nh, int nkv, int hd) {
   Shape s;
   s.G = nh / nkv;
   const int rows = max_q * s.G;
-  const int most = hd > 128 ? 2 : 4;
-  s.RT = rows <= 16 ? 1 : rows <= 32 || most == 2 ? 2 : 4;
+  s.RT = rows <= 64 ? (rows + 15) / 16 : 8;
   s.RB = (rows + 16 * s.RT - 1) / (16 * s.RT);
   s.unit = nkv * s.RB;
+  // Items aimed at: whole rounds of the workgroups that fit the card at once (`slots`), less
+  // the half range that every request adds on average.
+  const int slots = kCus * (s.RT == 1 || s.RT == 8 || hd > 128 ? 2 : 3), pairs = B * s.unit;
+  s.target = std::max(slots / 2, (pairs / slots + 1) * slots - pairs / 2);
   // a split request has more keys than a range, so its ranges are fewer than twice its
-  // keys over the range's length, and all of them together at most 2 kTarget / unit
-  s.pid_cap = 2 * (kTarget / s.unit + 1) + 1;
+  // keys over the range's length, and all of them together at most 2 target / unit
+  s.pid_cap = 2 * (s.target / s.unit + 1) + 1;
   s.off_req = 0;
   s.off_ml = al((size_t)B * sizeof(int2));
   s.off_o = s.off_ml + al((size_t)s.pid_cap * s.unit * 16 * s.RT * 2 * sizeof(float));
@@ -501,16 +823,33 @@ Shape shape_of(int B, int max_q, int nh, int nkv, int hd) {
   return s;
 }
 
+template <int HD, int RT, bool kSlots>
+hipError_t launch_rows(const Work& w, int grid, hipStream_t stream) {
+#ifndef STREAM_FROM
+#define STREAM_FROM 2
+#endif
+  if constexpr (RT >= STREAM_FROM) {
+    constexpr int lds = shared_lds<HD>();
+    if (lds > 64 * 1024) {
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&paged_shared<HD, RT, kSlots>),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+      if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((paged_shared<HD, RT, kSlots>), dim3(grid), dim3(64 * RT), lds, stream, w);
+  } else {
+    hipLaunchKernelGGL((paged_rows<HD, RT, kSlots>), dim3(grid), dim3(64 * NW), 0, stream, w);
+  }
+  return hipGetLastError();
+}
+
 template <int HD, int RT>
 hipError_t launch(const Work& w, int64_t items, int max_kv, hipStream_t stream) {
   const int grid = (int)items;
-  if (w.a.page_shift < 4)
-    hipLaunchKernelGGL((paged_rows<HD, RT, true>), dim3(grid), dim3(64 * NW), 0, stream, w);
-  else
-    hipLaunchKernelGGL((paged_rows<HD, RT, false>), dim3(grid), dim3(64 * NW), 0, stream, w);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = w.a.page_shift < 4 ? launch_rows<HD, RT, true>(w, grid, stream) : launch_rows<HD, RT, false>(w, grid, stream);
   if (e != hipSuccess || max_kv <= kMinChunk) return e;
-  hipLaunchKernelGGL((paged_join<HD, RT>), dim3(w.a.B * w.unit), dim3(256), 0, stream, w);
+  const int rows = std::min(16 * RT, w.a.max_q * w.G);
+  const int step = std::max(1, std::min(rows, (int)((int64_t)w.a.B * w.unit * rows / kJoinGroups)));
+  hipLaunchKernelGGL((paged_join<HD, RT>), dim3(w.a.B * w.unit, (rows + step - 1) / step), dim3(256), 0, stream, w, step);
   return hipGetLastError();
 }
 
@@ -519,9 +858,9 @@ hipError_t launch_rt(const Work& w, int RT, int64_t items, int max_kv, hipStream
   switch (RT) {
     case 1: return launch<HD, 1>(w, items, max_kv, stream);
     case 2: return launch<HD, 2>(w, items, max_kv, stream);
-    default:
-      if constexpr (HD <= 128) return launch<HD, 4>(w, items, max_kv, stream);
-      return hipErrorInvalidValue;
+    case 3: return launch<HD, 3>(w, items, max_kv, stream);
+    case 4: return launch<HD, 4>(w, items, max_kv, stream);
+    default: return launch<HD, 8>(w, items, max_kv, stream);
   }
 }
 
@@ -539,6 +878,7 @@ hipError_t launch_paged_attention(const PagedArgs& a, int hd, void* workspace, h
   w.G = s.G;
   w.RB = s.RB;
   w.unit = s.unit;
+  w.target = s.target;
   w.pid_cap = s.pid_cap;
   w.c = a.scale * kLog2e;
   char* base = static_cast<char*>(workspace);
@@ -548,7 +888,7 @@ hipError_t launch_paged_attention(const PagedArgs& a, int hd, void* workspace, h
   // at most one range per request, plus the ones the balancing adds
   const int max_kv = a.width << a.page_shift;
   const int64_t most = (int64_t)a.B * s.unit * std::max(1, (max_kv + kMinChunk - 1) / kMinChunk);
-  const int64_t items = std::min(most, (int64_t)a.B * s.unit + kTarget + s.unit);
+  const int64_t items = std::min(most, (int64_t)a.B * s.unit + s.target + s.unit);
   switch (hd) {
     case 64: return launch_rt<64>(w, s.RT, items, max_kv, stream);
     case 128: return launch_rt<128>(w, s.RT, items, max_kv, stream);
