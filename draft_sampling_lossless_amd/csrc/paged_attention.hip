@@ -6,21 +6,25 @@
 // query heads that share a kv head, times the request's query tokens, are the rows of one
 // product, so a key or value is read from memory once per kv head (row blocks of 16 RT).
 //
-// Each wave takes tiles of 32 keys, all by itself in registers (no LDS in the loop: no
-// other wave needs its keys).  Scores are formed transposed, S^T = K Q^T, with
-// v_mfma_f32_16x16x32_bf16: lane (g, c) = (lane / 16, lane % 16) then holds row c and the
-// keys 16 s + 4 g + i (s = 0, 1; i = 0..3).  The second product O^T = V^T P^T may take its
-// 32 keys in any order as long as both operands agree, so those eight scores, rounded to
-// bf16, are its B operand as they stand.  Its A operand needs eight keys of one dim per
-// lane: a lane loads 8 consecutive dims of its eight keys (16 lanes cover a row, 16 bytes
-// each) and transposes the 8 x 8 block with byte permutes; product t then covers the
-// dims 8 c + t.
+// Scores are formed transposed, S^T = K Q^T, with v_mfma_f32_16x16x32_bf16 over tiles of 32
+// keys: lane (g, c) = (lane / 16, lane % 16) then holds row c and the keys 16 s + 4 g + i
+// (s = 0, 1; i = 0..3).  The second product O^T = V^T P^T may take its 32 keys in any order
+// as long as both operands agree, so those eight scores, rounded to bf16, are its B operand
+// as they stand.
 //
-// Work items (request, range of its keys, row block, kv head) come from the lengths on
-// the device: ranges are all of one length, chosen so that all items together are about
-// `target`, and a request shorter than that is one item, written straight to the output.
-// The others leave a maximum, a sum and an unnormalised row each, joined by
-// paged_join in the order of the ranges.
+// Up to 16 rows (paged_rows): memory-bound, one product hardly fills a matrix instruction.
+// Each of a workgroup's four waves takes tiles of its own straight into registers; V's
+// operand (eight keys of one dim per lane) comes from loads of 8 consecutive dims of eight
+// keys (16 lanes cover a row, 16 bytes each), transposed by byte permutes, product t then
+// covering the dims 8 c + t.  The waves are joined through LDS at the end.  256 requests of
+// one token over 2048 keys, 32/8 heads of 128: 380 us, 5.7 TB/s.
+// More rows (paged_shared): below.
+//
+// Work items (request, range of its keys) times (row block, kv head) come from the lengths
+// on the device: ranges are cut equal and listed by falling length (paged_plan), each
+// workgroup takes one.  A request of one range is written straight to the output; the
+// others leave a maximum, a sum and an unnormalised row each, joined by paged_join in the
+// order of the ranges.
 #include <algorithm>
 
 #include "attention.hpp"
@@ -37,23 +41,31 @@ constexpr float kRaise = 8.0f;
 
 constexpr int NW = 4;          // waves per workgroup; they take tiles in turn
 constexpr int KT = 32;         // keys per tile
-constexpr int kMinChunk = 512; // keys of a range, at least
+constexpr int kStep = KT * NW; // ranges are whole numbers of these
 constexpr int kCus = 256;      // compute units of the card
 constexpr int kJoinGroups = 2048;   // workgroups of the joining pass aimed at
+
+// a range of one request's keys: the work of a workgroup for every (row block, kv head)
+struct __attribute__((aligned(16))) Item {
+  int b, k0, k1;       // request, its keys k0 .. k1 - 1
+  int pid;             // partial to leave, or -1: the request's only range
+  int q0, n, kv;       // the request's first query token, their number, its keys
+  int pad;
+};
 
 struct Work {
   PagedArgs a;
   int G, RB, unit;     // heads per kv head, row blocks, nkv * RB
   int target;          // items aimed at
+  int min_chunk;       // keys of a range, at least
+  int whole;           // no request is cut where none can be longer than this
   int pid_cap;         // ranges the workspace has room for
   float c;             // scale * log2 e
   float* part_o;       // [pid_cap, unit, 16 RT, hd]
   float* part_ml;      // [pid_cap, unit, 16 RT, 2]
-  int2* req;           // [B]: first range and number of ranges of a split request
-};
-
-struct Item {
-  int b, q0, n, kv, split, nsplit, pid, chunk;
+  int2* req;           // [B]: first partial and number of ranges of a split request (one: not split)
+  Item* plan;          // the items, dearest first, or null: one request, or none is ever cut
+  int* count;          // how many of them
 };
 
 // n counts all of the request's query tokens; the first max_q of them are computed
@@ -63,69 +75,136 @@ __device__ __forceinline__ void request(const PagedArgs& a, int b, int& q0, int&
   kv = clampi(a.kv_len[b], 0, a.width << a.page_shift);
 }
 
-__device__ __forceinline__ int wave_incl_scan(int v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(v, o);
-    if (lane >= o) v += u;
-  }
-  return v;
+// Ranges of all requests are at most `chunk` keys; a longer request is cut into equal ones.
+__device__ __forceinline__ int chunk_of(const Work& w, int64_t total) {
+  const int64_t per = (total * w.unit + w.target - 1) / w.target;
+  const int64_t up = (per + kStep - 1) / kStep * kStep;
+  return (int)(up < w.min_chunk ? w.min_chunk : up > (1 << 30) ? (1 << 30) : up);
+}
+__device__ __forceinline__ int range_len(int kv, int ranges) {
+  return ((kv + ranges - 1) / ranges + kStep - 1) / kStep * kStep;
 }
 
-// the u-th (request, range) of the call; every wave finds it for itself
-__device__ bool find_item(const Work& w, int u, Item& it) {
+// the u-th item of the call
+__device__ __forceinline__ bool find_item(const Work& w, int u, Item& it) {
   const PagedArgs& a = w.a;
-  const int lane = threadIdx.x & 63;
-  const int step = KT * NW;
-  if (a.B == 1) {
+  if (w.plan) {
+    if (u >= *w.count) return false;
+    it = w.plan[u];
+  } else if (a.B == 1 && (a.width << a.page_shift) > w.whole) {
     request(a, 0, it.q0, it.n, it.kv);
-    if (it.n == 0) return false;
-    const int64_t per = ((int64_t)it.kv * w.unit + w.target - 1) / w.target;
-    it.chunk = max(kMinChunk, (int)((per + step - 1) / step * step));
+    const int chunk = chunk_of(w, it.kv);
+    const int len = range_len(it.kv, max(1, (it.kv + chunk - 1) / chunk));
+    const int ranges = len > 0 ? (it.kv + len - 1) / len : 1;
+    if (u >= ranges || it.n == 0) return false;
     it.b = 0;
-    it.nsplit = max(1, (it.kv + it.chunk - 1) / it.chunk);
-    it.split = u;
-    it.pid = u;
-    return u < it.nsplit;
+    it.k0 = u * len;
+    it.k1 = min(it.kv, it.k0 + len);
+    it.pid = ranges > 1 ? u : -1;
+    if (u == 0 && threadIdx.x == 0) w.req[0] = make_int2(0, ranges);
+  } else {
+    request(a, u, it.q0, it.n, it.kv);
+    if (it.n == 0) return false;
+    it.b = u;
+    it.k0 = 0;
+    it.k1 = it.kv;
+    it.pid = -1;
   }
-  int q0, n, kv;
+  it.b = uniform(it.b);
+  it.k0 = uniform(it.k0);
+  it.k1 = uniform(it.k1);
+  it.pid = uniform(it.pid);
+  it.q0 = uniform(it.q0);
+  it.n = uniform(it.n);
+  it.kv = uniform(it.kv);
+  return true;
+}
+
+// The plan of a call with several requests: one workgroup cuts the requests into ranges
+// and lists them by falling length (to a 256th of the longest), so that the dearest start
+// first.  The order among equals is that of the atomics and decides nothing but time: a
+// range's place among the partials comes from the order of the requests.
+constexpr int kPlanThreads = 1024, kPlanEach = (4096 + kPlanThreads - 1) / kPlanThreads;
+
+__global__ __launch_bounds__(kPlanThreads) void paged_plan(Work w) {
+  const PagedArgs& a = w.a;
+  __shared__ int64_t sums[kPlanThreads / 64];
+  __shared__ int offs[kPlanThreads / 64], bins[256], cursor[256];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int q0[kPlanEach], n[kPlanEach], kv[kPlanEach], ranges[kPlanEach], len[kPlanEach];
   int64_t total = 0;
-  for (int base = 0; base < a.B; base += 64) {
-    if (base + lane < a.B) {
-      request(a, base + lane, q0, n, kv);
-      if (n > 0) total += kv;
-    }
+#pragma unroll
+  for (int e = 0; e < kPlanEach; ++e) {
+    const int b = tid * kPlanEach + e;
+    q0[e] = n[e] = kv[e] = 0;
+    if (b < a.B) request(a, b, q0[e], n[e], kv[e]);
+    if (n[e] > 0) total += kv[e];
   }
   for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o);
-  const int64_t per = (total * w.unit + w.target - 1) / w.target;
-  const int64_t up = (per + step - 1) / step * step;
-  it.chunk = (int)(up < kMinChunk ? kMinChunk : up > (1 << 30) ? (1 << 30) : up);
-  int before = 0, pids = 0;
-  for (int base = 0; base < a.B; base += 64) {
-    int cnt = 0;
-    q0 = n = kv = 0;
-    if (base + lane < a.B) {
-      request(a, base + lane, q0, n, kv);
-      if (n > 0) cnt = max(1, (kv + it.chunk - 1) / it.chunk);
+  if (lane == 0) sums[wave] = total;
+  if (tid < 256) bins[tid] = 0;
+  __syncthreads();
+  total = 0;
+  for (int v = 0; v < kPlanThreads / 64; ++v) total += sums[v];
+  const int chunk = chunk_of(w, total);
+  auto bin = [&](int keys) { return 255 - min(255, (int)((int64_t)keys * 256 / (chunk + 1))); };
+  int split = 0;                                  // ranges of this thread's split requests
+#pragma unroll
+  for (int e = 0; e < kPlanEach; ++e) {
+    ranges[e] = 0;
+    if (n[e] > 0) {
+      len[e] = range_len(kv[e], max(1, (kv[e] + chunk - 1) / chunk));
+      ranges[e] = len[e] > 0 ? (kv[e] + len[e] - 1) / len[e] : 1;
+      if (ranges[e] > 1) {
+        split += ranges[e];
+        atomicAdd(&bins[bin(len[e])], ranges[e] - 1);
+      }
+      atomicAdd(&bins[bin(kv[e] - (ranges[e] - 1) * len[e])], 1);
     }
-    const int split_cnt = cnt > 1 ? cnt : 0;
-    const int inc = wave_incl_scan(cnt, lane), pinc = wave_incl_scan(split_cnt, lane);
-    const uint64_t hit = __ballot(before + inc > u);
-    if (hit) {
-      const int s = __builtin_ctzll(hit);
-      it.b = __builtin_amdgcn_readfirstlane(base + s);
-      it.q0 = __builtin_amdgcn_readlane(q0, s);
-      it.n = __builtin_amdgcn_readlane(n, s);
-      it.kv = __builtin_amdgcn_readlane(kv, s);
-      it.nsplit = __builtin_amdgcn_readlane(cnt, s);
-      it.split = u - before - (__builtin_amdgcn_readlane(inc, s) - it.nsplit);
-      it.pid = pids + __builtin_amdgcn_readlane(pinc, s) - __builtin_amdgcn_readlane(split_cnt, s) + it.split;
-      return true;
-    }
-    before += __builtin_amdgcn_readlane(inc, 63);
-    pids += __builtin_amdgcn_readlane(pinc, 63);
   }
-  return false;
+  int before = split;                             // inclusive scan over the workgroup
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(before, o);
+    if (lane >= o) before += v;
+  }
+  if (lane == 63) offs[wave] = before;
+  __syncthreads();
+  for (int v = 0; v < wave; ++v) before += offs[v];
+  if (wave == 0) {                                // where each length's items begin
+    int c[4], sum = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum += c[e] = bins[4 * lane + e];
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(inc, o);
+      if (lane >= o) inc += v;
+    }
+    int at = inc - sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      cursor[4 * lane + e] = at;
+      at += c[e];
+    }
+    if (lane == 63) *w.count = inc;
+  }
+  __syncthreads();
+  int pid = before - split;
+#pragma unroll
+  for (int e = 0; e < kPlanEach; ++e) {
+    if (n[e] == 0) continue;
+    const int b = tid * kPlanEach + e, full = ranges[e] - 1;
+    w.req[b] = make_int2(pid, ranges[e]);
+    if (full > 0) {
+      const int at = atomicAdd(&cursor[bin(len[e])], full);
+      for (int r = 0; r < full; ++r)
+        w.plan[at + r] = Item{b, r * len[e], (r + 1) * len[e], pid + r, q0[e], n[e], kv[e], 0};
+    }
+    const int at = atomicAdd(&cursor[bin(kv[e] - full * len[e])], 1);
+    w.plan[at] = Item{b, full * len[e], kv[e], full > 0 ? pid + full : -1, q0[e], n[e], kv[e], 0};
+    if (full > 0) pid += ranges[e];
+  }
 }
 
 // max / sum over the four lane groups that share a row
@@ -153,7 +232,7 @@ struct Dims {
 
 // kSlots: pages smaller than 16, so the slot of every key is looked up by a lane of its
 // own; otherwise 16 aligned keys lie in one page and the wave looks up two
-template <int HD, int RT, bool kSlots>
+template <int HD, bool kSlots>
 __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
   using D = Dims<HD>;
   constexpr int ODIM = 16 * D::VD;                // dims of one group
@@ -161,285 +240,223 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
   __shared__ float obuf[NW][16][ODIM + 4];
   __shared__ float mbuf[NW][16], lbuf[NW][16];
 
-  const int u = blockIdx.x / w.unit, rest = blockIdx.x % w.unit;
-  const int kvh = rest % a.nkv, rb = rest / a.nkv;
+  const int u = blockIdx.x / w.unit, kvh = blockIdx.x % w.unit;
   Item it;
   if (!find_item(w, u, it)) return;
-  it.b = uniform(it.b);
-  it.q0 = uniform(it.q0);
-  it.n = uniform(it.n);
-  it.kv = uniform(it.kv);
-  it.chunk = uniform(it.chunk);
-  it.split = uniform(it.split);
-  it.nsplit = uniform(it.nsplit);
-  it.pid = uniform(it.pid);
-  if (rest == 0 && it.split == 0 && threadIdx.x == 0)
-    w.req[it.b] = make_int2(it.pid, it.nsplit);
+  if (it.pid >= w.pid_cap) return;                // (the workspace holds every range)
   const int nq = min(it.n, a.max_q);
-  const int rows = nq * w.G - rb * 16 * RT;       // rows of this block, possibly none
-  if (rows <= 0) return;
-  if (it.nsplit > 1 && it.pid >= w.pid_cap) return;   // (the workspace holds every range)
 
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = uniform(threadIdx.x >> 6);
 
-  // queries: the B operand of S^T, row 16 rt + c, dims 32 kk + 8 g ..
-  bf16x8 qf[RT][HD / 32];
-  int lim[RT];                                    // keys below lim are seen
-  int minlim = it.kv;
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int r = rb * 16 * RT + 16 * rt + c;
-    const int j = r / w.G, h = kvh * w.G + r % w.G;
-    const bool ok = j < nq;
-    lim[rt] = ok && a.causal ? it.kv - it.n + j + 1 : it.kv;
-    const uint16_t* src = a.q + (size_t)(it.q0 + (ok ? j : 0)) * a.q_stride + (size_t)(ok ? h : 0) * HD;
+  // queries: the B operand of S^T, row c, dims 32 kk + 8 g ..
+  const int qj = c / w.G;
+  const bool ok = qj < nq;
+  const int lim = ok && a.causal ? it.kv - it.n + qj + 1 : it.kv;   // keys below lim are seen
+  const int minlim = a.causal ? it.kv - it.n + 1 : it.kv;
+  bf16x8 qf[HD / 32];
+  {
+    const uint16_t* src = a.q + (size_t)(it.q0 + (ok ? qj : 0)) * a.q_stride + (size_t)(ok ? kvh * w.G + c % w.G : 0) * HD;
 #pragma unroll
     for (int kk = 0; kk < HD / 32; ++kk) {
       const uint4 v = *reinterpret_cast<const uint4*>(src + 32 * kk + 8 * g);
-      qf[rt][kk] = __builtin_bit_cast(bf16x8, ok ? v : make_uint4(0, 0, 0, 0));
+      qf[kk] = __builtin_bit_cast(bf16x8, ok ? v : make_uint4(0, 0, 0, 0));
     }
   }
-  if (a.causal) minlim = it.kv - it.n + 1 + (rb * 16 * RT) / w.G;
 
-  floatx4 o[RT][D::VU][D::VD];
-  float m[RT], l[RT];
+  floatx4 o[D::VU][D::VD];
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    m[rt] = -INFINITY;
-    l[rt] = 0.0f;
+  for (int x = 0; x < D::VU; ++x)
 #pragma unroll
-    for (int x = 0; x < D::VU; ++x)
-#pragma unroll
-      for (int t = 0; t < D::VD; ++t) o[rt][x][t] = floatx4{0.f, 0.f, 0.f, 0.f};
-  }
+    for (int t = 0; t < D::VD; ++t) o[x][t] = floatx4{0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, mb = 0.0f, l = 0.0f;       // mb: m, or 0 while the row has seen nothing
 
-  const int k0 = it.split * it.chunk, k1 = min(it.kv, k0 + it.chunk);
   const int32_t* table = a.page_table + (size_t)it.b * a.width;
   const int rstride = a.nkv * HD;                 // elements between slots
   const int pmask = (1 << a.page_shift) - 1;
 
-  for (int key0 = k0 + KT * wave; key0 < k1; key0 += KT * NW) {
+  for (int key0 = it.k0 + KT * wave; key0 < it.k1; key0 += KT * NW) {
     // the tile's keys and values; a key that does not exist reads an existing row
     uint32_t held;                                // bit i: key key0 + i exists
     uint32_t kf[2][HD / 32][4], vf[D::VU][8][D::VW];
+    auto key_row = [&](int s, const uint16_t* src) {
+#pragma unroll
+      for (int kk = 0; kk < HD / 32; ++kk)
+        *reinterpret_cast<uint4*>(kf[s][kk]) = *reinterpret_cast<const uint4*>(src + 32 * kk + 8 * g);
+    };
+    auto value_row = [&](int j, const uint16_t* src) {
+#pragma unroll
+      for (int x = 0; x < D::VU; ++x)
+        if constexpr (D::VD == 8)
+          *reinterpret_cast<uint4*>(vf[x][j]) = *reinterpret_cast<const uint4*>(src + ODIM * x + 8 * c);
+        else
+          *reinterpret_cast<uint2*>(vf[x][j]) = *reinterpret_cast<const uint2*>(src + ODIM * x + 4 * c);
+    };
     if constexpr (kSlots) {
       const int key = min(key0 + (lane & 31), it.kv - 1);
       const int page = table[key >> a.page_shift];
-      const bool ok = key0 + (lane & 31) < it.kv && page >= 0 && page < a.num_pages;
-      const int slot = (page >= 0 && page < a.num_pages ? page << a.page_shift : 0) + (key & pmask);
-      held = (uint32_t)__ballot(ok);
+      const bool there = page >= 0 && page < a.num_pages;
+      const int slot = (there ? page << a.page_shift : 0) + (key & pmask);
+      held = (uint32_t)__ballot(there && key0 + (lane & 31) < it.kv);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint16_t* src = a.k_cache + ((size_t)__shfl(slot, 16 * s + c) * rstride + kvh * HD);
+      for (int s = 0; s < 2; ++s) key_row(s, a.k_cache + ((size_t)__shfl(slot, 16 * s + c) * rstride + kvh * HD));
 #pragma unroll
-        for (int kk = 0; kk < HD / 32; ++kk)
-          *reinterpret_cast<uint4*>(kf[s][kk]) = *reinterpret_cast<const uint4*>(src + 32 * kk + 8 * g);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint16_t* src = a.v_cache + ((size_t)__shfl(slot, 16 * (j >> 2) + 4 * g + (j & 3)) * rstride + kvh * HD);
-#pragma unroll
-        for (int x = 0; x < D::VU; ++x)
-          if constexpr (D::VD == 8)
-            *reinterpret_cast<uint4*>(vf[x][j]) = *reinterpret_cast<const uint4*>(src + ODIM * x + 8 * c);
-          else
-            *reinterpret_cast<uint2*>(vf[x][j]) = *reinterpret_cast<const uint2*>(src + ODIM * x + 4 * c);
-      }
+      for (int j = 0; j < 8; ++j)
+        value_row(j, a.v_cache + ((size_t)__shfl(slot, 16 * (j >> 2) + 4 * g + (j & 3)) * rstride + kvh * HD));
     } else {
       held = 0;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int ks = key0 + 16 * s;
-        int cnt = min(16, it.kv - ks);            // keys of this half, possibly <= 0
         int page = uniform(table[min(ks, it.kv - 1) >> a.page_shift]);
-        if (page < 0 || page >= a.num_pages) {
-          page = 0;
-          cnt = 0;
-        }
-        cnt = max(cnt, 0);
+        int cnt = clampi(it.kv - ks, 0, 16);      // keys of this half
+        if (page < 0 || page >= a.num_pages) page = cnt = 0;
         held |= ((1u << cnt) - 1u) << (16 * s);
-        const size_t slot = ((size_t)page << a.page_shift) + (ks & pmask);
-        const uint16_t* kb = a.k_cache + (slot * rstride + kvh * HD);
-        const uint16_t* vb = a.v_cache + (slot * rstride + kvh * HD);
+        const size_t at = (((size_t)page << a.page_shift) + (ks & pmask)) * rstride + kvh * HD;
         const int last = max(cnt - 1, 0);
-        const uint16_t* src = kb + min(c, last) * rstride;
+        key_row(s, a.k_cache + at + min(c, last) * rstride);
 #pragma unroll
-        for (int kk = 0; kk < HD / 32; ++kk)
-          *reinterpret_cast<uint4*>(kf[s][kk]) = *reinterpret_cast<const uint4*>(src + 32 * kk + 8 * g);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint16_t* vs = vb + min(4 * g + j, last) * rstride;
-#pragma unroll
-          for (int x = 0; x < D::VU; ++x)
-            if constexpr (D::VD == 8)
-              *reinterpret_cast<uint4*>(vf[x][4 * s + j]) = *reinterpret_cast<const uint4*>(vs + ODIM * x + 8 * c);
-            else
-              *reinterpret_cast<uint2*>(vf[x][4 * s + j]) = *reinterpret_cast<const uint2*>(vs + ODIM * x + 4 * c);
-        }
+        for (int j = 0; j < 4; ++j) value_row(4 * s + j, a.v_cache + at + min(4 * g + j, last) * rstride);
       }
     }
     held = (uint32_t)uniform((int)held);
     const bool partial = uniform(held != 0xFFFFFFFFu || key0 + KT > minlim) != 0;
 
     // scores, and from them the weights: registers only
-    bf16x8 p[RT];
+    floatx4 sc[2];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      if (16 * rt >= rows) break;
-      floatx4 sc[2];
+    for (int s = 0; s < 2; ++s) {
+      sc[s] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        sc[s] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kk = 0; kk < HD / 32; ++kk)
-          sc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8, *reinterpret_cast<uint4*>(kf[s][kk])), qf[rt][kk], sc[s], 0, 0, 0);
-      }
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = sc[e >> 2][e & 3] * w.c;
-      if (partial) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int i = 16 * (e >> 2) + 4 * g + (e & 3);
-          if (!((held >> i) & 1u) || key0 + i >= lim[rt]) x[e] = -INFINITY;
-        }
-      }
-      float tm = x[0];
-#pragma unroll
-      for (int e = 1; e < 8; ++e) tm = fmaxf(tm, x[e]);
-      tm = groups_max(tm);
-      const float mn = fmaxf(m[rt], tm);
-      const float ms = mn == -INFINITY ? 0.0f : mn;   // a row that has seen nothing yet
-      const float al = __builtin_amdgcn_exp2f(m[rt] - ms);
-      m[rt] = mn;
-      float sum = 0.0f;
+      for (int kk = 0; kk < HD / 32; ++kk)
+        sc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, *reinterpret_cast<uint4*>(kf[s][kk])), qf[kk], sc[s], 0, 0, 0);
+    }
+    uint32_t top = 0;                             // the largest exponent of a value, in the high half
+    if (partial) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[e] = __builtin_amdgcn_exp2f(x[e] - ms);
-        sum += x[e];
+        const int i = 16 * (e >> 2) + 4 * g + (e & 3);
+        if (!((held >> i) & 1u) || key0 + i >= lim) sc[e >> 2][e & 3] = -INFINITY;
       }
-      l[rt] = l[rt] * al + sum;
-      // the weights' rounding to bf16, the second product's operand type
-      p[rt] = __builtin_bit_cast(bf16x8, make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                    pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
-      if (__any(al != 1.0f)) {
-#pragma unroll
-        for (int y = 0; y < D::VU; ++y)
-#pragma unroll
-          for (int t = 0; t < D::VD; ++t) o[rt][y][t] *= al;
-      }
-    }
-
-    // in a tile some row does not see whole, a value that is not finite must not meet
-    // that row's zero weight
-    int odd = 0;
-    if (partial) {
-      bool any = false;
 #pragma unroll
       for (int y = 0; y < D::VU; ++y)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
-          for (int d = 0; d < D::VW; ++d) any |= bf16x2_nonfinite(vf[y][j][d]);
-      odd = __any(any);
+          for (int d = 0; d < D::VW; ++d) {
+            const uint32_t e = vf[y][j][d] & 0x7F807F80u;
+            top = max(top, max(e, e << 16));
+          }
     }
-    odd = uniform(odd);
+    float hi = sc[0][0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) hi = fmaxf(hi, sc[e >> 2][e & 3]);
+    const float tm = groups_max(hi) * w.c;
+    if (uniform(__any(tm > m + kRaise))) {
+      const float mn = tm > m + kRaise ? tm : m;
+      const float al = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      mb = mn == -INFINITY ? 0.0f : mn;
+      l *= al;
+#pragma unroll
+      for (int y = 0; y < D::VU; ++y)
+#pragma unroll
+        for (int t = 0; t < D::VD; ++t) o[y][t] *= al;
+    }
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[e >> 2][e & 3], w.c, -mb));
+    l += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+    // the weights' rounding to bf16, the second product's operand type
+    const bf16x8 p = __builtin_bit_cast(bf16x8, make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                           pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
+
+    // in a tile some row does not see whole, a value that is not finite must not meet
+    // that row's zero weight
+    const int odd = uniform(__any(top >= 0x7F800000u));
 #pragma unroll
     for (int y = 0; y < D::VU; ++y) {
 #pragma unroll
       for (int t = 0; t < D::VD; ++t) {
-        const uint32_t sel = t & 1 ? 0x07060302u : 0x05040100u;
         uint32_t vt[4];
 #pragma unroll
         for (int d = 0; d < 4; ++d)
-          vt[d] = __builtin_amdgcn_perm(vf[y][2 * d + 1][t >> 1], vf[y][2 * d][t >> 1], sel);
+          vt[d] = __builtin_amdgcn_perm(vf[y][2 * d + 1][t >> 1], vf[y][2 * d][t >> 1], t & 1 ? 0x07060302u : 0x05040100u);
         if (!odd) {
-          const bf16x8 va = __builtin_bit_cast(bf16x8, make_uint4(vt[0], vt[1], vt[2], vt[3]));
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-            if (16 * rt < rows) o[rt][y][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, p[rt], o[rt][y][t], 0, 0, 0);
+          o[y][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, make_uint4(vt[0], vt[1], vt[2], vt[3])), p, o[y][t], 0, 0, 0);
         } else {
           // key by key, added only to the rows that see it
+#pragma unroll 1
           for (int k = 0; k < KT; ++k) {
             if (!((held >> k) & 1u)) continue;
             const int j = (k & 3) | ((k >> 4) << 2);
-            const uint32_t half = j & 1 ? 0xFFFF0000u : 0x0000FFFFu;
-            const bool mine = g == ((k >> 2) & 3);
+            const uint32_t keep = g == ((k >> 2) & 3) ? (j & 1 ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
             const bf16x8 va = __builtin_bit_cast(
-                bf16x8, make_uint4(mine && j / 2 == 0 ? vt[0] & half : 0u, mine && j / 2 == 1 ? vt[1] & half : 0u,
-                                   mine && j / 2 == 2 ? vt[2] & half : 0u, mine && j / 2 == 3 ? vt[3] & half : 0u));
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-              if (16 * rt >= rows) break;
-              const floatx4 add = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, p[rt], (floatx4{0.f, 0.f, 0.f, 0.f}), 0, 0, 0);
-              if (key0 + k < lim[rt]) o[rt][y][t] += add;
-            }
+                bf16x8, make_uint4(j / 2 == 0 ? vt[0] & keep : 0u, j / 2 == 1 ? vt[1] & keep : 0u,
+                                   j / 2 == 2 ? vt[2] & keep : 0u, j / 2 == 3 ? vt[3] & keep : 0u));
+            const floatx4 add = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, p, (floatx4{0.f, 0.f, 0.f, 0.f}), 0, 0, 0);
+            if (key0 + k < lim) o[y][t] += add;
           }
         }
       }
     }
   }
 
-  // join the four waves, 16 rows and one dim group at a time
+  // join the four waves, one dim group at a time
   const int tr = threadIdx.x >> 4, tc = threadIdx.x & 15;
+  l = groups_sum(l);
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    if (16 * rt >= rows) break;
-    const float lt = groups_sum(l[rt]);
+  for (int y = 0; y < D::VU; ++y) {
+    if (y) __syncthreads();
+    if (g == 0 && y == 0) {
+      mbuf[wave][c] = m;
+      lbuf[wave][c] = l;
+    }
 #pragma unroll
-    for (int y = 0; y < D::VU; ++y) {
-      __syncthreads();
-      if (g == 0 && y == 0) {
-        mbuf[wave][c] = m[rt];
-        lbuf[wave][c] = lt;
-      }
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int t = 0; t < D::VD; t += 4)
+        *reinterpret_cast<floatx4*>(&obuf[wave][c][D::VD * (4 * g + i) + t]) =
+            floatx4{o[y][t][i], o[y][t + 1][i], o[y][t + 2][i], o[y][t + 3][i]};
+    __syncthreads();
+    float mm = -INFINITY, ll = 0.0f, f[NW], acc[D::VD];
 #pragma unroll
-        for (int t = 0; t < D::VD; t += 4)
-          *reinterpret_cast<floatx4*>(&obuf[wave][c][D::VD * (4 * g + i) + t]) =
-              floatx4{o[rt][y][t][i], o[rt][y][t + 1][i], o[rt][y][t + 2][i], o[rt][y][t + 3][i]};
-      __syncthreads();
-      float mm = -INFINITY, ll = 0.0f, f[NW], acc[D::VD];
+    for (int v = 0; v < NW; ++v) mm = fmaxf(mm, mbuf[v][tr]);
+    const float ms = mm == -INFINITY ? 0.0f : mm;
 #pragma unroll
-      for (int v = 0; v < NW; ++v) mm = fmaxf(mm, mbuf[v][tr]);
-      const float ms = mm == -INFINITY ? 0.0f : mm;
+    for (int v = 0; v < NW; ++v) {
+      f[v] = __builtin_amdgcn_exp2f(mbuf[v][tr] - ms);
+      ll += lbuf[v][tr] * f[v];
+    }
 #pragma unroll
-      for (int v = 0; v < NW; ++v) {
-        f[v] = __builtin_amdgcn_exp2f(mbuf[v][tr] - ms);
-        ll += lbuf[v][tr] * f[v];
-      }
+    for (int t = 0; t < D::VD; ++t) {
+      acc[t] = 0.0f;
 #pragma unroll
-      for (int t = 0; t < D::VD; ++t) {
-        acc[t] = 0.0f;
+      for (int v = 0; v < NW; ++v) acc[t] += obuf[v][tr][D::VD * tc + t] * f[v];
+    }
+    const int j = tr / w.G, h = kvh * w.G + tr % w.G;
+    if (j >= nq) continue;
+    if (it.pid < 0) {
+      const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+      const size_t at = (size_t)(it.q0 + j) * a.nh + h;
+      uint32_t pk[D::VW];
 #pragma unroll
-        for (int v = 0; v < NW; ++v) acc[t] += obuf[v][tr][D::VD * tc + t] * f[v];
-      }
-      const int r = rb * 16 * RT + 16 * rt + tr;
-      const int j = r / w.G, h = kvh * w.G + r % w.G;
-      if (j >= nq) continue;
-      if (it.nsplit == 1) {
-        const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-        const size_t at = (size_t)(it.q0 + j) * a.nh + h;
-        uint32_t pk[D::VW];
+      for (int t = 0; t < D::VW; ++t) pk[t] = ll == 0.0f ? 0u : pack_bf16x2(acc[2 * t] * inv, acc[2 * t + 1] * inv);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * HD + ODIM * y + D::VD * tc);
 #pragma unroll
-        for (int t = 0; t < D::VW; ++t) pk[t] = ll == 0.0f ? 0u : pack_bf16x2(acc[2 * t] * inv, acc[2 * t + 1] * inv);
-        uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * HD + ODIM * y + D::VD * tc);
+      for (int t = 0; t < D::VW; ++t) dst[t] = pk[t];
+      if (a.lse && y == 0 && tc == 0) a.lse[at] = row_lse(mm, ll);
+    } else {
+      const size_t at = ((size_t)it.pid * w.unit + kvh) * 16 + tr;
+      float* dst = w.part_o + at * HD + ODIM * y + D::VD * tc;
 #pragma unroll
-        for (int t = 0; t < D::VW; ++t) dst[t] = pk[t];
-        if (a.lse && y == 0 && tc == 0) a.lse[at] = row_lse(mm, ll);
-      } else {
-        const size_t at = ((size_t)it.pid * w.unit + rest) * (16 * RT) + 16 * rt + tr;
-        float* dst = w.part_o + at * HD + ODIM * y + D::VD * tc;
-#pragma unroll
-        for (int t = 0; t < D::VD; t += 4)
-          *reinterpret_cast<floatx4*>(dst + t) = floatx4{acc[t], acc[t + 1], acc[t + 2], acc[t + 3]};
-        if (y == 0 && tc == 0) {
-          w.part_ml[2 * at] = mm;
-          w.part_ml[2 * at + 1] = ll;
-        }
+      for (int t = 0; t < D::VD; t += 4)
+        *reinterpret_cast<floatx4*>(dst + t) = floatx4{acc[t], acc[t + 1], acc[t + 2], acc[t + 3]};
+      if (y == 0 && tc == 0) {
+        w.part_ml[2 * at] = mm;
+        w.part_ml[2 * at + 1] = ll;
       }
     }
   }
@@ -447,15 +464,16 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
 
 // ------------------------------------------------------------------ many rows
 // The same work for more than 16 rows: a wave takes 16 rows, and all waves of the
-// workgroup share the keys, which pass through three LDS buffers of 32 (one worked on, two
-// filling straight from memory).  Rows lie there in 16-byte pieces permuted (piece p of
+// workgroup share the keys, which pass through three or four LDS buffers of 32 (one worked
+// on, the others filling straight from memory).  Rows lie there in 16-byte pieces permuted (piece p of
 // row r at p ^ swizzle(r)) so that the K reads (16 rows, one piece) and the transposing V
 // reads (8 rows, two pieces) touch every bank once.  The slots of kWindow keys (small
 // pages) or groups of 16 keys are looked up ahead into LDS by the whole workgroup.  Few
 // registers and 52 KB of LDS leave room for three workgroups on a compute unit, which
 // cover each other's waits.
 constexpr int kWindow = 1024;
-constexpr int kStages = 3;
+// LDS buffers of a workgroup, and how many workgroups they leave room for
+constexpr int shared_stages(int RT) { return RT == 8 ? 4 : 3; }
 
 template <int HD>
 __device__ __forceinline__ int swizzle(int r) {
@@ -463,17 +481,18 @@ __device__ __forceinline__ int swizzle(int r) {
   return ((r & 7) << 1) | ((r >> 3) & 1);
 }
 
-template <int HD>
+template <int HD, int RT>
 constexpr int shared_lds() {
-  return kStages * 2 * KT * HD * 2 + kWindow * 4;
+  return shared_stages(RT) * 2 * KT * HD * 2 + kWindow * 4;
 }
 
 template <int HD, int RT, bool kSlots>
-__global__ __launch_bounds__(64 * RT, HD > 128 || RT == 2 ? 2 : RT == 8 ? 4 : 3) void paged_shared(Work w) {
+__global__ __launch_bounds__(64 * RT, HD > 128 ? (RT == 8 ? 2 : 1) : RT == 2 ? 2 : RT == 8 ? 4 : 3) void paged_shared(Work w) {
   constexpr int ROWB = HD * 2, TILEB = KT * ROWB, PIECES = HD / 8;
   constexpr int LOADS = 2 * TILEB / 1024;         // 1 KB loads of one tile, K then V
   constexpr int LPW = (LOADS + RT - 1) / RT;      // of a wave (the last wave's may repeat the last load)
   constexpr int LR = 64 / PIECES;                 // rows of one load
+  constexpr int kStages = shared_stages(RT);
   extern __shared__ __attribute__((aligned(16))) char smem[];
   int32_t* slots = reinterpret_cast<int32_t*>(smem + kStages * 2 * TILEB);
   const PagedArgs& a = w.a;
@@ -481,18 +500,9 @@ __global__ __launch_bounds__(64 * RT, HD > 128 || RT == 2 ? 2 : RT == 8 ? 4 : 3)
   const int kvh = rest % a.nkv, rb = rest / a.nkv;
   Item it;
   if (!find_item(w, u, it)) return;
-  it.b = uniform(it.b);
-  it.q0 = uniform(it.q0);
-  it.n = uniform(it.n);
-  it.kv = uniform(it.kv);
-  it.chunk = uniform(it.chunk);
-  it.split = uniform(it.split);
-  it.nsplit = uniform(it.nsplit);
-  it.pid = uniform(it.pid);
-  if (rest == 0 && it.split == 0 && threadIdx.x == 0) w.req[it.b] = make_int2(it.pid, it.nsplit);
   const int nq = min(it.n, a.max_q), row0 = rb * 16 * RT;
   if (nq * w.G <= row0) return;                                 // (no row of this block exists)
-  if (it.nsplit > 1 && it.pid >= w.pid_cap) return;             // (the workspace holds every range)
+  if (it.pid >= w.pid_cap) return;                // (the workspace holds every range)
 
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = uniform(threadIdx.x >> 6);
@@ -515,7 +525,7 @@ __global__ __launch_bounds__(64 * RT, HD > 128 || RT == 2 ? 2 : RT == 8 ? 4 : 3)
   for (int d = 0; d < HD / 16; ++d) o[d] = floatx4{0.f, 0.f, 0.f, 0.f};
   float m = -INFINITY, mb = 0.0f, l = 0.0f;       // mb: m, or 0 while the row has seen nothing
 
-  const int k0 = it.split * it.chunk, k1 = min(it.kv, k0 + it.chunk);
+  const int k0 = it.k0, k1 = it.k1;
   const int32_t* table = a.page_table + (size_t)it.b * a.width;
   const int64_t rbytes = (int64_t)a.nkv * ROWB;   // bytes between slots
   const int pmask = (1 << a.page_shift) - 1;
@@ -524,8 +534,18 @@ __global__ __launch_bounds__(64 * RT, HD > 128 || RT == 2 ? 2 : RT == 8 ? 4 : 3)
   const int lrow = lane / PIECES, lslot = lane % PIECES;
   const uint32_t lds0 = lds_address(smem);
 
-  // this wave's loads of a tile; a key that does not exist reads an existing row
-  auto issue = [&](int key0, int win0, int stage) {
+  // this wave's loads of a tile: where they go (read from LDS a tile ahead), then the loads
+  // themselves; a key that does not exist reads an existing row
+  int slot[LPW];
+  auto find = [&](int key0, int win0, int win1) {
+#pragma unroll
+    for (int q = 0; q < LPW; ++q) {
+      const int fk = min(q * RT + wave, LOADS - 1) % (LOADS / 2);
+      const int key = min(key0 + (kSlots ? fk * LR + lrow : fk * LR & 16), win1 - 1) - win0;
+      slot[q] = slots[kSlots ? key : key >> 4];
+    }
+  };
+  auto issue = [&](int key0, int stage) {
 #pragma unroll
     for (int q = 0; q < LPW; ++q) {
       const int f = min(q * RT + wave, LOADS - 1), fk = f % (LOADS / 2);
@@ -534,11 +554,10 @@ __global__ __launch_bounds__(64 * RT, HD > 128 || RT == 2 ? 2 : RT == 8 ? 4 : 3)
       const uint32_t piece = (uint32_t)(lslot ^ swizzle<HD>(r)) << 4;
       const uint32_t lds = lds0 + stage * 2 * TILEB + f * 1024;
       if constexpr (kSlots) {
-        const int64_t slot = max(slots[min(key0 + r, it.kv - 1) - win0], 0);
-        load_to_lds16(base + slot * rbytes + piece, uniform(lds));
+        load_to_lds16(base + (int64_t)max(slot[q], 0) * rbytes + piece, uniform(lds));
       } else {
         const int ks = key0 + (fk * LR & 16);     // the 16 keys of one page it falls in
-        const int first = uniform(slots[(min(ks, it.kv - 1) - win0) >> 4]);
+        const int first = uniform(slot[q]);
         const int last = first < 0 ? 0 : clampi(it.kv - 1 - ks, 0, 15);
         load_to_lds16(base + (int64_t)max(first, 0) * rbytes, (uint32_t)min(r & 15, last) * (uint32_t)rbytes + piece,
                       uniform(lds));
@@ -565,15 +584,13 @@ __global__ __launch_bounds__(64 * RT, HD > 128 || RT == 2 ? 2 : RT == 8 ? 4 : 3)
     return f;
   };
 
-  auto work_on = [&](const char* kb, int key0, int win0) {
-    const char* vb = kb + TILEB;
-    asm volatile("" : "+v"(koff), "+v"(voff[0]), "+v"(voff[1]));   // (flipped offsets are cheaper than registers)
-    bool there = key0 + (lane & 31) < it.kv;
-    if (there) {
-      const int e = key0 + (lane & 31) - win0;
-      there = slots[kSlots ? e : e >> 4] >= 0;
-    }
-    floatx4 sc[2];
+  // bit i: key key0 + i exists
+  auto held_of = [&](int key0, int win0) {
+    const int key = min(key0 + (lane & 31), it.kv - 1), e = key - win0;
+    const bool there = slots[kSlots ? e : e >> 4] >= 0 && key0 + (lane & 31) < it.kv;
+    return (uint32_t)uniform((int)(uint32_t)__ballot(there));
+  };
+  auto scores = [&](const char* kb, floatx4 (&sc)[2]) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       sc[s] = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -583,23 +600,52 @@ __global__ __launch_bounds__(64 * RT, HD > 128 || RT == 2 ? 2 : RT == 8 ? 4 : 3)
         sc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[kk], sc[s], 0, 0, 0);
       }
     }
-    const uint32_t held = (uint32_t)uniform((int)(uint32_t)__ballot(there));   // bit i: key key0 + i exists
-    const bool partial = uniform(held != 0xFFFFFFFFu || key0 + KT > minlim) != 0;
-    uint32_t top = 0;                             // the largest exponent of a value, in the high half
-    if (partial) {
+  };
+  auto mask = [&](floatx4 (&sc)[2], uint32_t held, int key0) {
+    held >>= 4 * g;
+    const int left = lim - key0 - 4 * g;          // keys below this are seen
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int i = 16 * (e >> 2) + 4 * g + (e & 3);
-        if (!((held >> i) & 1u) || key0 + i >= lim) sc[e >> 2][e & 3] = -INFINITY;
-      }
-      for (int q = 0; q < TILEB / 1024; ++q) {
-        const uint4 v = *reinterpret_cast<const uint4*>(vb + q * 1024 + lane * 16);
-        const uint32_t x[4] = {v.x & 0x7F807F80u, v.y & 0x7F807F80u, v.z & 0x7F807F80u, v.w & 0x7F807F80u};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top = max(top, max(x[k], x[k] << 16));
-      }
+    for (int e = 0; e < 8; ++e) {
+      constexpr int at[8] = {0, 1, 2, 3, 16, 17, 18, 19};
+      if (!((held >> at[e]) & 1u) || at[e] >= left) sc[e >> 2][e & 3] = -INFINITY;
     }
-    float hi = sc[0][0];
+  };
+  auto weights = [&](const floatx4 (&sc)[2], float& sum) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[e >> 2][e & 3], w.c, -mb));
+    sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+    // rounded to bf16, the second product's operand type
+    return __builtin_bit_cast(bf16x8, make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                 pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
+  };
+  auto finite = [&](const char* vb) {             // every value of the tile
+    uint32_t top = 0;                             // the largest exponent, in the high half
+#pragma unroll 1
+    for (int q = 0; q < TILEB / 1024; ++q) {
+      const uint4 v = *reinterpret_cast<const uint4*>(vb + q * 1024 + lane * 16);
+      const uint32_t x[4] = {v.x & 0x7F807F80u, v.y & 0x7F807F80u, v.z & 0x7F807F80u, v.w & 0x7F807F80u};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = max(top, max(x[k], x[k] << 16));
+    }
+    return !uniform(__any(top >= 0x7F800000u));
+  };
+
+  // In a tile that some row does not see whole, a value that is not finite must not meet
+  // that row's zero weight: such a tile's values are left out here and added afterwards.
+  int left_out = 0, gaps = 0;                     // gaps: a key of the window has no slot
+  auto work_on = [&](const char* kb, int key0, int win0) {
+    const char* vb = kb + TILEB;
+    asm volatile("" : "+v"(koff), "+v"(voff[0]), "+v"(voff[1]));   // (flipped offsets are cheaper than registers)
+    floatx4 sc[2];
+    scores(kb, sc);
+    int whole = 1;
+    if (uniform(gaps || key0 + KT > minlim)) {
+      mask(sc, held_of(key0, win0), key0);
+      whole = uniform(finite(vb));
+      left_out |= !whole;
+    }
+    float hi = sc[0][0], sum;
 #pragma unroll
     for (int e = 1; e < 8; ++e) hi = fmaxf(hi, sc[e >> 2][e & 3]);
     const float tm = groups_max(hi) * w.c;
@@ -612,69 +658,99 @@ __global__ __launch_bounds__(64 * RT, HD > 128 || RT == 2 ? 2 : RT == 8 ? 4 : 3)
 #pragma unroll
       for (int d = 0; d < HD / 16; ++d) o[d] *= al;
     }
-    // weights, rounded to bf16 (the second product's operand type), and their sum
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[e >> 2][e & 3], w.c, -mb));
-    l += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-    const bf16x8 p = __builtin_bit_cast(bf16x8, make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                           pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
-    // in a tile some row does not see whole, a value that is not finite must not meet
-    // that row's zero weight
-    if (!uniform(__any(top >= 0x7F800000u))) {
+    const bf16x8 p = weights(sc, sum);
+    l += sum;
+    if (uniform(whole)) {
 #pragma unroll
       for (int d = 0; d < HD / 16; ++d) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(value_frag(vb, d).v, p, o[d], 0, 0, 0);
-    } else {
-      // key by key, added only to the rows that see it
+    }
+  };
+  // a tile that was left out, key by key, added only to the rows that see it
+  auto add_left_out = [&](const char* kb, int key0, int win0) {
+    const char* vb = kb + TILEB;
+    if (!uniform(gaps || key0 + KT > minlim) || finite(vb)) return;
+    const uint32_t held = held_of(key0, win0);
+    floatx4 sc[2];
+    float sum;
+    scores(kb, sc);
+    mask(sc, held, key0);
+    const bf16x8 p = weights(sc, sum);
 #pragma unroll 1
-      for (int k = 0; k < KT; ++k) {
-        if (!((held >> k) & 1u)) continue;
-        const int jj = (k & 3) | ((k >> 4) << 2);
-        const uint32_t half = jj & 1 ? 0xFFFF0000u : 0x0000FFFFu;
-        const uint32_t keep = g == ((k >> 2) & 3) ? half : 0u;
+    for (int k = 0; k < KT; ++k) {
+      if (!((held >> k) & 1u)) continue;
+      const int jj = (k & 3) | ((k >> 4) << 2);
+      const uint32_t keep = g == ((k >> 2) & 3) ? (jj & 1 ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
 #pragma unroll
-        for (int d = 0; d < HD / 16; ++d) {
-          const VFrag f = value_frag(vb, d);
-          const bf16x8 va = __builtin_bit_cast(
-              bf16x8, make_uint4(jj / 2 == 0 ? f.w[0] & keep : 0u, jj / 2 == 1 ? f.w[1] & keep : 0u,
-                                 jj / 2 == 2 ? f.w[2] & keep : 0u, jj / 2 == 3 ? f.w[3] & keep : 0u));
-          const floatx4 add = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, p, (floatx4{0.f, 0.f, 0.f, 0.f}), 0, 0, 0);
-          if (key0 + k < lim) o[d] += add;
-          __builtin_amdgcn_sched_barrier(0);
-        }
+      for (int d = 0; d < HD / 16; ++d) {
+        const VFrag f = value_frag(vb, d);
+        const bf16x8 va = __builtin_bit_cast(
+            bf16x8, make_uint4(jj / 2 == 0 ? f.w[0] & keep : 0u, jj / 2 == 1 ? f.w[1] & keep : 0u,
+                               jj / 2 == 2 ? f.w[2] & keep : 0u, jj / 2 == 3 ? f.w[3] & keep : 0u));
+        const floatx4 add = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, p, (floatx4{0.f, 0.f, 0.f, 0.f}), 0, 0, 0);
+        if (key0 + k < lim) o[d] += add;
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
 
   constexpr int wkeys = kSlots ? kWindow : kWindow * 16;
-  for (int win0 = k0; win0 < k1; win0 += wkeys) {
-    const int win1 = min(k1, win0 + wkeys);
+  auto look_up = [&](int win0, int win1) {        // the slots of a window's keys
     __syncthreads();
     const int entries = kSlots ? win1 - win0 : (win1 - win0 + 15) >> 4;
+    int missing = 0;
     for (int e = threadIdx.x; e < entries; e += 64 * RT) {
       const int key = win0 + (kSlots ? e : e << 4);
       const int page = table[key >> a.page_shift];
       slots[e] = page >= 0 && page < a.num_pages ? (page << a.page_shift) + (key & pmask) : -1;
+      missing |= slots[e] < 0;
     }
+    gaps = uniform(__syncthreads_or(missing));
+  };
+  // every tile of the range, loaded kStages - 1 tiles ahead
+  auto walk = [&](auto on_tile) {
+    for (int win0 = k0; win0 < k1; win0 += wkeys) {
+      const int win1 = min(k1, win0 + wkeys);
+      look_up(win0, win1);
+#pragma unroll 1
+      for (int s = 0; s < kStages - 1 && win0 + s * KT < win1; ++s) {
+        find(win0 + s * KT, win0, win1);
+        issue(win0 + s * KT, s);
+      }
+      find(win0 + (kStages - 1) * KT, win0, win1);
+      int stage = 0;
+      for (int key0 = win0; key0 < win1; key0 += KT) {
+        // this wave's loads of the tile have landed; after the barrier everyone's have, and
+        // everyone is done with the tile before
+        const int ahead = win1 - key0 - 1;        // / KT: younger tiles on their way, at most kStages - 2
+        if (uniform(ahead >= (kStages - 2) * KT)) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kStages - 2) * LPW) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        lds_barrier();
+        if (uniform(ahead >= (kStages - 1) * KT)) {
+          issue(key0 + (kStages - 1) * KT, stage == 0 ? kStages - 1 : stage - 1);
+          find(key0 + kStages * KT, win0, win1);
+        }
+        on_tile(smem + stage * 2 * TILEB, key0, win0);
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+      }
+    }
+  };
+  if (idle) walk([](const char*, int, int) {});
+  else walk(work_on);
+  int* const again = slots;                       // (free: a window is looked up anew)
+  __syncthreads();
+  if (threadIdx.x == 0) *again = 0;
+  __syncthreads();
+  if (left_out && lane == 0) *again = 1;
+  __syncthreads();
+  if (uniform(*again)) {
     __syncthreads();
-    issue(win0, win0, 0);
-    if (win0 + KT < win1) issue(win0 + KT, win0, 1);
-    int stage = 0;
-    for (int key0 = win0; key0 < win1; key0 += KT) {
-      // this wave's loads of the tile have landed; after the barrier everyone's have, and
-      // everyone is done with the tile before
-      if (uniform(key0 + KT < win1)) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LPW) : "memory");
-      else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      lds_barrier();
-      if (uniform(key0 + 2 * KT < win1)) issue(key0 + 2 * KT, win0, stage == 0 ? 2 : stage - 1);
-      if (!idle) work_on(smem + stage * 2 * TILEB, key0, win0);
-      stage = stage == 2 ? 0 : stage + 1;
-    }
+    if (idle) walk([](const char*, int, int) {});
+    else walk(add_left_out);
   }
 
   l = groups_sum(l);
   if (idle || !ok) return;
-  if (it.nsplit == 1) {
+  if (it.pid < 0) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const size_t at = (size_t)(it.q0 + j) * a.nh + h;
 #pragma unroll
@@ -797,8 +873,8 @@ __global__ __launch_bounds__(256) void paged_join(Work w, int step) {
 }
 
 struct Shape {
-  int RT, RB, G, unit, target, pid_cap;
-  size_t off_o, off_ml, off_req, bytes;
+  int RT, RB, G, unit, target, min_chunk, whole, pid_cap;
+  size_t off_o, off_ml, off_req, off_plan, off_count, bytes;
 };
 
 Shape shape_of(int B, int max_q, int nh, int nkv, int hd) {
@@ -809,15 +885,21 @@ Shape shape_of(int B, int max_q, int nh, int nkv, int hd) {
   s.RT = rows <= 64 ? (rows + 15) / 16 : 8;
   s.RB = (rows + 16 * s.RT - 1) / (16 * s.RT);
   s.unit = nkv * s.RB;
-  // Items aimed at: whole rounds of the workgroups that fit the card at once (`slots`), less
-  // the half range that every request adds on average.
-  const int slots = kCus * (s.RT == 1 || s.RT == 8 || hd > 128 ? 2 : 3), pairs = B * s.unit;
-  s.target = std::max(slots / 2, (pairs / slots + 1) * slots - pairs / 2);
+  // items aimed at: two workgroups on each compute unit (one with heads of 256) draw all
+  // that memory gives, and shorter ranges cost more in starting and joining than they
+  // even out: 64 blocks of 16 x 4 rows over 100..4000 keys take 153 us so, 160 at twice
+  // and 169 us at three times as many; one row over 131071 keys 101, 105 and 115 us
+  s.target = kCus * (hd > 128 ? 1 : 2);
+  // a range shorter than this costs more to start and join than it takes
+  s.min_chunk = s.RT == 1 ? 512 : 256;
+  s.whole = 2 * s.min_chunk;
   // a split request has more keys than a range, so its ranges are fewer than twice its
   // keys over the range's length, and all of them together at most 2 target / unit
   s.pid_cap = 2 * (s.target / s.unit + 1) + 1;
   s.off_req = 0;
-  s.off_ml = al((size_t)B * sizeof(int2));
+  s.off_count = al((size_t)B * sizeof(int2));
+  s.off_plan = s.off_count + 256;
+  s.off_ml = s.off_plan + al(((size_t)s.target / s.unit + B + 2) * sizeof(Item));
   s.off_o = s.off_ml + al((size_t)s.pid_cap * s.unit * 16 * s.RT * 2 * sizeof(float));
   s.bytes = s.off_o + al((size_t)s.pid_cap * s.unit * 16 * s.RT * hd * sizeof(float));
   return s;
@@ -825,11 +907,8 @@ Shape shape_of(int B, int max_q, int nh, int nkv, int hd) {
 
 template <int HD, int RT, bool kSlots>
 hipError_t launch_rows(const Work& w, int grid, hipStream_t stream) {
-#ifndef STREAM_FROM
-#define STREAM_FROM 2
-#endif
-  if constexpr (RT >= STREAM_FROM) {
-    constexpr int lds = shared_lds<HD>();
+  if constexpr (RT > 1) {
+    constexpr int lds = shared_lds<HD, RT>();
     if (lds > 64 * 1024) {
       const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&paged_shared<HD, RT, kSlots>),
                                                hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -837,7 +916,7 @@ hipError_t launch_rows(const Work& w, int grid, hipStream_t stream) {
     }
     hipLaunchKernelGGL((paged_shared<HD, RT, kSlots>), dim3(grid), dim3(64 * RT), lds, stream, w);
   } else {
-    hipLaunchKernelGGL((paged_rows<HD, RT, kSlots>), dim3(grid), dim3(64 * NW), 0, stream, w);
+    hipLaunchKernelGGL((paged_rows<HD, kSlots>), dim3(grid), dim3(64 * NW), 0, stream, w);
   }
   return hipGetLastError();
 }
@@ -846,7 +925,7 @@ template <int HD, int RT>
 hipError_t launch(const Work& w, int64_t items, int max_kv, hipStream_t stream) {
   const int grid = (int)items;
   const hipError_t e = w.a.page_shift < 4 ? launch_rows<HD, RT, true>(w, grid, stream) : launch_rows<HD, RT, false>(w, grid, stream);
-  if (e != hipSuccess || max_kv <= kMinChunk) return e;
+  if (e != hipSuccess || max_kv <= w.whole) return e;
   const int rows = std::min(16 * RT, w.a.max_q * w.G);
   const int step = std::max(1, std::min(rows, (int)((int64_t)w.a.B * w.unit * rows / kJoinGroups)));
   hipLaunchKernelGGL((paged_join<HD, RT>), dim3(w.a.B * w.unit, (rows + step - 1) / step), dim3(256), 0, stream, w, step);
@@ -879,16 +958,26 @@ hipError_t launch_paged_attention(const PagedArgs& a, int hd, void* workspace, h
   w.RB = s.RB;
   w.unit = s.unit;
   w.target = s.target;
+  w.min_chunk = s.min_chunk;
+  w.whole = s.whole;
   w.pid_cap = s.pid_cap;
   w.c = a.scale * kLog2e;
   char* base = static_cast<char*>(workspace);
   w.req = reinterpret_cast<int2*>(base + s.off_req);
   w.part_ml = reinterpret_cast<float*>(base + s.off_ml);
   w.part_o = reinterpret_cast<float*>(base + s.off_o);
+  w.plan = nullptr;
+  w.count = reinterpret_cast<int*>(base + s.off_count);
   // at most one range per request, plus the ones the balancing adds
   const int max_kv = a.width << a.page_shift;
-  const int64_t most = (int64_t)a.B * s.unit * std::max(1, (max_kv + kMinChunk - 1) / kMinChunk);
+  const int64_t most = (int64_t)a.B * s.unit * (max_kv <= s.whole ? 1 : (max_kv + s.min_chunk - 1) / s.min_chunk);
   const int64_t items = std::min(most, (int64_t)a.B * s.unit + s.target + s.unit);
+  if (a.B > 1 && max_kv > s.whole) {
+    w.plan = reinterpret_cast<Item*>(base + s.off_plan);
+    hipLaunchKernelGGL(paged_plan, dim3(1), dim3(kPlanThreads), 0, stream, w);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   switch (hd) {
     case 64: return launch_rt<64>(w, s.RT, items, max_kv, stream);
     case 128: return launch_rt<128>(w, s.RT, items, max_kv, stream);
