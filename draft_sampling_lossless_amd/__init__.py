@@ -501,43 +501,50 @@ def admit(cond_accept: torch.Tensor, K: int, survival: Optional[torch.Tensor] = 
 
 # ---------------------------------------------------------------- the cache and attention over it
 
-def _rows(t: torch.Tensor, name: str, device, shape) -> int:
+def _rows(t: torch.Tensor, name: str, dev: int, rows: int, heads: int, hd: int) -> int:
     """Element distance between the tokens of a [tokens, heads, hd] bf16 tensor whose
     heads lie contiguously: a tensor of its own or a column range of a wider product."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _BF16:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {_BF16}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    rows, heads, hd = shape
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if t.shape != (rows, heads, hd):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, heads, hd)}")
     row, head, one = t.stride()
     if (one != 1 and hd > 1) or (head != hd and heads > 1):
         raise ValueError(f"{name}: the heads of a token must lie contiguously (strides {t.stride()})")
-    if rows <= 1:
-        return heads * hd
-    return row
+    return row if rows > 1 else heads * hd
 
 
-def _device_of(t: torch.Tensor, name: str):
+def _arg(t: Optional[torch.Tensor], name: str, dtypes, dev: int, shape) -> Optional[int]:
+    """_ptr for a known device index, without its cost on arguments that are right."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.get_device() == dev and t.shape == shape \
+            and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t, name, dtypes, torch.device("cuda", dev), shape)
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device (cuda/hip) tensor")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, hd], got shape {tuple(t.shape)}")
-    return t.device
+    return t.get_device()
 
 
-def _on(dev, name: str, call, *args) -> None:
+def _on(dev: int, name: str, call, *args) -> None:
     """call(*args, stream) on dev's current stream, with dev the current device."""
-    if dev.index == torch.cuda.current_device():
-        status = call(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if dev == torch.cuda.current_device():
+        status = call(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            status = call(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = call(*args, torch._C._cuda_getCurrentRawStream(dev))
     if status != 0:
         _check(name, status)
 
@@ -558,27 +565,27 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: 
     if k_cache.dim() != 3:
         raise ValueError(f"k_cache must be [num_slots, nkv, hd], got shape {tuple(k_cache.shape)}")
     S = k_cache.shape[0]
-    ks, vs = _rows(k, "k", dev, k.shape), _rows(v, "v", dev, k.shape)
+    ks, vs = _rows(k, "k", dev, M, nkv, hd), _rows(v, "v", dev, M, nkv, hd)
     nh = qs = qos = kos = 0
     qp = qop = kop = None
     if q is not None:
         _device_of(q, "q")
         nh = q.shape[1]
-        qs = _rows(q, "q", dev, (M, nh, hd))
+        qs = _rows(q, "q", dev, M, nh, hd)
         if q_out is None:
-            q_out = torch.empty((M, nh, hd), dtype=q.dtype, device=dev)
-        qos = _rows(q_out, "q_out", dev, (M, nh, hd))
+            q_out = torch.empty((M, nh, hd), dtype=q.dtype, device=q.device)
+        qos = _rows(q_out, "q_out", dev, M, nh, hd)
         qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None or qnorm_w is not None:
         raise ValueError("q_out and qnorm_w need q")
     if k_out is not None:
-        kos = _rows(k_out, "k_out", dev, k.shape)
+        kos = _rows(k_out, "k_out", dev, M, nkv, hd)
         kop = k_out.data_ptr()
     _on(dev, "dspark_kv_append", load().dspark_kv_append,
-        qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(qnorm_w, "qnorm_w", _BF16, dev, (hd,)),
-        _ptr(knorm_w, "knorm_w", _BF16, dev, (hd,)), _ptr(positions, "positions", _I32, dev, (M,)),
-        _ptr(slots, "slots", _I64, dev, (M,)), qop, qos, kop, kos,
-        _ptr(k_cache, "k_cache", _BF16, dev, (S, nkv, hd)), _ptr(v_cache, "v_cache", _BF16, dev, (S, nkv, hd)),
+        qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, _arg(qnorm_w, "qnorm_w", _BF16, dev, (hd,)),
+        _arg(knorm_w, "knorm_w", _BF16, dev, (hd,)), _arg(positions, "positions", _I32, dev, (M,)),
+        _arg(slots, "slots", _I64, dev, (M,)), qop, qos, kop, kos,
+        _arg(k_cache, "k_cache", _BF16, dev, (S, nkv, hd)), _arg(v_cache, "v_cache", _BF16, dev, (S, nkv, hd)),
         M, nh, nkv, hd, S, eps, rope_theta)
     return q_out
 
@@ -599,7 +606,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     receives each row's log sum of exponentials.  Returns out [T, nh, hd]."""
     dev = _device_of(q, "q")
     T, nh, hd = q.shape
-    qs = _rows(q, "q", dev, q.shape)
+    qs = _rows(q, "q", dev, T, nh, hd)
     if k_cache.dim() != 3 or page_table.dim() != 2:
         raise ValueError("k_cache must be [num_slots, nkv, hd] and page_table [B, max_pages]")
     S, nkv = k_cache.shape[0], k_cache.shape[1]
@@ -607,16 +614,19 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if page_size < 1 or S % page_size:
         raise ValueError(f"num_slots ({S}) must be a multiple of page_size ({page_size})")
     if out is None:
-        out = torch.empty((T, nh, hd), dtype=q.dtype, device=dev)
+        out = torch.empty((T, nh, hd), dtype=q.dtype, device=q.device)
     lib = load()
-    ws = _workspace(workspace, lib.dspark_paged_attention_workspace_size(T, B, max_q, nh, nkv, hd), dev)
-    if ws.device != dev:
-        raise ValueError(f"workspace is on {ws.device}, expected {dev}")
+    ws = workspace
+    if ws is None:
+        ws = torch.empty(max(16, lib.dspark_paged_attention_workspace_size(T, B, max_q, nh, nkv, hd)),
+                         dtype=torch.uint8, device=q.device)
+    elif ws.get_device() != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{dev}")
     _on(dev, "dspark_paged_attention", lib.dspark_paged_attention,
-        q.data_ptr(), qs, _ptr(k_cache, "k_cache", _BF16, dev, (S, nkv, hd)),
-        _ptr(v_cache, "v_cache", _BF16, dev, (S, nkv, hd)), _ptr(page_table, "page_table", _I32, dev, (B, width)),
-        _ptr(kv_len, "kv_len", _I32, dev, (B,)), _ptr(cu_q, "cu_q", _I32, dev, (B + 1,)),
-        _ptr(out, "out", _BF16, dev, (T, nh, hd)), _ptr(lse, "lse", _F32, dev, (T, nh)), T, B, max_q, nh, nkv, hd,
+        q.data_ptr(), qs, _arg(k_cache, "k_cache", _BF16, dev, (S, nkv, hd)),
+        _arg(v_cache, "v_cache", _BF16, dev, (S, nkv, hd)), _arg(page_table, "page_table", _I32, dev, (B, width)),
+        _arg(kv_len, "kv_len", _I32, dev, (B,)), _arg(cu_q, "cu_q", _I32, dev, (B + 1,)),
+        _arg(out, "out", _BF16, dev, (T, nh, hd)), _arg(lse, "lse", _F32, dev, (T, nh)), T, B, max_q, nh, nkv, hd,
         page_size, width, S // page_size, 1 if causal else 0, hd ** -0.5 if scale is None else scale,
         ws.data_ptr(), ws.numel())
     return out
@@ -634,13 +644,13 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     T, nh, hd = q.shape
     _device_of(k, "k")
     nkv = k.shape[1]
-    qs = _rows(q, "q", dev, q.shape)
-    ks, vs = _rows(k, "k", dev, (T, nkv, hd)), _rows(v, "v", dev, (T, nkv, hd))
+    qs = _rows(q, "q", dev, T, nh, hd)
+    ks, vs = _rows(k, "k", dev, T, nkv, hd), _rows(v, "v", dev, T, nkv, hd)
     B = cu_seqlens.numel() - 1
     if out is None:
-        out = torch.empty((T, nh, hd), dtype=q.dtype, device=dev)
+        out = torch.empty((T, nh, hd), dtype=q.dtype, device=q.device)
     _on(dev, "dspark_prompt_attention", load().dspark_prompt_attention,
-        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(cu_seqlens, "cu_seqlens", _I32, dev, (B + 1,)),
-        _ptr(out, "out", _BF16, dev, (T, nh, hd)), _ptr(lse, "lse", _F32, dev, (T, nh)), T, B, nh, nkv, hd,
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _arg(cu_seqlens, "cu_seqlens", _I32, dev, (B + 1,)),
+        _arg(out, "out", _BF16, dev, (T, nh, hd)), _arg(lse, "lse", _F32, dev, (T, nh)), T, B, nh, nkv, hd,
         1 if causal else 0, hd ** -0.5 if scale is None else scale)
     return out

@@ -275,6 +275,17 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
   const int rstride = a.nkv * HD;                 // elements between slots
   const int pmask = (1 << a.page_shift) - 1;
 
+  // where a tile lies, looked up a tile ahead (behind the last: some page of the request)
+  int where[2];                                   // the pages of its halves; kSlots: of key lane % 32
+  auto find = [&](int key0) {
+    if constexpr (kSlots) {
+      where[0] = table[min(key0 + (lane & 31), it.kv - 1) >> a.page_shift];
+    } else {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) where[s] = table[min(key0 + 16 * s, it.kv - 1) >> a.page_shift];
+    }
+  };
+  if (it.k0 + KT * wave < it.k1) find(it.k0 + KT * wave);
   for (int key0 = it.k0 + KT * wave; key0 < it.k1; key0 += KT * NW) {
     // the tile's keys and values; a key that does not exist reads an existing row
     uint32_t held;                                // bit i: key key0 + i exists
@@ -293,8 +304,7 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
           *reinterpret_cast<uint2*>(vf[x][j]) = *reinterpret_cast<const uint2*>(src + ODIM * x + 4 * c);
     };
     if constexpr (kSlots) {
-      const int key = min(key0 + (lane & 31), it.kv - 1);
-      const int page = table[key >> a.page_shift];
+      const int key = min(key0 + (lane & 31), it.kv - 1), page = where[0];
       const bool there = page >= 0 && page < a.num_pages;
       const int slot = (there ? page << a.page_shift : 0) + (key & pmask);
       held = (uint32_t)__ballot(there && key0 + (lane & 31) < it.kv);
@@ -308,7 +318,7 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int ks = key0 + 16 * s;
-        int page = uniform(table[min(ks, it.kv - 1) >> a.page_shift]);
+        int page = uniform(where[s]);
         int cnt = clampi(it.kv - ks, 0, 16);      // keys of this half
         if (page < 0 || page >= a.num_pages) page = cnt = 0;
         held |= ((1u << cnt) - 1u) << (16 * s);
@@ -319,6 +329,7 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
         for (int j = 0; j < 4; ++j) value_row(4 * s + j, a.v_cache + at + min(4 * g + j, last) * rstride);
       }
     }
+    find(key0 + KT * NW);
     held = (uint32_t)uniform((int)held);
     const bool partial = uniform(held != 0xFFFFFFFFu || key0 + KT > minlim) != 0;
 
