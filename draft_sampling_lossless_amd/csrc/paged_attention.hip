@@ -545,33 +545,51 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? (RT == 8 ? 2 : 1) : RT == 2 ? 2
   const int lrow = lane / PIECES, lslot = lane % PIECES;
   const uint32_t lds0 = lds_address(smem);
 
-  // this wave's loads of a tile: where they go (read from LDS a tile ahead), then the loads
-  // themselves; a key that does not exist reads an existing row
-  int slot[LPW];
-  auto find = [&](int key0, int win0, int win1) {
+  int gaps = 0;                                   // a key of the window has no slot
+  // this wave's loads of a tile: load f = q RT + wave (of K, then of V) takes LR rows
+  const char* from[LPW];                          // K or V
+  uint32_t to[LPW], off[LPW];                     // LDS offset in the tile; byte offset behind the 16 keys' first slot
+  int half[LPW], row_of[LPW];                     // which 16 keys; this lane's row of the tile
 #pragma unroll
-    for (int q = 0; q < LPW; ++q) {
-      const int fk = min(q * RT + wave, LOADS - 1) % (LOADS / 2);
-      const int key = min(key0 + (kSlots ? fk * LR + lrow : fk * LR & 16), win1 - 1) - win0;
-      slot[q] = slots[kSlots ? key : key >> 4];
+  for (int q = 0; q < LPW; ++q) {
+    const int f = uniform(min(q * RT + wave, LOADS - 1)), fk = f % (LOADS / 2), r = fk * LR + lrow;
+    from[q] = f < LOADS / 2 ? kbase : vbase;
+    to[q] = f * 1024;
+    half[q] = fk * LR >> 4;
+    row_of[q] = r;
+    off[q] = (uint32_t)(lslot ^ swizzle<HD>(r)) << 4;
+    if (!kSlots) off[q] += (uint32_t)(r & 15) * (uint32_t)rbytes;
+  }
+  // Where a tile lies is read from LDS a tile ahead; a key that does not exist reads an
+  // existing row.
+  int slot[kSlots ? LPW : 2];                     // of this lane's rows; of the two first keys
+  auto find = [&](int key0, int win0, int win1) {
+    if constexpr (kSlots) {
+#pragma unroll
+      for (int q = 0; q < LPW; ++q) slot[q] = slots[min(key0 + row_of[q], win1 - 1) - win0];
+    } else {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) slot[s] = slots[(min(key0 + 16 * s, win1 - 1) - win0) >> 4];
     }
   };
   auto issue = [&](int key0, int stage) {
+    const uint32_t lds = lds0 + stage * 2 * TILEB;
+    if constexpr (kSlots) {
 #pragma unroll
-    for (int q = 0; q < LPW; ++q) {
-      const int f = min(q * RT + wave, LOADS - 1), fk = f % (LOADS / 2);
-      const char* base = f < LOADS / 2 ? kbase : vbase;
-      const int r = fk * LR + lrow;               // row of the tile
-      const uint32_t piece = (uint32_t)(lslot ^ swizzle<HD>(r)) << 4;
-      const uint32_t lds = lds0 + stage * 2 * TILEB + f * 1024;
-      if constexpr (kSlots) {
-        load_to_lds16(base + (int64_t)max(slot[q], 0) * rbytes + piece, uniform(lds));
-      } else {
-        const int ks = key0 + (fk * LR & 16);     // the 16 keys of one page it falls in
-        const int first = uniform(slot[q]);
-        const int last = first < 0 ? 0 : clampi(it.kv - 1 - ks, 0, 15);
-        load_to_lds16(base + (int64_t)max(first, 0) * rbytes, (uint32_t)min(r & 15, last) * (uint32_t)rbytes + piece,
-                      uniform(lds));
+      for (int q = 0; q < LPW; ++q) load_to_lds16(from[q] + (int64_t)max(slot[q], 0) * rbytes + off[q], uniform(lds + to[q]));
+    } else {
+      int64_t at[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) at[s] = (int64_t)max(uniform(slot[s]), 0) * rbytes;
+      const bool tail = uniform(gaps || key0 + KT > it.kv) != 0;
+#pragma unroll
+      for (int q = 0; q < LPW; ++q) {
+        uint32_t o = off[q];
+        if (tail) {
+          const int first = half[q] ? uniform(slot[1]) : uniform(slot[0]), r = row_of[q] & 15;
+          o -= (uint32_t)max(r - (first < 0 ? 0 : clampi(it.kv - 1 - key0 - 16 * half[q], 0, 15)), 0) * (uint32_t)rbytes;
+        }
+        load_to_lds16(from[q] + (half[q] ? at[1] : at[0]), o, uniform(lds + to[q]));
       }
     }
   };
@@ -644,7 +662,7 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? (RT == 8 ? 2 : 1) : RT == 2 ? 2
 
   // In a tile that some row does not see whole, a value that is not finite must not meet
   // that row's zero weight: such a tile's values are left out here and added afterwards.
-  int left_out = 0, gaps = 0;                     // gaps: a key of the window has no slot
+  int left_out = 0;
   auto work_on = [&](const char* kb, int key0, int win0) {
     const char* vb = kb + TILEB;
     asm volatile("" : "+v"(koff), "+v"(voff[0]), "+v"(voff[1]));   // (flipped offsets are cheaper than registers)
@@ -901,8 +919,11 @@ Shape shape_of(int B, int max_q, int nh, int nkv, int hd) {
   // even out: 64 blocks of 16 x 4 rows over 100..4000 keys take 153 us so, 160 at twice
   // and 169 us at three times as many; one row over 131071 keys 101, 105 and 115 us
   s.target = kCus * (hd > 128 ? 1 : 2);
-  // a range shorter than this costs more to start and join than it takes
-  s.min_chunk = s.RT == 1 ? 512 : 256;
+  // A shorter range costs more to start and join than it takes.  A tile of 32 keys takes a
+  // workgroup of shared tiles about 0.9 us alone, four tiles the waves of paged_rows; the
+  // joining pass, about 5 us.  Calls that leave most of the card idle cut finer: 9 tokens
+  // over 512 keys of one request 12.8 us so and 19.8 us whole, of 64 requests 39 and 30 us.
+  s.min_chunk = s.RT == 1 ? 512 : B * s.unit <= kCus / 4 ? 128 : 256;
   s.whole = 2 * s.min_chunk;
   // a split request has more keys than a range, so its ranges are fewer than twice its
   // keys over the range's length, and all of them together at most 2 target / unit
