@@ -63,16 +63,10 @@ __device__ bool find_tile(const Work& w, int u, int rows, int& start, int& n, in
     int s = 0, len = 0;
     if (lane < a.B) sequence(a, lane, s, len);
     const int mine = tiles_of(len);
-    int hi = mine;
-    for (int o = 32; o > 0; o >>= 1) hi = max(hi, __shfl_xor(hi, o));
-    // the level: the largest index that leaves more than u tiles at or above it
-    auto at_least = [&](int level) {
-      int c = max(mine - level, 0);
-      for (int o = 32; o > 0; o >>= 1) c += __shfl_xor(c, o);
-      return uniform(c);
-    };
-    int lo = 0;
-    hi = uniform(hi);
+    // the level: the largest index that leaves more than u tiles at or above it (all counts
+    // are below 2^24: exact in float)
+    auto at_least = [&](int level) { return uniform((int)group_sum((float)max(mine - level, 0), 64)); };
+    int lo = 0, hi = uniform((int)wave_max_u32((uint32_t)mine));
     if (at_least(0) <= u) return false;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
