@@ -19,9 +19,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((floatx2{a, b}), bf16x2));
 }
 
-// whether a pair of bf16 holds an infinity or a NaN (exponent bits all set)
-__device__ __forceinline__ bool bf16x2_nonfinite(uint32_t w) {
-  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+// c + the two bf16 of a pair, in float.  The output divides by the sum of the weights as
+// they are multiplied, rounded: a row that one key dominates then keeps that key's value
+// exactly, whatever its weight was rounded to.  The log-sum-exp takes the unrounded sum.
+__device__ __forceinline__ float add_bf16x2(uint32_t w, float c) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), __builtin_bit_cast(bf16x2, 0x3F803F80u), c, false);
 }
 
 // transposing LDS read: the 16 lanes of a quarter wave name four rows of 16 bf16 (lane i

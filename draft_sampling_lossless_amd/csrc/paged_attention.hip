@@ -62,7 +62,7 @@ struct Work {
   int pid_cap;         // ranges the workspace has room for
   float c;             // scale * log2 e
   float* part_o;       // [pid_cap, unit, 16 RT, hd]
-  float* part_ml;      // [pid_cap, unit, 16 RT, 2]
+  floatx4* part_ml;    // [pid_cap, unit, 16 RT]: maximum, sum of rounded weights, of unrounded ones
   int2* req;           // [B]: first partial and number of ranges of a split request (one: not split)
   Item* plan;          // the items, dearest first, or null: one request, or none is ever cut
   int* count;          // how many of them
@@ -223,6 +223,17 @@ __device__ __forceinline__ float groups_sum(float v) {
   return __uint_as_float(a) + __uint_as_float(b);
 }
 
+// eight weights rounded to bf16, and added to the sum of the rounded and (kLse) of the unrounded
+template <bool kLse>
+__device__ __forceinline__ bf16x8 pack_weights(const float (&x)[8], float& l, float& lx) {
+  uint32_t p[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) p[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+  l += add_bf16x2(p[1], add_bf16x2(p[0], 0.0f)) + add_bf16x2(p[3], add_bf16x2(p[2], 0.0f));
+  if (kLse) lx += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+  return __builtin_bit_cast(bf16x8, make_uint4(p[0], p[1], p[2], p[3]));
+}
+
 template <int HD>
 struct Dims {
   static constexpr int VD = HD >= 128 ? 8 : 4;    // dims a lane loads of a value row, per group of 16 VD
@@ -232,13 +243,13 @@ struct Dims {
 
 // kSlots: pages smaller than 16, so the slot of every key is looked up by a lane of its
 // own; otherwise 16 aligned keys lie in one page and the wave looks up two
-template <int HD, bool kSlots>
+template <int HD, bool kSlots, bool kLse>
 __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
   using D = Dims<HD>;
   constexpr int ODIM = 16 * D::VD;                // dims of one group
   const PagedArgs& a = w.a;
   __shared__ float obuf[NW][16][ODIM + 4];
-  __shared__ float mbuf[NW][16], lbuf[NW][16];
+  __shared__ float mbuf[NW][16], lbuf[NW][16], xbuf[NW][16];
 
   const int u = blockIdx.x / w.unit, kvh = blockIdx.x % w.unit;
   Item it;
@@ -269,7 +280,7 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
   for (int x = 0; x < D::VU; ++x)
 #pragma unroll
     for (int t = 0; t < D::VD; ++t) o[x][t] = floatx4{0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, mb = 0.0f, l = 0.0f;       // mb: m, or 0 while the row has seen nothing
+  float m = -INFINITY, mb = 0.0f, l = 0.0f, lx = 0.0f;   // mb: m, or 0 while the row has seen nothing; lx: l unrounded
 
   const int32_t* table = a.page_table + (size_t)it.b * a.width;
   const int rstride = a.nkv * HD;                 // elements between slots
@@ -370,6 +381,7 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
       m = mn;
       mb = mn == -INFINITY ? 0.0f : mn;
       l *= al;
+      lx *= al;
 #pragma unroll
       for (int y = 0; y < D::VU; ++y)
 #pragma unroll
@@ -378,10 +390,8 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[e >> 2][e & 3], w.c, -mb));
-    l += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
     // the weights' rounding to bf16, the second product's operand type
-    const bf16x8 p = __builtin_bit_cast(bf16x8, make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                           pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
+    const bf16x8 p = pack_weights<kLse>(x, l, lx);
 
     // in a tile some row does not see whole, a value that is not finite must not meet
     // that row's zero weight
@@ -418,12 +428,14 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
   // join the four waves, one dim group at a time
   const int tr = threadIdx.x >> 4, tc = threadIdx.x & 15;
   l = groups_sum(l);
+  if (kLse) lx = groups_sum(lx);
 #pragma unroll
   for (int y = 0; y < D::VU; ++y) {
     if (y) __syncthreads();
     if (g == 0 && y == 0) {
       mbuf[wave][c] = m;
       lbuf[wave][c] = l;
+      if (kLse) xbuf[wave][c] = lx;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -432,7 +444,7 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
         *reinterpret_cast<floatx4*>(&obuf[wave][c][D::VD * (4 * g + i) + t]) =
             floatx4{o[y][t][i], o[y][t + 1][i], o[y][t + 2][i], o[y][t + 3][i]};
     __syncthreads();
-    float mm = -INFINITY, ll = 0.0f, f[NW], acc[D::VD];
+    float mm = -INFINITY, ll = 0.0f, xx = 0.0f, f[NW], acc[D::VD];
 #pragma unroll
     for (int v = 0; v < NW; ++v) mm = fmaxf(mm, mbuf[v][tr]);
     const float ms = mm == -INFINITY ? 0.0f : mm;
@@ -440,6 +452,7 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
     for (int v = 0; v < NW; ++v) {
       f[v] = __builtin_amdgcn_exp2f(mbuf[v][tr] - ms);
       ll += lbuf[v][tr] * f[v];
+      if (kLse) xx += xbuf[v][tr] * f[v];
     }
 #pragma unroll
     for (int t = 0; t < D::VD; ++t) {
@@ -458,17 +471,14 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
       uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * HD + ODIM * y + D::VD * tc);
 #pragma unroll
       for (int t = 0; t < D::VW; ++t) dst[t] = pk[t];
-      if (a.lse && y == 0 && tc == 0) a.lse[at] = row_lse(mm, ll);
+      if (kLse && y == 0 && tc == 0) a.lse[at] = row_lse(mm, xx);
     } else {
       const size_t at = ((size_t)it.pid * w.unit + kvh) * 16 + tr;
       float* dst = w.part_o + at * HD + ODIM * y + D::VD * tc;
 #pragma unroll
       for (int t = 0; t < D::VD; t += 4)
         *reinterpret_cast<floatx4*>(dst + t) = floatx4{acc[t], acc[t + 1], acc[t + 2], acc[t + 3]};
-      if (y == 0 && tc == 0) {
-        w.part_ml[2 * at] = mm;
-        w.part_ml[2 * at + 1] = ll;
-      }
+      if (y == 0 && tc == 0) w.part_ml[at] = floatx4{mm, ll, xx, 0.0f};
     }
   }
 }
@@ -497,7 +507,7 @@ constexpr int shared_lds() {
   return shared_stages(RT) * 2 * KT * HD * 2 + kWindow * 4;
 }
 
-template <int HD, int RT, bool kSlots>
+template <int HD, int RT, bool kSlots, bool kLse>
 __global__ __launch_bounds__(64 * RT, HD > 128 ? (RT == 8 ? 2 : 1) : RT == 2 ? 2 : RT == 8 ? 4 : 3) void paged_shared(Work w) {
   constexpr int ROWB = HD * 2, TILEB = KT * ROWB, PIECES = HD / 8;
   constexpr int LOADS = 2 * TILEB / 1024;         // 1 KB loads of one tile, K then V
@@ -534,7 +544,7 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? (RT == 8 ? 2 : 1) : RT == 2 ? 2
   floatx4 o[HD / 16];                             // dims 16 d + 4 g + i of row c
 #pragma unroll
   for (int d = 0; d < HD / 16; ++d) o[d] = floatx4{0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, mb = 0.0f, l = 0.0f;       // mb: m, or 0 while the row has seen nothing
+  float m = -INFINITY, mb = 0.0f, l = 0.0f, lx = 0.0f;   // mb: m, or 0 while the row has seen nothing; lx: l unrounded
 
   const int k0 = it.k0, k1 = it.k1;
   const int32_t* table = a.page_table + (size_t)it.b * a.width;
@@ -639,14 +649,12 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? (RT == 8 ? 2 : 1) : RT == 2 ? 2
       if (!((held >> at[e]) & 1u) || at[e] >= left) sc[e >> 2][e & 3] = -INFINITY;
     }
   };
-  auto weights = [&](const floatx4 (&sc)[2], float& sum) {
+  // weights, rounded to bf16 (the second product's operand type), added to two sums
+  auto weights = [&](const floatx4 (&sc)[2], float& sum, float& sumx) {
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[e >> 2][e & 3], w.c, -mb));
-    sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-    // rounded to bf16, the second product's operand type
-    return __builtin_bit_cast(bf16x8, make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                 pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
+    return pack_weights<kLse>(x, sum, sumx);
   };
   auto finite = [&](const char* vb) {             // every value of the tile
     uint32_t top = 0;                             // the largest exponent, in the high half
@@ -674,7 +682,7 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? (RT == 8 ? 2 : 1) : RT == 2 ? 2
       whole = uniform(finite(vb));
       left_out |= !whole;
     }
-    float hi = sc[0][0], sum;
+    float hi = sc[0][0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) hi = fmaxf(hi, sc[e >> 2][e & 3]);
     const float tm = groups_max(hi) * w.c;
@@ -684,11 +692,11 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? (RT == 8 ? 2 : 1) : RT == 2 ? 2
       m = mn;
       mb = mn == -INFINITY ? 0.0f : mn;
       l *= al;
+      lx *= al;
 #pragma unroll
       for (int d = 0; d < HD / 16; ++d) o[d] *= al;
     }
-    const bf16x8 p = weights(sc, sum);
-    l += sum;
+    const bf16x8 p = weights(sc, l, lx);
     if (uniform(whole)) {
 #pragma unroll
       for (int d = 0; d < HD / 16; ++d) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(value_frag(vb, d).v, p, o[d], 0, 0, 0);
@@ -700,10 +708,10 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? (RT == 8 ? 2 : 1) : RT == 2 ? 2
     if (!uniform(gaps || key0 + KT > minlim) || finite(vb)) return;
     const uint32_t held = held_of(key0, win0);
     floatx4 sc[2];
-    float sum;
+    float counted = 0.0f;                         // (its weights are in the sums already)
     scores(kb, sc);
     mask(sc, held, key0);
-    const bf16x8 p = weights(sc, sum);
+    const bf16x8 p = weights(sc, counted, counted);
 #pragma unroll 1
     for (int k = 0; k < KT; ++k) {
       if (!((held >> k) & 1u)) continue;
@@ -778,6 +786,7 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? (RT == 8 ? 2 : 1) : RT == 2 ? 2
   }
 
   l = groups_sum(l);
+  if (kLse) lx = groups_sum(lx);
   if (idle || !ok) return;
   if (it.pid < 0) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -787,15 +796,12 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? (RT == 8 ? 2 : 1) : RT == 2 ? 2
       *reinterpret_cast<uint2*>(a.out + at * HD + 16 * d + 4 * g) =
           l == 0.0f ? make_uint2(0u, 0u)
                     : make_uint2(pack_bf16x2(o[d][0] * inv, o[d][1] * inv), pack_bf16x2(o[d][2] * inv, o[d][3] * inv));
-    if (a.lse && g == 0) a.lse[at] = row_lse(m, l);
+    if (kLse && g == 0) a.lse[at] = row_lse(m, lx);
   } else {
     const size_t at = ((size_t)it.pid * w.unit + rest) * (16 * RT) + 16 * wave + c;
 #pragma unroll
     for (int d = 0; d < HD / 16; ++d) *reinterpret_cast<floatx4*>(w.part_o + at * HD + 16 * d + 4 * g) = o[d];
-    if (g == 0) {
-      w.part_ml[2 * at] = m;
-      w.part_ml[2 * at + 1] = l;
-    }
+    if (g == 0) w.part_ml[at] = floatx4{m, l, lx, 0.0f};
   }
 }
 
@@ -806,23 +812,22 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? (RT == 8 ? 2 : 1) : RT == 2 ? 2
 constexpr int kFew = 16;
 
 struct Joined {
-  float m, l;
+  float m, l, lx;
   floatx4 acc;
 };
 
 // ranges first, first + hop, .. of row at0 (partials `stride` rows apart)
 __device__ __forceinline__ Joined join_ranges(const Work& w, size_t at0, size_t stride, int ns, int first, int hop, int hd, int d) {
-  Joined t{-INFINITY, 0.0f, floatx4{0.f, 0.f, 0.f, 0.f}};
+  Joined t{-INFINITY, 0.0f, 0.0f, floatx4{0.f, 0.f, 0.f, 0.f}};
   for (int s0 = first; s0 < ns; s0 += 4 * hop) {
-    floatx2 ml[4];
-    floatx4 v[4];
+    floatx4 ml[4], v[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int s = s0 + q * hop;
       const size_t at = at0 + (size_t)min(s, ns - 1) * stride;
-      ml[q] = *reinterpret_cast<const floatx2*>(w.part_ml + 2 * at);
+      ml[q] = w.part_ml[at];
       v[q] = *reinterpret_cast<const floatx4*>(w.part_o + at * hd + 4 * d);
-      if (s >= ns) ml[q] = floatx2{-INFINITY, 0.0f};
+      if (s >= ns) ml[q][0] = -INFINITY;
     }
     float mn = t.m;
 #pragma unroll
@@ -830,6 +835,7 @@ __device__ __forceinline__ Joined join_ranges(const Work& w, size_t at0, size_t 
     const float ms = mn == -INFINITY ? 0.0f : mn;
     const float f0 = __builtin_amdgcn_exp2f(t.m - ms);
     t.l *= f0;
+    t.lx *= f0;
     t.acc *= f0;
     t.m = mn;
 #pragma unroll
@@ -837,6 +843,7 @@ __device__ __forceinline__ Joined join_ranges(const Work& w, size_t at0, size_t 
       const float f = __builtin_amdgcn_exp2f(ml[q][0] - ms);
       if (f != 0.0f) {                            // (a range behind the last has weight 0, whatever lies there)
         t.l += ml[q][1] * f;
+        t.lx += ml[q][2] * f;
         t.acc += v[q] * f;
       }
     }
@@ -858,7 +865,7 @@ __global__ __launch_bounds__(256) void paged_join(Work w, int step) {
   const int ns = min(rq.y, w.pid_cap - rq.x), last = min(rows, first + step);
   constexpr int TPR = HD / 4, GR = 256 / TPR;
   __shared__ floatx4 part[GR][TPR];
-  __shared__ float gm[GR], gl[GR];
+  __shared__ float gm[GR], gl[GR], gx[GR];
   const int d = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const size_t stride = (size_t)w.unit * (16 * RT), base = ((size_t)rq.x * w.unit + rest) * (16 * RT);
   auto finish = [&](int r, const Joined& t) {
@@ -868,7 +875,7 @@ __global__ __launch_bounds__(256) void paged_join(Work w, int step) {
     uint2 pk = make_uint2(0u, 0u);
     if (t.l != 0.0f) pk = make_uint2(pack_bf16x2(t.acc[0] * inv, t.acc[1] * inv), pack_bf16x2(t.acc[2] * inv, t.acc[3] * inv));
     *reinterpret_cast<uint2*>(a.out + at * HD + 4 * d) = pk;
-    if (a.lse && d == 0) a.lse[at] = row_lse(t.m, t.l);
+    if (a.lse && d == 0) a.lse[at] = row_lse(t.m, t.lx);
   };
   if (ns <= kFew) {
     for (int r = first + grp; r < last; r += GR) finish(r, join_ranges(w, base + r, stride, ns, 0, 1, HD, d));
@@ -881,6 +888,7 @@ __global__ __launch_bounds__(256) void paged_join(Work w, int step) {
     if (d == 0) {
       gm[grp] = t.m;
       gl[grp] = t.l;
+      gx[grp] = t.lx;
     }
     __syncthreads();
     if (grp == 0) {
@@ -888,12 +896,13 @@ __global__ __launch_bounds__(256) void paged_join(Work w, int step) {
 #pragma unroll
       for (int q = 0; q < GR; ++q) t.m = fmaxf(t.m, gm[q]);
       const float ms = t.m == -INFINITY ? 0.0f : t.m;
-      t.l = 0.0f;
+      t.l = t.lx = 0.0f;
       t.acc = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int q = 0; q < GR; ++q) {
         const float f = __builtin_amdgcn_exp2f(gm[q] - ms);
         t.l += gl[q] * f;
+        t.lx += gx[q] * f;
         t.acc += part[q][d] * f;
       }
       finish(r, t);
@@ -932,23 +941,23 @@ Shape shape_of(int B, int max_q, int nh, int nkv, int hd) {
   s.off_count = al((size_t)B * sizeof(int2));
   s.off_plan = s.off_count + 256;
   s.off_ml = s.off_plan + al(((size_t)s.target / s.unit + B + 2) * sizeof(Item));
-  s.off_o = s.off_ml + al((size_t)s.pid_cap * s.unit * 16 * s.RT * 2 * sizeof(float));
+  s.off_o = s.off_ml + al((size_t)s.pid_cap * s.unit * 16 * s.RT * sizeof(floatx4));
   s.bytes = s.off_o + al((size_t)s.pid_cap * s.unit * 16 * s.RT * hd * sizeof(float));
   return s;
 }
 
-template <int HD, int RT, bool kSlots>
+template <int HD, int RT, bool kSlots, bool kLse>
 hipError_t launch_rows(const Work& w, int grid, hipStream_t stream) {
   if constexpr (RT > 1) {
     constexpr int lds = shared_lds<HD, RT>();
     if (lds > 64 * 1024) {
-      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&paged_shared<HD, RT, kSlots>),
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&paged_shared<HD, RT, kSlots, kLse>),
                                                hipFuncAttributeMaxDynamicSharedMemorySize, lds);
       if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((paged_shared<HD, RT, kSlots>), dim3(grid), dim3(64 * RT), lds, stream, w);
+    hipLaunchKernelGGL((paged_shared<HD, RT, kSlots, kLse>), dim3(grid), dim3(64 * RT), lds, stream, w);
   } else {
-    hipLaunchKernelGGL((paged_rows<HD, kSlots>), dim3(grid), dim3(64 * NW), 0, stream, w);
+    hipLaunchKernelGGL((paged_rows<HD, kSlots, kLse>), dim3(grid), dim3(64 * NW), 0, stream, w);
   }
   return hipGetLastError();
 }
@@ -956,7 +965,10 @@ hipError_t launch_rows(const Work& w, int grid, hipStream_t stream) {
 template <int HD, int RT>
 hipError_t launch(const Work& w, int64_t items, int max_kv, hipStream_t stream) {
   const int grid = (int)items;
-  const hipError_t e = w.a.page_shift < 4 ? launch_rows<HD, RT, true>(w, grid, stream) : launch_rows<HD, RT, false>(w, grid, stream);
+  const bool slots = w.a.page_shift < 4, lse = w.a.lse != nullptr;
+  const hipError_t e = slots ? lse ? launch_rows<HD, RT, true, true>(w, grid, stream) : launch_rows<HD, RT, true, false>(w, grid, stream)
+                       : lse ? launch_rows<HD, RT, false, true>(w, grid, stream)
+                             : launch_rows<HD, RT, false, false>(w, grid, stream);
   if (e != hipSuccess || max_kv <= w.whole) return e;
   const int rows = std::min(16 * RT, w.a.max_q * w.G);
   const int step = std::max(1, std::min(rows, (int)((int64_t)w.a.B * w.unit * rows / kJoinGroups)));
@@ -996,7 +1008,7 @@ hipError_t launch_paged_attention(const PagedArgs& a, int hd, void* workspace, h
   w.c = a.scale * kLog2e;
   char* base = static_cast<char*>(workspace);
   w.req = reinterpret_cast<int2*>(base + s.off_req);
-  w.part_ml = reinterpret_cast<float*>(base + s.off_ml);
+  w.part_ml = reinterpret_cast<floatx4*>(base + s.off_ml);
   w.part_o = reinterpret_cast<float*>(base + s.off_o);
   w.plan = nullptr;
   w.count = reinterpret_cast<int*>(base + s.off_count);

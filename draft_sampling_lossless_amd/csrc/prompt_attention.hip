@@ -107,6 +107,12 @@ __device__ bool find_tile(const Work& w, int u, int rows, int& start, int& n, in
   return false;
 }
 
+__device__ __forceinline__ float halves_sum(float v) {
+  uint32_t lo, hi;
+  halves_pair(__float_as_uint(v), lo, hi);
+  return __uint_as_float(lo) + __uint_as_float(hi);
+}
+
 // RW blocks of 32 rows a wave.  One pass of the loop holds the weights of tile t and the
 // scores of tile t + 1 at once, so that the first product of the next tile (matrix pipe)
 // runs beside the exponentials of this one (vector pipe).  K is read one tile ahead of V;
@@ -116,7 +122,7 @@ __device__ bool find_tile(const Work& w, int u, int rows, int& start, int& n, in
 // are rescaled on a row's first tile and hardly ever after.
 constexpr float kRaise = 8.0f;
 
-template <int HD, int RW, int NW, bool kCausal>
+template <int HD, int RW, int NW, bool kCausal, bool kLse>
 __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
   constexpr int KT = tile_keys(HD);         // keys per tile
   constexpr int SB = KT / 32, UG = KT / 16; // its score blocks, its groups of 16 keys
@@ -190,11 +196,11 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
   const uint16_t* vbase = a.v + (size_t)start * a.v_stride + (size_t)kvh * HD;
 
   floatx16 o[RW][HD / 32];
-  float m[RW], mb[RW], l[RW];               // mb: m, or 0 while a row has seen nothing
+  float m[RW], mb[RW], l[RW], lx[RW];       // mb: m, or 0 while a row has seen nothing; lx: l of unrounded weights
 #pragma unroll
   for (int b = 0; b < RW; ++b) {
     m[b] = -INFINITY;
-    mb[b] = l[b] = 0.0f;
+    mb[b] = l[b] = lx[b] = 0.0f;
 #pragma unroll
     for (int d = 0; d < HD / 32; ++d) o[b][d] = floatx16{};
   }
@@ -250,6 +256,7 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
         m[b] = mn;
         mb[b] = mn == -INFINITY ? 0.0f : mn;
         l[b] *= al;
+        lx[b] *= al;
 #pragma unroll
         for (int d = 0; d < HD / 32; ++d) o[b][d] *= al;
       }
@@ -261,9 +268,10 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
     float x[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[u >> 1][8 * (u & 1) + 4 * half + e], w.c, -mb[b]));
-    l[b] += (x[0] + x[1]) + (x[2] + x[3]);
+    if (kLse) lx[b] += (x[0] + x[1]) + (x[2] + x[3]);
     p[2 * half] = pack_bf16x2(x[0], x[1]);
     p[2 * half + 1] = pack_bf16x2(x[2], x[3]);
+    l[b] = add_bf16x2(p[2 * half + 1], add_bf16x2(p[2 * half], l[b]));
     asm volatile("" : "+v"(p[2 * half]), "+v"(p[2 * half + 1]));
   };
   auto as_frag = [](const uint32_t (&p)[4]) { return __builtin_bit_cast(bf16x8, make_uint4(p[0], p[1], p[2], p[3])); };
@@ -476,9 +484,7 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
 
 #pragma unroll
   for (int b = 0; b < RW; ++b) {
-    uint32_t lo, hi;
-    halves_pair(__float_as_uint(l[b]), lo, hi);
-    const float lt = __uint_as_float(lo) + __uint_as_float(hi);
+    const float lt = halves_sum(l[b]), lxt = kLse ? halves_sum(lx[b]) : 0.0f;
     if (!ok[b]) continue;
     const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
     const size_t at = (size_t)(start + row_j[b]) * a.nh + row_h[b];
@@ -490,27 +496,29 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
             lt == 0.0f ? make_uint2(0u, 0u)
                        : make_uint2(pack_bf16x2(o[b][d][4 * q] * inv, o[b][d][4 * q + 1] * inv),
                                     pack_bf16x2(o[b][d][4 * q + 2] * inv, o[b][d][4 * q + 3] * inv));
-    if (a.lse && hh == 0) a.lse[at] = row_lse(m[b], lt);
+    if (kLse && hh == 0) a.lse[at] = row_lse(m[b], lxt);
   }
 }
 
-template <int HD, int RW, int NW, bool kCausal>
+template <int HD, int RW, int NW, bool kCausal, bool kLse>
 hipError_t launch_one(const Work& w, hipStream_t stream) {
   const PromptArgs& a = w.a;
   constexpr int rows = 32 * RW * NW, lds = 6 * tile_keys(HD) * HD * 2;
   const int64_t tiles = ((int64_t)a.T * w.G + rows - 1) / rows + a.B;
   if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&prompt_rows<HD, RW, NW, kCausal>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&prompt_rows<HD, RW, NW, kCausal, kLse>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((prompt_rows<HD, RW, NW, kCausal>), dim3((unsigned)(tiles * a.nkv)), dim3(64 * NW), lds, stream, w);
+  hipLaunchKernelGGL((prompt_rows<HD, RW, NW, kCausal, kLse>), dim3((unsigned)(tiles * a.nkv)), dim3(64 * NW), lds, stream, w);
   return hipGetLastError();
 }
 
 template <int HD, int RW, int NW>
 hipError_t launch(const Work& w, hipStream_t stream) {
-  return w.a.causal ? launch_one<HD, RW, NW, true>(w, stream) : launch_one<HD, RW, NW, false>(w, stream);
+  if (w.a.lse)
+    return w.a.causal ? launch_one<HD, RW, NW, true, true>(w, stream) : launch_one<HD, RW, NW, false, true>(w, stream);
+  return w.a.causal ? launch_one<HD, RW, NW, true, false>(w, stream) : launch_one<HD, RW, NW, false, false>(w, stream);
 }
 
 }  // namespace
