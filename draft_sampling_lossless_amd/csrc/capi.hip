@@ -543,8 +543,8 @@ dspark_status dspark_paged_attention(const uint16_t* q, int64_t q_stride, const 
   REQUIRE((page_size & (page_size - 1)) == 0, DSPARK_ERR_UNSUPPORTED, "page_size must be a power of two (got %d)",
           page_size);
   REQUIRE(max_pages >= 1 && num_pages >= 1, DSPARK_ERR_INVALID, "max_pages and num_pages must be >= 1");
-  REQUIRE((int64_t)max_pages * page_size < ((int64_t)1 << 31) && (int64_t)num_pages * page_size < ((int64_t)1 << 31),
-          DSPARK_ERR_UNSUPPORTED, "max_pages * page_size and num_pages * page_size must be < 2^31");
+  REQUIRE((int64_t)max_pages * page_size <= ((int64_t)1 << 30) && (int64_t)num_pages * page_size < ((int64_t)1 << 31),
+          DSPARK_ERR_UNSUPPORTED, "max_pages * page_size must be <= 2^30 and num_pages * page_size < 2^31");
   REQUIRE(causal == 0 || causal == 1, DSPARK_ERR_INVALID, "causal must be 0 or 1 (got %d)", causal);
   if (T == 0) return ok();
   REQUIRE_PTR16(q, "q");

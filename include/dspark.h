@@ -458,11 +458,14 @@ dspark_status dspark_kv_append(const uint16_t* q, int64_t q_stride, const uint16
  *   cu_q[B], are left as they were.  A page outside [0, num_pages) hides its keys from
  *   every row; kv_len is taken as at most max_pages * page_size and at least 0.
  *   page_size a power of two; hd in {64, 128, 256}; nh % nkv == 0; nh <= 1024;
- *   1 <= B <= DSPARK_MAX_SEQS; 1 <= max_q <= DSPARK_MAX_BLOCK; num_pages * page_size and
- *   max_pages * page_size < 2^31; T * nh < 2^30; scale > 0 and finite; T == 0
+ *   1 <= B <= DSPARK_MAX_SEQS; 1 <= max_q <= DSPARK_MAX_BLOCK; num_pages * page_size < 2^31;
+ *   max_pages * page_size <= 2^30; T * nh < 2^30; scale > 0 and finite; T == 0
  *   enqueues nothing.
- *   Products on bf16 MFMA, accumulated in float32; softmax statistics and sums float32;
- *   the softmax weights are rounded to bf16 for the second product (its operand type).
+ *   Products on bf16 MFMA, accumulated in float32; softmax statistics and sums float32.
+ *   The softmax weights are rounded to bf16 for the second product (its operand type), and
+ *   the row is divided by the sum of the rounded weights; lse takes the unrounded ones.
+ *   Weights reach 2^8 before that division: values of magnitude up to 2^119 over the
+ *   number of keys stay finite.
  *   Long caches are split over workgroups and joined in a fixed order: results repeat
  *   bit for bit.  workspace >= dspark_paged_attention_workspace_size(...) bytes, device,
  *   16-byte aligned. */

@@ -66,6 +66,7 @@ def test_paged_validation(dspark_lib):
     assert _paged(page_size=0) == INVALID and _paged(page_size=24) == UNSUPPORTED
     assert _paged(max_pages=0) == INVALID and _paged(num_pages=0) == INVALID
     assert _paged(num_pages=1 << 27) == UNSUPPORTED and _paged(max_pages=1 << 27) == UNSUPPORTED
+    assert _paged(max_pages=(1 << 26) + 1) == UNSUPPORTED                # more than 2^30 keys of a request
     assert _paged(causal=2) == INVALID
     for name in ("q", "k_cache", "v_cache", "page_table", "kv_len", "cu_q", "out"):
         assert _paged(**{name: None}) == INVALID and name in _err()
