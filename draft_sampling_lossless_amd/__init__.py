@@ -562,8 +562,8 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: 
     of one product.  Returns q_out (None without q)."""
     dev = _device_of(k, "k")
     M, nkv, hd = k.shape
-    if k_cache.dim() != 3:
-        raise ValueError(f"k_cache must be [num_slots, nkv, hd], got shape {tuple(k_cache.shape)}")
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 3:
+        raise ValueError("k_cache must be a tensor [num_slots, nkv, hd]")
     S = k_cache.shape[0]
     ks, vs = _rows(k, "k", dev, M, nkv, hd), _rows(v, "v", dev, M, nkv, hd)
     nh = qs = qos = kos = 0
@@ -607,8 +607,9 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     dev = _device_of(q, "q")
     T, nh, hd = q.shape
     qs = _rows(q, "q", dev, T, nh, hd)
-    if k_cache.dim() != 3 or page_table.dim() != 2:
-        raise ValueError("k_cache must be [num_slots, nkv, hd] and page_table [B, max_pages]")
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 3 or not isinstance(page_table, torch.Tensor) \
+            or page_table.dim() != 2:
+        raise ValueError("k_cache must be a tensor [num_slots, nkv, hd] and page_table a tensor [B, max_pages]")
     S, nkv = k_cache.shape[0], k_cache.shape[1]
     B, width = page_table.shape
     if page_size < 1 or S % page_size:
@@ -620,7 +621,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if ws is None:
         ws = torch.empty(max(16, lib.dspark_paged_attention_workspace_size(T, B, max_q, nh, nkv, hd)),
                          dtype=torch.uint8, device=q.device)
-    elif ws.get_device() != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+    elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{dev}")
     _on(dev, "dspark_paged_attention", lib.dspark_paged_attention,
         q.data_ptr(), qs, _arg(k_cache, "k_cache", _BF16, dev, (S, nkv, hd)),
@@ -646,6 +647,8 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     nkv = k.shape[1]
     qs = _rows(q, "q", dev, T, nh, hd)
     ks, vs = _rows(k, "k", dev, T, nkv, hd), _rows(v, "v", dev, T, nkv, hd)
+    if not isinstance(cu_seqlens, torch.Tensor):
+        raise TypeError("cu_seqlens must be a torch.Tensor")
     B = cu_seqlens.numel() - 1
     if out is None:
         out = torch.empty((T, nh, hd), dtype=q.dtype, device=q.device)

@@ -1,5 +1,5 @@
-// Building blocks of the two attention kernels: bf16 packing, the finiteness test of
-// masked tiles, the online-softmax constants.
+// Building blocks of the two attention kernels: bf16 packing, loads into LDS, transposing
+// LDS reads, wave-uniform values.
 #pragma once
 
 #include "device.hpp"
@@ -39,11 +39,11 @@ __device__ __forceinline__ shortx4 lds_read_tr(const char* p) {
 // (s_waitcnt vmcnt, then a barrier) before a buffer is read.  It has no register result.
 __device__ __forceinline__ void load_to_lds16(const char* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-               : "memory");
+               : "memory", "m0");
 }
 // the same with an address of its own for every lane
 __device__ __forceinline__ void load_to_lds16(const char* src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
 }
 __device__ __forceinline__ uint32_t lds_address(const char* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;

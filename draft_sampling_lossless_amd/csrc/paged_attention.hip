@@ -485,7 +485,7 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
 
 // ------------------------------------------------------------------ many rows
 // The same work for more than 16 rows: a wave takes 16 rows, and all waves of the
-// workgroup share the keys, which pass through three or four LDS buffers of 32 (one worked
+// workgroup share the keys, which pass through three LDS buffers of 32 (one worked
 // on, the others filling straight from memory).  Rows lie there in 16-byte pieces permuted (piece p of
 // row r at p ^ swizzle(r)) so that the K reads (16 rows, one piece) and the transposing V
 // reads (8 rows, two pieces) touch every bank once.  The slots of kWindow keys (small
@@ -493,8 +493,7 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
 // registers and 52 KB of LDS leave room for three workgroups on a compute unit, which
 // cover each other's waits.
 constexpr int kWindow = 1024;
-// LDS buffers of a workgroup, and how many workgroups they leave room for
-constexpr int shared_stages(int RT) { return RT == 8 ? 4 : 3; }
+constexpr int kStages = 3;     // LDS buffers
 
 template <int HD>
 __device__ __forceinline__ int swizzle(int r) {
@@ -502,9 +501,9 @@ __device__ __forceinline__ int swizzle(int r) {
   return ((r & 7) << 1) | ((r >> 3) & 1);
 }
 
-template <int HD, int RT>
+template <int HD>
 constexpr int shared_lds() {
-  return shared_stages(RT) * 2 * KT * HD * 2 + kWindow * 4;
+  return kStages * 2 * KT * HD * 2 + kWindow * 4;
 }
 
 template <int HD, int RT, bool kSlots, bool kLse>
@@ -513,7 +512,6 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? (RT == 8 ? 2 : 1) : RT == 2 ? 2
   constexpr int LOADS = 2 * TILEB / 1024;         // 1 KB loads of one tile, K then V
   constexpr int LPW = (LOADS + RT - 1) / RT;      // of a wave (the last wave's may repeat the last load)
   constexpr int LR = 64 / PIECES;                 // rows of one load
-  constexpr int kStages = shared_stages(RT);
   extern __shared__ __attribute__((aligned(16))) char smem[];
   int32_t* slots = reinterpret_cast<int32_t*>(smem + kStages * 2 * TILEB);
   const PagedArgs& a = w.a;
@@ -949,7 +947,7 @@ Shape shape_of(int B, int max_q, int nh, int nkv, int hd) {
 template <int HD, int RT, bool kSlots, bool kLse>
 hipError_t launch_rows(const Work& w, int grid, hipStream_t stream) {
   if constexpr (RT > 1) {
-    constexpr int lds = shared_lds<HD, RT>();
+    constexpr int lds = shared_lds<HD>();
     if (lds > 64 * 1024) {
       const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&paged_shared<HD, RT, kSlots, kLse>),
                                                hipFuncAttributeMaxDynamicSharedMemorySize, lds);

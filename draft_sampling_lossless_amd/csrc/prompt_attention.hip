@@ -23,7 +23,6 @@ namespace dspark {
 
 namespace {
 
-
 // keys per tile: 16 KB of K and of V (8 KB for heads of 64)
 __host__ __device__ constexpr int tile_keys(int hd) { return hd > 128 ? 32 : 64; }
 
@@ -113,23 +112,23 @@ __device__ __forceinline__ float halves_sum(float v) {
   return __uint_as_float(lo) + __uint_as_float(hi);
 }
 
-// RW blocks of 32 rows a wave.  One pass of the loop holds the weights of tile t and the
+// 32 rows a wave.  One pass of the loop holds the weights of tile t and the
 // scores of tile t + 1 at once, so that the first product of the next tile (matrix pipe)
 // runs beside the exponentials of this one (vector pipe).  K is read one tile ahead of V;
-// three LDS buffers of K and two of V are filled straight from memory while the others are
+// four LDS buffers of K and two of V are filled straight from memory while the others are
 // in use, with one barrier a tile.  The running maximum is raised only when a row's scores exceed it
 // by kRaise (weights up to 2^kRaise, which neither float nor bf16 minds): the accumulators
 // are rescaled on a row's first tile and hardly ever after.
 constexpr float kRaise = 8.0f;
 
-template <int HD, int RW, int NW, bool kCausal, bool kLse>
+template <int HD, int NW, bool kCausal, bool kLse>
 __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
   constexpr int KT = tile_keys(HD);         // keys per tile
   constexpr int SB = KT / 32, UG = KT / 16; // its score blocks, its groups of 16 keys
   constexpr int PIECES = HD / 8;            // 16-byte pieces of a row
   constexpr int ROWB = HD * 2;
   constexpr int TILEB = KT * ROWB;
-  constexpr int WGROWS = 32 * RW * NW;
+  constexpr int WGROWS = 32 * NW;
   constexpr int LOADS = KT * PIECES / (64 * NW);   // 1 KB loads of a wave for one tile of K (or V)
   const PromptArgs& a = w.a;
   extern __shared__ __attribute__((aligned(16))) char smem[];   // four K tiles, two V tiles
@@ -139,29 +138,24 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
   if (!find_tile(w, blockIdx.x / a.nkv, WGROWS, start, n, tile)) return;
   const int lane = threadIdx.x & 63, col = lane & 31, hh = lane >> 5;
   const int wave = uniform(threadIdx.x >> 6);
-  const int r0 = tile * WGROWS, w0 = r0 + 32 * RW * wave;        // first row of the workgroup, of the wave
+  const int r0 = tile * WGROWS, w0 = r0 + 32 * wave;        // first row of the workgroup, of the wave
   const int ghigh = kCausal ? min(n, (r0 + WGROWS - 1) / w.G + 1) : n;
   const int nt = (ghigh + KT - 1) / KT;
   // tiles every row of the wave sees whole, and tiles some row sees at all
   const int wlow = kCausal ? min(n, w0 / w.G + 1) : n;
-  const int whigh = w0 / w.G >= n ? 0 : kCausal ? min(n, (w0 + 32 * RW - 1) / w.G + 1) : n;
+  const int whigh = w0 / w.G >= n ? 0 : kCausal ? min(n, (w0 + 31) / w.G + 1) : n;
   const int nsome = (whigh + KT - 1) / KT, nfull = min(wlow / KT, nsome);
 
-  int row_j[RW], row_h[RW], lim[RW];
-  bool ok[RW];
-  bf16x8 qf[RW][HD / 16];
-#pragma unroll
-  for (int b = 0; b < RW; ++b) {
-    const int row = w0 + 32 * b + col;
-    row_j[b] = row / w.G;
-    row_h[b] = kvh * w.G + row % w.G;
-    ok[b] = row_j[b] < n;
-    lim[b] = kCausal && ok[b] ? row_j[b] + 1 : n;                // keys below lim are seen
-    const uint16_t* src = a.q + (size_t)(start + (ok[b] ? row_j[b] : 0)) * a.q_stride + (size_t)(ok[b] ? row_h[b] : 0) * HD;
+  const int row = w0 + col, row_j = row / w.G, row_h = kvh * w.G + row % w.G;
+  const bool ok = row_j < n;
+  const int lim = kCausal && ok ? row_j + 1 : n;                 // keys below lim are seen
+  bf16x8 qf[HD / 16];
+  {
+    const uint16_t* src = a.q + (size_t)(start + (ok ? row_j : 0)) * a.q_stride + (size_t)(ok ? row_h : 0) * HD;
 #pragma unroll
     for (int kk = 0; kk < HD / 16; ++kk) {
       const uint4 v = *reinterpret_cast<const uint4*>(src + 16 * kk + 8 * hh);
-      qf[b][kk] = __builtin_bit_cast(bf16x8, ok[b] ? v : make_uint4(0, 0, 0, 0));
+      qf[kk] = __builtin_bit_cast(bf16x8, ok ? v : make_uint4(0, 0, 0, 0));
     }
   }
 
@@ -195,15 +189,10 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
   const uint16_t* kbase = a.k + (size_t)start * a.k_stride + (size_t)kvh * HD;
   const uint16_t* vbase = a.v + (size_t)start * a.v_stride + (size_t)kvh * HD;
 
-  floatx16 o[RW][HD / 32];
-  float m[RW], mb[RW], l[RW], lx[RW];       // mb: m, or 0 while a row has seen nothing; lx: l of unrounded weights
+  floatx16 o[HD / 32];
+  float m = -INFINITY, mb = 0.0f, l = 0.0f, lx = 0.0f;   // mb: m, or 0 while a row has seen nothing; lx: l of unrounded weights
 #pragma unroll
-  for (int b = 0; b < RW; ++b) {
-    m[b] = -INFINITY;
-    mb[b] = l[b] = lx[b] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < HD / 32; ++d) o[b][d] = floatx16{};
-  }
+  for (int d = 0; d < HD / 32; ++d) o[d] = floatx16{};
 
   // K operand kk of 32 rows: this lane's row, piece 2 kk + hh; the swizzle repeats every 16
   // rows, so the second 32 rows are a constant further, and kk only flips bits
@@ -211,17 +200,13 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
   auto key_frag = [&](const char* kb, int s, int kk) {
     return *reinterpret_cast<const bf16x8*>(kb + ((koff ^ (kk << 5)) + 32 * s * ROWB));
   };
-  auto scores = [&](floatx16 (&sc)[RW][SB], const char* kb) {
+  auto scores = [&](floatx16 (&sc)[SB], const char* kb) {
 #pragma unroll
     for (int s = 0; s < SB; ++s) {
+      sc[s] = floatx16{};
 #pragma unroll
-      for (int b = 0; b < RW; ++b) sc[b][s] = floatx16{};
-#pragma unroll
-      for (int kk = 0; kk < HD / 16; ++kk) {
-        const bf16x8 kf = key_frag(kb, s, kk);
-#pragma unroll
-        for (int b = 0; b < RW; ++b) sc[b][s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[b][kk], sc[b][s], 0, 0, 0);
-      }
+      for (int kk = 0; kk < HD / 16; ++kk)
+        sc[s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_frag(kb, s, kk), qf[kk], sc[s], 0, 0, 0);
     }
   };
   auto row_max = [&](const floatx16 (&sc)[SB]) {
@@ -234,44 +219,36 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
     halves_pair(__float_as_uint(top), lo, hi);
     return fmaxf(__uint_as_float(lo), __uint_as_float(hi)) * w.c;
   };
-  auto mask = [&](floatx16 (&sc)[RW][SB], int t) {
+  auto mask = [&](floatx16 (&sc)[SB], int t) {
 #pragma unroll
-    for (int b = 0; b < RW; ++b)
+    for (int s = 0; s < SB; ++s)
 #pragma unroll
-      for (int s = 0; s < SB; ++s)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (t * KT + 32 * s + 8 * (e >> 2) + 4 * hh + (e & 3) >= lim[b]) sc[b][s][e] = -INFINITY;
+      for (int e = 0; e < 16; ++e)
+        if (t * KT + 32 * s + 8 * (e >> 2) + 4 * hh + (e & 3) >= lim) sc[s][e] = -INFINITY;
   };
   // raise the maxima that tile t's scores exceed by too much
-  auto raise = [&](const float (&tm)[RW]) {
-    bool up = false;
+  auto raise = [&](float tm) {
+    if (uniform(__any(tm > m + kRaise))) {
+      const float mn = tm > m + kRaise ? tm : m;
+      const float al = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      mb = mn == -INFINITY ? 0.0f : mn;
+      l *= al;
+      lx *= al;
 #pragma unroll
-    for (int b = 0; b < RW; ++b) up |= tm[b] > m[b] + kRaise;
-    if (uniform(__any(up))) {
-#pragma unroll
-      for (int b = 0; b < RW; ++b) {
-        const float mn = tm[b] > m[b] + kRaise ? tm[b] : m[b];
-        const float al = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[b] - mn);
-        m[b] = mn;
-        mb[b] = mn == -INFINITY ? 0.0f : mn;
-        l[b] *= al;
-        lx[b] *= al;
-#pragma unroll
-        for (int d = 0; d < HD / 32; ++d) o[b][d] *= al;
-      }
+      for (int d = 0; d < HD / 32; ++d) o[d] *= al;
     }
   };
   // weights of keys 16 u .. 16 u + 15 of the tile, rounded to bf16 (the second product's
   // operand type), and their sum
-  auto weights = [&](const floatx16 (&sc)[SB], int b, int u, int half, uint32_t (&p)[4]) {
+  auto weights = [&](const floatx16 (&sc)[SB], int u, int half, uint32_t (&p)[4]) {
     float x[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[u >> 1][8 * (u & 1) + 4 * half + e], w.c, -mb[b]));
-    if (kLse) lx[b] += (x[0] + x[1]) + (x[2] + x[3]);
+    for (int e = 0; e < 4; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[u >> 1][8 * (u & 1) + 4 * half + e], w.c, -mb));
+    if (kLse) lx += (x[0] + x[1]) + (x[2] + x[3]);
     p[2 * half] = pack_bf16x2(x[0], x[1]);
     p[2 * half + 1] = pack_bf16x2(x[2], x[3]);
-    l[b] = add_bf16x2(p[2 * half + 1], add_bf16x2(p[2 * half], l[b]));
+    l = add_bf16x2(p[2 * half + 1], add_bf16x2(p[2 * half], l));
     asm volatile("" : "+v"(p[2 * half]), "+v"(p[2 * half + 1]));
   };
   auto as_frag = [](const uint32_t (&p)[4]) { return __builtin_bit_cast(bf16x8, make_uint4(p[0], p[1], p[2], p[3])); };
@@ -317,15 +294,15 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
   // barrier) and an equal share of the vector work
   constexpr int KG = SB * (HD / 16) / 4, VG = HD / 32;
   bf16x8 kf[2][KG];
-  auto step = [&](floatx16 (&cur)[RW][SB], floatx16 (&nxt)[RW][SB]) {
+  auto step = [&](floatx16 (&cur)[SB], floatx16 (&nxt)[SB]) {
     open_tile();
     if (uniform((t + 4) * KT > n && t + 3 < nt)) cut(koffs, a.k_stride, t + 3);
     if (uniform((t + 2) * KT > n && t + 1 < nt)) cut(voffs, a.v_stride, t + 1);
     fresh();
     const char* kb = kbuf_of(t + 1);
     const char* vb = vbuf_of(t);
-    uint32_t p[RW][UG][4];
-    float tm[RW];
+    uint32_t p[UG][4];
+    float tm = 0.0f;
     VFrag vf[2][VG];
 #pragma unroll
     for (int gq = 0; gq < 4; ++gq) {
@@ -339,20 +316,15 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
 #pragma unroll
         for (int i = 0; i < VG; ++i) vf[0][i] = value_frag(vb, 0, i);
       }
+      if (gq == 0)
 #pragma unroll
-      for (int b = 0; b < RW; ++b) {
-        if (gq == 0)
+        for (int s = 0; s < SB; ++s) nxt[s] = floatx16{};
+      weights(cur, gq >> 1, gq & 1, p[gq >> 1]);
 #pragma unroll
-          for (int s = 0; s < SB; ++s) nxt[b][s] = floatx16{};
-        weights(cur[b], b, gq >> 1, gq & 1, p[b][gq >> 1]);
+      for (int i = 0; i < KG; ++i) {
+        const int f = gq * KG + i;
+        nxt[f % SB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[gq & 1][i], qf[f / SB], nxt[f % SB], 0, 0, 0);
       }
-#pragma unroll
-      for (int i = 0; i < KG; ++i)
-#pragma unroll
-        for (int b = 0; b < RW; ++b) {
-          const int f = gq * KG + i;
-          nxt[b][f % SB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[gq & 1][i], qf[b][f / SB], nxt[b][f % SB], 0, 0, 0);
-        }
       __builtin_amdgcn_sched_barrier(0);
       // the loads to come, spread over the tile: all at once they would hold up every wave
       if (uniform(t + 3 < nt)) {
@@ -370,21 +342,15 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
 #pragma unroll
         for (int i = 0; i < KG; ++i) kf[0][i] = key_frag(kbuf_of(t + 2), i % SB, i / SB);
       }
-#pragma unroll
-      for (int b = 0; b < RW; ++b) {
-        if (UG > 2 && u == 0) {
-          weights(cur[b], b, 2, 0, p[b][2]);
-          weights(cur[b], b, 2, 1, p[b][2]);
-        } else if (UG > 2 && u < 3) {
-          weights(cur[b], b, 3, u - 1, p[b][3]);
-        }
-        if (u == UG - 1) tm[b] = row_max(nxt[b]);
+      if (UG > 2 && u == 0) {
+        weights(cur, 2, 0, p[2]);
+        weights(cur, 2, 1, p[2]);
+      } else if (UG > 2 && u < 3) {
+        weights(cur, 3, u - 1, p[3]);
       }
+      if (u == UG - 1) tm = row_max(nxt);
 #pragma unroll
-      for (int d = 0; d < VG; ++d)
-#pragma unroll
-        for (int b = 0; b < RW; ++b)
-          o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[u & 1][d].v, as_frag(p[b][u]), o[b][d], 0, 0, 0);
+      for (int d = 0; d < VG; ++d) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[u & 1][d].v, as_frag(p[u]), o[d], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
       if (uniform(t + 1 < nt)) {
 #pragma unroll
@@ -395,15 +361,12 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
     ++t;
     if (uniform(t < nfull)) raise(tm);      // (the scores of a tile seen in part are formed again, masked)
   };
-  floatx16 sa[RW][SB];
+  floatx16 sa[SB];
   open_tile();
   if (uniform(nfull > 0)) {
-    floatx16 sb[RW][SB];
-    float tm[RW];
+    floatx16 sb[SB];
     scores(sa, kbuf_of(0));
-#pragma unroll
-    for (int b = 0; b < RW; ++b) tm[b] = row_max(sa[b]);
-    raise(tm);
+    raise(row_max(sa));
 #pragma unroll
     for (int i = 0; i < KG; ++i) kf[0][i] = key_frag(kbuf_of(1), i % SB, i / SB);
     while (true) {
@@ -421,26 +384,18 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
     if (t + 1 < nt) fetch(vbase, a.v_stride, voffs, t + 1, vbuf_of(t + 1));
     if (uniform(t < nsome)) {
       const char* vb = vbuf_of(t);
-      float tm[RW];
       scores(sa, kbuf_of(t));
       mask(sa, t);
-#pragma unroll
-      for (int b = 0; b < RW; ++b) tm[b] = row_max(sa[b]);
-      raise(tm);
+      raise(row_max(sa));
 #pragma unroll
       for (int u = 0; u < UG; ++u) {
         const int first = t * KT + 16 * u;
         if (uniform(first >= whigh)) continue;
-        bf16x8 p[RW];
         VFrag f[HD / 32];
-        uint32_t top = 0;                   // the largest exponent, in the high half
-#pragma unroll
-        for (int b = 0; b < RW; ++b) {
-          uint32_t pw[4];
-          weights(sa[b], b, u, 0, pw);
-          weights(sa[b], b, u, 1, pw);
-          p[b] = as_frag(pw);
-        }
+        uint32_t pw[4], top = 0;            // top: the largest exponent, in the high half
+        weights(sa, u, 0, pw);
+        weights(sa, u, 1, pw);
+        const bf16x8 p = as_frag(pw);
 #pragma unroll
         for (int d = 0; d < HD / 32; ++d) f[d] = value_frag(vb, u, d);
         if (uniform(first + 16 > wlow)) {
@@ -455,9 +410,7 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
         }
         if (!uniform(__any(top >= 0x7F800000u))) {
 #pragma unroll
-          for (int d = 0; d < HD / 32; ++d)
-#pragma unroll
-            for (int b = 0; b < RW; ++b) o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[d].v, p[b], o[b][d], 0, 0, 0);
+          for (int d = 0; d < HD / 32; ++d) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[d].v, p, o[d], 0, 0, 0);
         } else {
           // key by key, added only to the rows that see it
 #pragma unroll 1
@@ -470,11 +423,8 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
               const bf16x8 one = __builtin_bit_cast(
                   bf16x8, make_uint4(jj / 2 == 0 ? f[d].w[0] & keep : 0u, jj / 2 == 1 ? f[d].w[1] & keep : 0u,
                                      jj / 2 == 2 ? f[d].w[2] & keep : 0u, jj / 2 == 3 ? f[d].w[3] & keep : 0u));
-#pragma unroll
-              for (int b = 0; b < RW; ++b) {
-                const floatx16 add = __builtin_amdgcn_mfma_f32_32x32x16_bf16(one, p[b], floatx16{}, 0, 0, 0);
-                if (first + k < lim[b]) o[b][d] += add;
-              }
+              const floatx16 add = __builtin_amdgcn_mfma_f32_32x32x16_bf16(one, p, floatx16{}, 0, 0, 0);
+              if (first + k < lim) o[d] += add;
             }
           }
         }
@@ -482,43 +432,40 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
     }
   }
 
+  const float lt = halves_sum(l), lxt = kLse ? halves_sum(lx) : 0.0f;
+  if (!ok) return;
+  const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
+  const size_t at = (size_t)(start + row_j) * a.nh + row_h;
 #pragma unroll
-  for (int b = 0; b < RW; ++b) {
-    const float lt = halves_sum(l[b]), lxt = kLse ? halves_sum(lx[b]) : 0.0f;
-    if (!ok[b]) continue;
-    const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
-    const size_t at = (size_t)(start + row_j[b]) * a.nh + row_h[b];
+  for (int d = 0; d < HD / 32; ++d)
 #pragma unroll
-    for (int d = 0; d < HD / 32; ++d)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<uint2*>(a.out + at * HD + 32 * d + 8 * q + 4 * hh) =
-            lt == 0.0f ? make_uint2(0u, 0u)
-                       : make_uint2(pack_bf16x2(o[b][d][4 * q] * inv, o[b][d][4 * q + 1] * inv),
-                                    pack_bf16x2(o[b][d][4 * q + 2] * inv, o[b][d][4 * q + 3] * inv));
-    if (kLse && hh == 0) a.lse[at] = row_lse(m[b], lxt);
-  }
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<uint2*>(a.out + at * HD + 32 * d + 8 * q + 4 * hh) =
+          lt == 0.0f ? make_uint2(0u, 0u)
+                     : make_uint2(pack_bf16x2(o[d][4 * q] * inv, o[d][4 * q + 1] * inv),
+                                  pack_bf16x2(o[d][4 * q + 2] * inv, o[d][4 * q + 3] * inv));
+  if (kLse && hh == 0) a.lse[at] = row_lse(m, lxt);
 }
 
-template <int HD, int RW, int NW, bool kCausal, bool kLse>
+template <int HD, int NW, bool kCausal, bool kLse>
 hipError_t launch_one(const Work& w, hipStream_t stream) {
   const PromptArgs& a = w.a;
-  constexpr int rows = 32 * RW * NW, lds = 6 * tile_keys(HD) * HD * 2;
+  constexpr int rows = 32 * NW, lds = 6 * tile_keys(HD) * HD * 2;
   const int64_t tiles = ((int64_t)a.T * w.G + rows - 1) / rows + a.B;
   if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&prompt_rows<HD, RW, NW, kCausal, kLse>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&prompt_rows<HD, NW, kCausal, kLse>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((prompt_rows<HD, RW, NW, kCausal, kLse>), dim3((unsigned)(tiles * a.nkv)), dim3(64 * NW), lds, stream, w);
+  hipLaunchKernelGGL((prompt_rows<HD, NW, kCausal, kLse>), dim3((unsigned)(tiles * a.nkv)), dim3(64 * NW), lds, stream, w);
   return hipGetLastError();
 }
 
-template <int HD, int RW, int NW>
+template <int HD, int NW>
 hipError_t launch(const Work& w, hipStream_t stream) {
   if (w.a.lse)
-    return w.a.causal ? launch_one<HD, RW, NW, true, true>(w, stream) : launch_one<HD, RW, NW, false, true>(w, stream);
-  return w.a.causal ? launch_one<HD, RW, NW, true, false>(w, stream) : launch_one<HD, RW, NW, false, false>(w, stream);
+    return w.a.causal ? launch_one<HD, NW, true, true>(w, stream) : launch_one<HD, NW, false, true>(w, stream);
+  return w.a.causal ? launch_one<HD, NW, true, false>(w, stream) : launch_one<HD, NW, false, false>(w, stream);
 }
 
 }  // namespace
@@ -529,9 +476,9 @@ hipError_t launch_prompt_attention(const PromptArgs& a, int hd, hipStream_t stre
   w.G = a.nh / a.nkv;
   w.c = a.scale * kLog2e;
   switch (hd) {
-    case 64: return launch<64, 1, 8>(w, stream);
-    case 128: return launch<128, 1, 8>(w, stream);
-    case 256: return launch<256, 1, 4>(w, stream);
+    case 64: return launch<64, 8>(w, stream);
+    case 128: return launch<128, 8>(w, stream);
+    case 256: return launch<256, 4>(w, stream);
     default: return hipErrorInvalidValue;
   }
 }
