@@ -4,13 +4,16 @@
 Bounds.  A rounding to bf16 is off by at most 2^-8 of the value.
   * append: one such rounding of the output, and float32 work of a few tens of operations
     on the pair (x, y): |err| <= 2^-8 |ref| + 2^-18 sqrt(x^2 + y^2).
-  * attention: the output's rounding, 2^-8 |ref|; the weights' rounding, 2^-8 sum p|v|
-    =: 2^-8 A; and float32 errors, each relative to A: a score of magnitude at most
+  * attention: the output's rounding, 2^-8 |ref|; the weights' rounding: with weights
+    p (1 + d), |d| <= 2^-8, in the numerator and in the sum that divides it, the row is off
+    by |sum p d v - ref sum p d| / sum p (1 + d) <= 2^-8 (A + |ref|) / (1 - 2^-8), A = sum p|v|;
+    and float32 errors, each relative to A: a score of magnitude at most
     D = max scale sum|q||k| is off by e_s <= (hd + 4) 2^-24 D (accumulation and scaling)
     and moves a weight by e_s, its exponential by 2^-22 (argument and hardware rounding,
     up to 2^-23 of the argument's magnitude 2 D log2 e), numerator and denominator both; the sums
     over n keys are off by n 2^-24 each.  Together
-        |err| <= 2^-8 |ref| + A (2^-8 + 2 e_s + 2^-20 (1 + D) + 2 n 2^-24) (1 + 2^-7).
+        |err| <= 2^-8 |ref| + (2^-8 |ref| + A (2^-8 + 2 e_s + 2^-20 (1 + D) + 2 n 2^-24)) (1 + 2^-6),
+    the last factor over (1 + 2^-8) / (1 - 2^-8): the output's rounding of the other errors.
   * lse: e_s + 2^-21 (1 + D) + n 2^-24 + 2^-22 |ref|.
 """
 import numpy as np
@@ -55,7 +58,7 @@ def check_rows(out, lse, ref, hd, label=""):
     n = ref["keys"][w][:, None]
     es = (hd + 4) * 2.0 ** -24 * dot
     rel = 2.0 ** -8 + 2 * es + 2.0 ** -20 * (1 + dot) + 2 * n * 2.0 ** -24
-    tol = 2.0 ** -8 * np.abs(want) + mag * rel[..., None] * (1 + 2.0 ** -7)
+    tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -8 * np.abs(want) + mag * rel[..., None]) * (1 + 2.0 ** -6)
     err = np.abs(got - want)
     bad = ~(err <= tol)
     assert not bad.any(), (f"{label}: {int(bad.sum())} of {bad.size} outside the bound, first at "
@@ -201,6 +204,13 @@ def ref_paged(c, causal, scale=None):
     (24, 8, 64, 32, [5, 0, 2], [50, 60, 1100], True),         # a request without query tokens
     (8, 2, 128, 16, [2, 1, 3], [0, 0, 2], True),              # nothing cached; fewer keys than query tokens
     (8, 2, 128, 16, [2, 1], [0, 40], False),
+    (8, 1, 256, 16, [3], [150], True),                        # 24, 64 and 128 rows of 256
+    (8, 1, 256, 1, [8, 2], [700, 65], True),
+    (8, 1, 256, 32, [16, 16], [90, 300], True),
+    (8, 1, 64, 16, [3], [150], True),                         # the same of 64
+    (8, 1, 64, 1, [6, 2], [700, 65], False),
+    (8, 1, 64, 32, [8, 8], [90, 300], True),
+    (512, 1, 64, 16, [2], [70], True),                        # more heads on one than a row block
 ])
 def test_paged(nh, nkv, hd, page, qlen, kvlen, causal):
     say(f"paged nh={nh} nkv={nkv} hd={hd} page={page} q={qlen} kv={kvlen} causal={causal}")
@@ -222,6 +232,89 @@ def test_paged_many_requests(B):
     c = paged_case(g, 4, 2, 64, 16, qlen, kvlen)
     out, lse = run_paged(c, True)
     check_rows(out, lse, ref_paged(c, True), 64, "paged")
+
+
+def test_paged_most_requests():
+    """DSPARK_MAX_SEQS requests, most of one token over few keys, some of none, some long."""
+    g = np.random.default_rng(41)
+    B = 4096
+    qlen, kvlen = (g.random(B) < 0.9).astype(int).tolist(), g.integers(0, 9, B).tolist()
+    for b in (0, 1023, 1024, 4095):
+        qlen[b], kvlen[b] = 2, 1500
+    say(f"paged B={B}, {sum(qlen)} tokens")
+    c = paged_case(g, 2, 1, 64, 4, qlen, kvlen)
+    out, lse = run_paged(c, True)
+    check_rows(out, lse, ref_paged(c, True), 64, "paged")
+
+
+def test_paged_more_keys_than_a_window_of_slots():
+    """70 requests of 20 rows over 2100 keys each, found slot by slot: a workgroup takes a
+    request whole and looks its slots up in parts.  A value that is not finite in the last
+    part is kept from the rows that do not see it, and the other tokens are checked."""
+    g = np.random.default_rng(42)
+    B, nh, nkv, hd, n, kv = 70, 32, 8, 64, 5, 2100
+    S = B * kv
+    say(f"paged B={B} kv={kv} slots")
+    kc, vc = bits(g, S, nkv, hd), bits(g, S, nkv, hd)
+    table = g.permutation(S).astype(np.int32).reshape(B, kv)
+    c = dict(q=bits(g, B * n, nh, hd, std=2.0), kc=kc, vc=vc, table=table, kv=np.full(B, kv, np.int32),
+             cu=(np.arange(B + 1) * n).astype(np.int32), page=1, hd=hd, max_q=n)
+    table[7, 1500] = -1                                   # a key without a slot, in the second part
+    kc[table[7, kv - 2]], vc[table[7, kv - 2]] = NAN, INF   # seen by the last two tokens of request 7
+    out, lse = run_paged(c, True)
+    for b in (0, 7, 69):
+        d = dict(c, q=c["q"][b * n:(b + 1) * n], table=table[b:b + 1], kv=c["kv"][:1], cu=np.array([0, n], np.int32))
+        ref, o, ls = ref_paged(d, True), out[b * n:(b + 1) * n], lse[b * n:(b + 1) * n]
+        if b == 7:
+            assert np.isnan(value(o)[n - 2:]).all()
+            ref = {k: v[:n - 2] for k, v in ref.items()}
+            o, ls = o[:n - 2], ls[:n - 2]
+        check_rows(o, ls, ref, hd, f"request {b}")
+
+
+@pytest.mark.parametrize("nh,nkv,hd,page,qlen,kvlen,causal", [
+    (8, 2, 64, 16, [4, 1], [300, 70], True),
+    (8, 2, 256, 1, [2, 1], [300, 900], False),
+    (16, 2, 64, 1, [4, 1], [300, 70], True),
+    (16, 2, 128, 32, [16, 2], [2000, 70], False),
+    (16, 2, 256, 16, [7], [100], True),
+])
+def test_attention_without_lse_is_the_same(nh, nkv, hd, page, qlen, kvlen, causal):
+    g = np.random.default_rng(43)
+    c = paged_case(g, nh, nkv, hd, page, qlen, kvlen)
+    assert torch.equal(run_paged(c, causal)[0], run_paged(c, causal, lse=False)[0])
+    T = sum(kvlen)
+    q, k, v = bits(g, T, nh, hd, std=2.0), bits(g, T, nkv, hd), bits(g, T, nkv, hd)
+    cu = np.concatenate([[0], np.cumsum(kvlen)]).astype(np.int32)
+    want, _ = run_prompt(q, k, v, cu, causal)
+    assert torch.equal(dsl.prompt_attention(dev(q), dev(k), dev(v), dev(cu), causal=causal), want)
+
+
+def test_paged_a_page_listed_twice():
+    g = np.random.default_rng(44)
+    for qlen in ([2], [6]):                               # both kernels
+        c = paged_case(g, 8, 2, 128, 16, qlen, [100])
+        c["table"][0, 3] = c["table"][0, 5] = c["table"][0, 0]
+        out, lse = run_paged(c, True)
+        check_rows(out, lse, ref_paged(c, True), 128, str(qlen))
+
+
+def test_paged_two_calls_at_once():
+    """Calls on two streams, each with its workspace, split and joined at the same time."""
+    g = np.random.default_rng(45)
+    cases = [paged_case(g, 8, 2, 128, 16, [1, 2], [3000, 900]), paged_case(g, 8, 2, 128, 1, [7, 6], [2500, 1700])]
+    want = [run_paged(c, True)[0] for c in cases]
+    args = [[dev(c[k]) for k in ("q", "kc", "vc", "table", "kv", "cu")] for c in cases]
+    outs = [torch.empty_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, a, o, s in zip(cases, args, outs, streams):
+            with torch.cuda.stream(s):
+                dsl.paged_attention(*a, c["max_q"], c["page"], out=o)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
 
 
 def test_paged_unseen_keys_do_not_matter():
@@ -262,6 +355,22 @@ def test_paged_pages_outside_the_cache_hide_their_keys():
     assert not value(out).any() and np.isneginf(host(lse)).all()
 
 
+@pytest.mark.parametrize("page", [1, 16, 64])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_paged_pages_outside_the_cache_hide_their_keys_from_many_rows(page, hd):
+    g = np.random.default_rng(46)
+    c = paged_case(g, 8, 2, hd, page, [6, 5], [700, 90])
+    pages = c["kc"].shape[0] // page
+    for b, p, to in ((0, 0, -1), (0, 3, 2 ** 31 - 1), (1, 1, pages), (1, 0, -2 ** 31), (0, c["table"].shape[1] - 1, -1)):
+        c["table"][b, p] = to
+    out, lse = run_paged(c, True)
+    check_rows(out, lse, ref_paged(c, True), hd)
+    c["table"][0] = pages                                 # every page of one request
+    out, lse = run_paged(c, True)
+    check_rows(out, lse, ref_paged(c, True), hd)
+    assert not value(out)[:6].any() and np.isneginf(host(lse)[:6]).all()
+
+
 def test_paged_lengths_beyond_the_table_and_rows_behind():
     g = np.random.default_rng(11)
     c = paged_case(g, 8, 2, 128, 16, [2, 3], [64, 40])
@@ -280,6 +389,13 @@ def test_paged_lengths_beyond_the_table_and_rows_behind():
     out, _ = run_paged(c, True, max_q=2)
     assert np.all(host(out)[2:] == SENT)
     ref["written"][2:] = False
+    check_rows(out, None, ref, 128)
+    c = paged_case(g, 8, 2, 128, 16, [9, 7], [64, 900])          # more than 16 rows
+    ref = ref_paged(c, True)
+    out, _ = run_paged(c, True, max_q=6)
+    for lo, hi in ((6, 9), (15, 16)):
+        assert np.all(host(out)[lo:hi] == SENT)
+        ref["written"][lo:hi] = False
     check_rows(out, None, ref, 128)
 
 
@@ -362,6 +478,32 @@ def test_paged_strided_queries_streams_and_graph():
         assert torch.equal(out, run_paged(d, True)[0])
 
 
+def test_paged_block_captured_and_replayed():
+    """More than 16 rows, planned and joined on the device: lengths, pages and counts of
+    query tokens change between replays, and the program's own calls run in between."""
+    g = np.random.default_rng(47)
+    c = paged_case(g, 8, 2, 64, 1, [9, 9, 9], [1400, 600, 1100])
+    a = [dev(c[k]) for k in ("q", "kc", "vc", "table", "kv", "cu")]
+    out = torch.empty((27, 8, 64), dtype=torch.int16, device="cuda")
+    ws = torch.empty(dsl.paged_attention_workspace_size(27, 3, 9, 8, 2, 64), dtype=torch.uint8, device="cuda")
+    dsl.paged_attention(*a, 9, 1, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dsl.paged_attention(*a, 9, 1, out=out, workspace=ws)
+    for kv, cu in (([1400, 600, 1100], [0, 9, 18, 27]), ([9, 600, 3], [0, 5, 5, 14]), ([0, 33, 1100], [0, 1, 9, 18]),
+                   ([1400, 600, 1100], [0, 9, 18, 27])):
+        d = dict(c, kv=np.array(kv, np.int32), cu=np.array(cu, np.int32))
+        d["table"] = np.ascontiguousarray(c["table"][:, ::-1]) if kv[0] == 9 else c["table"]
+        for t, x in zip(a[3:], (d["table"], d["kv"], d["cu"])):
+            t.copy_(dev(x))
+        out.fill_(SENT)
+        want, _ = run_paged(d, True)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 # ---------------------------------------------------------------- prompt attention
 
 def run_prompt(q, k, v, cu, causal, scale=None):
@@ -384,6 +526,7 @@ def run_prompt(q, k, v, cu, causal, scale=None):
     (4, 2, 256, [150, 31]),
     (2, 2, 256, [65]),
     (4, 2, 128, [700]),                     # several key tiles and row tiles
+    (512, 1, 64, [2, 3]),                   # a token's heads are more than a row tile
 ])
 @pytest.mark.parametrize("causal", [True, False])
 def test_prompt(nh, nkv, hd, lens, causal):
