@@ -5,7 +5,9 @@
 // in one pass over a sequence's keys with a running maximum and sum.  The rows of a
 // product are (token, head) pairs of one kv head, token-major: the nh / nkv heads that
 // share keys share their tiles too.  A workgroup takes 32 NW rows, a wave 32, and keys
-// and values pass through LDS in tiles of 64 tokens.
+// and values pass through LDS in tiles of KT tokens.  One causal prompt of 8192 tokens, 32/8
+// heads of 128: 525 us, 1050 TFLOP/s (1110 without the mask), bound by the matrix pipe and
+// the exponentials and packing beside it; short sequences by their loads and stores.
 //
 // Scores are formed transposed, S^T = K Q^T, with v_mfma_f32_32x32x16_bf16: lane
 // (h, n) = (lane / 32, lane % 32) holds row n and the keys 8 (i / 4) + 4 h + i % 4 of
@@ -22,9 +24,6 @@
 namespace dspark {
 
 namespace {
-
-// keys per tile: 16 KB of K and of V (8 KB for heads of 64)
-__host__ __device__ constexpr int tile_keys(int hd) { return hd > 128 ? 32 : 64; }
 
 struct Work {
   PromptArgs a;
@@ -112,19 +111,18 @@ __device__ __forceinline__ float halves_sum(float v) {
   return __uint_as_float(lo) + __uint_as_float(hi);
 }
 
-// 32 rows a wave.  One pass of the loop holds the weights of tile t and the
-// scores of tile t + 1 at once, so that the first product of the next tile (matrix pipe)
-// runs beside the exponentials of this one (vector pipe).  K is read one tile ahead of V;
-// four LDS buffers of K and two of V are filled straight from memory while the others are
-// in use, with one barrier a tile.  The running maximum is raised only when a row's scores exceed it
-// by kRaise (weights up to 2^kRaise, which neither float nor bf16 minds): the accumulators
-// are rescaled on a row's first tile and hardly ever after.
+// 32 rows a wave.  One pass of the loop holds the weights of tile t and the scores of tile
+// t + 1 at once, so that the first product of the next tile (matrix pipe) runs beside the
+// exponentials of this one (vector pipe).  K is read one tile ahead of V; four LDS buffers
+// of K and two of V are filled straight from memory while the others are in use, with one
+// barrier a tile.  The running maximum is raised only when a row's scores exceed it by
+// kRaise (weights up to 2^kRaise, which neither float nor bf16 minds): the accumulators are
+// rescaled on a row's first tile and hardly ever after.
 constexpr float kRaise = 8.0f;
 
-template <int HD, int NW, bool kCausal, bool kLse>
-__global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
-  constexpr int KT = tile_keys(HD);         // keys per tile
-  constexpr int SB = KT / 32, UG = KT / 16; // its score blocks, its groups of 16 keys
+template <int HD, int NW, int KT, bool kCausal, bool kLse>
+__global__ __launch_bounds__(64 * NW, HD > 128 ? 1 : 2) void prompt_rows(Work w) {
+  constexpr int SB = KT / 32, UG = KT / 16; // score blocks of a tile of KT keys, its groups of 16 keys
   constexpr int PIECES = HD / 8;            // 16-byte pieces of a row
   constexpr int ROWB = HD * 2;
   constexpr int TILEB = KT * ROWB;
@@ -149,15 +147,6 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
   const int row = w0 + col, row_j = row / w.G, row_h = kvh * w.G + row % w.G;
   const bool ok = row_j < n;
   const int lim = kCausal && ok ? row_j + 1 : n;                 // keys below lim are seen
-  bf16x8 qf[HD / 16];
-  {
-    const uint16_t* src = a.q + (size_t)(start + (ok ? row_j : 0)) * a.q_stride + (size_t)(ok ? row_h : 0) * HD;
-#pragma unroll
-    for (int kk = 0; kk < HD / 16; ++kk) {
-      const uint4 v = *reinterpret_cast<const uint4*>(src + 16 * kk + 8 * hh);
-      qf[kk] = __builtin_bit_cast(bf16x8, ok ? v : make_uint4(0, 0, 0, 0));
-    }
-  }
 
   // LDS slot q of a tile (row q / PIECES) takes the piece swizzled into it.  The tile's
   // base is a scalar, a lane's offset into it 32 bits (token strides stay below 2^24); a
@@ -189,6 +178,25 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
   const uint16_t* kbase = a.k + (size_t)start * a.k_stride + (size_t)kvh * HD;
   const uint16_t* vbase = a.v + (size_t)start * a.v_stride + (size_t)kvh * HD;
 
+  // K tile t lies in buffer t % 4, V tile t in buffer t % 2; during tile t the loads of
+  // K t + 3 and V t + 1 are in flight
+  char* const vbuf = smem + 4 * TILEB;
+  auto kbuf_of = [&](int t) { return smem + (t & 3) * TILEB; };
+  auto vbuf_of = [&](int t) { return vbuf + (t & 1) * TILEB; };
+  fetch(kbase, a.k_stride, koffs, 0, kbuf_of(0));
+  if (nt > 1) fetch(kbase, a.k_stride, koffs, 1, kbuf_of(1));
+  if (nt > 2) fetch(kbase, a.k_stride, koffs, 2, kbuf_of(2));
+  fetch(vbase, a.v_stride, voffs, 0, vbuf_of(0));
+  bf16x8 qf[HD / 16];
+  {
+    const uint16_t* src = a.q + (size_t)(start + (ok ? row_j : 0)) * a.q_stride + (size_t)(ok ? row_h : 0) * HD;
+#pragma unroll
+    for (int kk = 0; kk < HD / 16; ++kk) {
+      const uint4 v = *reinterpret_cast<const uint4*>(src + 16 * kk + 8 * hh);
+      qf[kk] = __builtin_bit_cast(bf16x8, ok ? v : make_uint4(0, 0, 0, 0));
+    }
+  }
+
   floatx16 o[HD / 32];
   float m = -INFINITY, mb = 0.0f, l = 0.0f, lx = 0.0f;   // mb: m, or 0 while a row has seen nothing; lx: l of unrounded weights
 #pragma unroll
@@ -200,10 +208,11 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
   auto key_frag = [&](const char* kb, int s, int kk) {
     return *reinterpret_cast<const bf16x8*>(kb + ((koff ^ (kk << 5)) + 32 * s * ROWB));
   };
-  auto scores = [&](floatx16 (&sc)[SB], const char* kb) {
+  auto scores = [&](floatx16 (&sc)[SB], const char* kb, int keys) {   // of blocks that begin below `keys`
 #pragma unroll
     for (int s = 0; s < SB; ++s) {
       sc[s] = floatx16{};
+      if (s > 0 && uniform(32 * s >= keys)) continue;
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk)
         sc[s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_frag(kb, s, kk), qf[kk], sc[s], 0, 0, 0);
@@ -271,11 +280,6 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
     return f;
   };
 
-  // K tile t lies in buffer t % 4, V tile t in buffer t % 2; during tile t the loads of
-  // K t + 3 and V t + 1 are in flight
-  char* const vbuf = smem + 4 * TILEB;
-  auto kbuf_of = [&](int t) { return smem + (t & 3) * TILEB; };
-  auto vbuf_of = [&](int t) { return vbuf + (t & 1) * TILEB; };
   int t = 0;
   auto open_tile = [&]() {                  // tile t: its operands have landed, its buffers-to-be are free
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -283,10 +287,6 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
   };
   // keeps the flipped offsets out of registers across the loop: they are one instruction
   auto fresh = [&]() { asm volatile("" : "+v"(koff), "+v"(voff[0]), "+v"(voff[1])); };
-  fetch(kbase, a.k_stride, koffs, 0, kbuf_of(0));
-  if (nt > 1) fetch(kbase, a.k_stride, koffs, 1, kbuf_of(1));
-  if (nt > 2) fetch(kbase, a.k_stride, koffs, 2, kbuf_of(2));
-  fetch(vbase, a.v_stride, voffs, 0, vbuf_of(0));
 
   // tiles that every row of the wave sees whole: cur holds tile t's scores, nxt takes the
   // next tile's (of no use after the last).  Four groups of the first product and UG of
@@ -365,7 +365,7 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
   open_tile();
   if (uniform(nfull > 0)) {
     floatx16 sb[SB];
-    scores(sa, kbuf_of(0));
+    scores(sa, kbuf_of(0), KT);
     raise(row_max(sa));
 #pragma unroll
     for (int i = 0; i < KG; ++i) kf[0][i] = key_frag(kbuf_of(1), i % SB, i / SB);
@@ -384,7 +384,7 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
     if (t + 1 < nt) fetch(vbase, a.v_stride, voffs, t + 1, vbuf_of(t + 1));
     if (uniform(t < nsome)) {
       const char* vb = vbuf_of(t);
-      scores(sa, kbuf_of(t));
+      scores(sa, kbuf_of(t), whigh - t * KT);
       mask(sa, t);
       raise(row_max(sa));
 #pragma unroll
@@ -432,40 +432,52 @@ __global__ __launch_bounds__(64 * NW, NW > 4 ? 2 : 1) void prompt_rows(Work w) {
     }
   }
 
+  // The rows leave through LDS, a region of this wave's own once all are done with the
+  // tiles, so that a store writes whole rows.  Row r's dims 8 p + 4 h .. lie in its piece
+  // p ^ (r % 16), halves exchanged in the upper 16 rows: no bank twice.
   const float lt = halves_sum(l), lxt = kLse ? halves_sum(lx) : 0.0f;
-  if (!ok) return;
   const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
-  const size_t at = (size_t)(start + row_j) * a.nh + row_h;
+  const int at = ok ? (start + row_j) * a.nh + row_h : -1;
+  if (kLse && ok && hh == 0) a.lse[at] = row_lse(m, lxt);
+  __syncthreads();
+  char* const mine = smem + wave * 32 * ROWB;
 #pragma unroll
   for (int d = 0; d < HD / 32; ++d)
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<uint2*>(a.out + at * HD + 32 * d + 8 * q + 4 * hh) =
+      *reinterpret_cast<uint2*>(mine + col * ROWB + ((4 * d + q) ^ (col & (PIECES < 16 ? PIECES - 1 : 15))) * 16 + (hh ^ (col >> 4)) * 8) =
           lt == 0.0f ? make_uint2(0u, 0u)
                      : make_uint2(pack_bf16x2(o[d][4 * q] * inv, o[d][4 * q + 1] * inv),
                                   pack_bf16x2(o[d][4 * q + 2] * inv, o[d][4 * q + 3] * inv));
-  if (kLse && hh == 0) a.lse[at] = row_lse(m, lxt);
+  constexpr int RPI = 64 / PIECES;          // rows of one store
+#pragma unroll
+  for (int i = 0; i < 32 / RPI; ++i) {
+    const int r = i * RPI + lane / PIECES, p = lane % PIECES, to = __shfl(at, r);
+    uint4 v = *reinterpret_cast<const uint4*>(mine + r * ROWB + (p ^ (r & (PIECES < 16 ? PIECES - 1 : 15))) * 16);
+    if (r >= 16) v = make_uint4(v.z, v.w, v.x, v.y);
+    if (to >= 0) *reinterpret_cast<uint4*>(a.out + (size_t)to * HD + 8 * p) = v;
+  }
 }
 
-template <int HD, int NW, bool kCausal, bool kLse>
+template <int HD, int NW, int KT, bool kCausal, bool kLse>
 hipError_t launch_one(const Work& w, hipStream_t stream) {
   const PromptArgs& a = w.a;
-  constexpr int rows = 32 * NW, lds = 6 * tile_keys(HD) * HD * 2;
+  constexpr int rows = 32 * NW, lds = 6 * KT * HD * 2;
   const int64_t tiles = ((int64_t)a.T * w.G + rows - 1) / rows + a.B;
   if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&prompt_rows<HD, NW, kCausal, kLse>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&prompt_rows<HD, NW, KT, kCausal, kLse>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((prompt_rows<HD, NW, kCausal, kLse>), dim3((unsigned)(tiles * a.nkv)), dim3(64 * NW), lds, stream, w);
+  hipLaunchKernelGGL((prompt_rows<HD, NW, KT, kCausal, kLse>), dim3((unsigned)(tiles * a.nkv)), dim3(64 * NW), lds, stream, w);
   return hipGetLastError();
 }
 
-template <int HD, int NW>
+template <int HD, int NW, int KT>
 hipError_t launch(const Work& w, hipStream_t stream) {
   if (w.a.lse)
-    return w.a.causal ? launch_one<HD, NW, true, true>(w, stream) : launch_one<HD, NW, false, true>(w, stream);
-  return w.a.causal ? launch_one<HD, NW, true, false>(w, stream) : launch_one<HD, NW, false, false>(w, stream);
+    return w.a.causal ? launch_one<HD, NW, KT, true, true>(w, stream) : launch_one<HD, NW, KT, false, true>(w, stream);
+  return w.a.causal ? launch_one<HD, NW, KT, true, false>(w, stream) : launch_one<HD, NW, KT, false, false>(w, stream);
 }
 
 }  // namespace
@@ -475,10 +487,16 @@ hipError_t launch_prompt_attention(const PromptArgs& a, int hd, hipStream_t stre
   w.a = a;
   w.G = a.nh / a.nkv;
   w.c = a.scale * kLog2e;
+  // Workgroups of four waves, two on a compute unit, where sequences are short: one begins
+  // or ends, which is memory's time, while the other multiplies.  Eight waves where they are
+  // long: half the tiles to load.  32/8 heads of 128, causal, four waves against eight: 192
+  // sequences of 64 59 and 76 us, 24 of 512 107 and 112, 12 of 1024 170 and 161, one of 8192
+  // 611 and 536; 16/2 heads of 64: 64 of 256 35 and 36 us, one of 1024 18 and 23, two of 4096
+  // 100 and 92.  Heads of 256 leave registers for four waves only.
   switch (hd) {
-    case 64: return launch<64, 8>(w, stream);
-    case 128: return launch<128, 8>(w, stream);
-    case 256: return launch<256, 4>(w, stream);
+    case 64: return a.T <= (int64_t)1024 * a.B ? launch<64, 4, 64>(w, stream) : launch<64, 8, 64>(w, stream);
+    case 128: return a.T <= (int64_t)512 * a.B ? launch<128, 4, 32>(w, stream) : launch<128, 8, 64>(w, stream);
+    case 256: return launch<256, 4, 32>(w, stream);
     default: return hipErrorInvalidValue;
   }
 }
