@@ -527,6 +527,7 @@ def run_prompt(q, k, v, cu, causal, scale=None):
     (2, 2, 256, [65]),
     (4, 2, 128, [700]),                     # several key tiles and row tiles
     (512, 1, 64, [2, 3]),                   # a token's heads are more than a row tile
+    (4, 2, 64, [1300, 901]),                # long sequences of small heads
 ])
 @pytest.mark.parametrize("causal", [True, False])
 def test_prompt(nh, nkv, hd, lens, causal):
@@ -587,6 +588,31 @@ def test_prompt_unseen_keys_with_large_scores():
             assert torch.equal(out[:at], clean[:at]), f"hd {hd} key {at}"
             ref = oa.prompt(q, big, v, [0, T], True, hd ** -0.5)
             check_rows(out, lse, ref, hd, f"hd {hd} key {at}")
+
+
+@pytest.mark.parametrize("hd,lens", [(64, [1150, 1100]), (128, [700, 601])])
+def test_prompt_unseen_keys_of_long_sequences(hd, lens):
+    """The two tests before, at lengths where eight waves work on a tile."""
+    g = np.random.default_rng(25)
+    T = sum(lens)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    q, k, v = bits(g, T, 4, hd, std=2.0), bits(g, T, 2, hd), bits(g, T, 2, hd)
+    clean, _ = run_prompt(q, k, v, cu, True)
+    for at in (300, 511, 512, lens[0] - 40, lens[0] - 1):
+        big = k.copy()
+        big[at] = synth.bf16_bits((100 * ck.bf16_decode(q[at - 1, :2])).astype(np.float32))
+        out, _ = run_prompt(q, big, v, cu, True)
+        assert torch.equal(out[:at], clean[:at]) and torch.equal(out[lens[0]:], clean[lens[0]:]), f"key {at}"
+        bad = v.copy()
+        big[at], bad[at] = NAN, INF
+        out, _ = run_prompt(q, big, bad, cu, True)
+        assert torch.equal(out[:at], clean[:at]) and torch.equal(out[lens[0]:], clean[lens[0]:]), f"key {at}"
+        assert np.isnan(value(out)[at:lens[0]]).all()
+        bad = v.copy()
+        bad[at, 0, 3] = INF
+        out, _ = run_prompt(q, k, bad, cu, True)
+        assert torch.equal(out[:at], clean[:at]) and torch.equal(out[lens[0]:], clean[lens[0]:]), f"value {at}"
+        assert np.isposinf(value(out)[at:lens[0], :2, 3]).all() and np.isfinite(value(out)[at:lens[0], 2:]).all()
 
 
 def test_prompt_strided_columns_and_graph():
