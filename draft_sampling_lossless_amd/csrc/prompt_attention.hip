@@ -292,7 +292,7 @@ __global__ __launch_bounds__(64 * NW, HD > 128 ? 1 : 2) void prompt_rows(Work w)
   // next tile's (of no use after the last).  Four groups of the first product and UG of
   // the second, each with its operands read one group ahead (the first group's before the
   // barrier) and an equal share of the vector work
-  constexpr int KG = SB * (HD / 16) / 4, VG = HD / 32;
+  constexpr int KG = SB * (HD / 16) / 4, DH = HD > 128 ? 2 : 1, VG = HD / 32 / DH, OG = UG * DH;
   bf16x8 kf[2][KG];
   auto step = [&](floatx16 (&cur)[SB], floatx16 (&nxt)[SB]) {
     open_tile();
@@ -334,10 +334,11 @@ __global__ __launch_bounds__(64 * NW, HD > 128 ? 1 : 2) void prompt_rows(Work w)
       }
     }
 #pragma unroll
-    for (int u = 0; u < UG; ++u) {
-      if (u < UG - 1) {
+    for (int gq = 0; gq < OG; ++gq) {
+      const int u = gq / DH, d0 = gq % DH * VG;
+      if (gq < OG - 1) {
 #pragma unroll
-        for (int i = 0; i < VG; ++i) vf[(u + 1) & 1][i] = value_frag(vb, u + 1, i);
+        for (int i = 0; i < VG; ++i) vf[(gq + 1) & 1][i] = value_frag(vb, (gq + 1) / DH, (gq + 1) % DH * VG + i);
       } else {
 #pragma unroll
         for (int i = 0; i < KG; ++i) kf[0][i] = key_frag(kbuf_of(t + 2), i % SB, i / SB);
@@ -348,14 +349,15 @@ __global__ __launch_bounds__(64 * NW, HD > 128 ? 1 : 2) void prompt_rows(Work w)
       } else if (UG > 2 && u < 3) {
         weights(cur, 3, u - 1, p[3]);
       }
-      if (u == UG - 1) tm = row_max(nxt);
+      if (gq == OG - 1) tm = row_max(nxt);
 #pragma unroll
-      for (int d = 0; d < VG; ++d) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[u & 1][d].v, as_frag(p[u]), o[d], 0, 0, 0);
+      for (int i = 0; i < VG; ++i)
+        o[d0 + i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[gq & 1][i].v, as_frag(p[u]), o[d0 + i], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
       if (uniform(t + 1 < nt)) {
 #pragma unroll
         for (int q = 0; q < LOADS; ++q)
-          if (q * UG / LOADS == u) fetch_one(vbase, a.v_stride, voffs, t + 1, vbuf_of(t + 1), q);
+          if (q * OG / LOADS == gq) fetch_one(vbase, a.v_stride, voffs, t + 1, vbuf_of(t + 1), q);
       }
     }
     ++t;
