@@ -56,7 +56,7 @@ struct __attribute__((aligned(16))) Item {
 struct Work {
   PagedArgs a;
   int G, RB, unit;     // heads per kv head, row blocks, nkv * RB
-  int target;          // items aimed at
+  int target_log2;     // items aimed at, a power of two
   int min_chunk;       // keys of a range, at least
   int whole;           // no request is cut where none can be longer than this
   int pid_cap;         // ranges the workspace has room for
@@ -77,7 +77,7 @@ __device__ __forceinline__ void request(const PagedArgs& a, int b, int& q0, int&
 
 // Ranges of all requests are at most `chunk` keys; a longer request is cut into equal ones.
 __device__ __forceinline__ int chunk_of(const Work& w, int64_t total) {
-  const int64_t per = (total * w.unit + w.target - 1) / w.target;
+  const int64_t per = (total * w.unit + (1 << w.target_log2) - 1) >> w.target_log2;
   const int64_t up = (per + kStep - 1) / kStep * kStep;
   return (int)(up < w.min_chunk ? w.min_chunk : up > (1 << 30) ? (1 << 30) : up);
 }
@@ -123,19 +123,19 @@ __device__ __forceinline__ bool find_item(const Work& w, int u, Item& it) {
 // The plan of a call with several requests: one workgroup cuts the requests into ranges
 // and lists them by falling length (to a 256th of the longest), so that the dearest start
 // first.  The order among equals is that of the atomics and decides nothing but time: a
-// range's place among the partials comes from the order of the requests.
-constexpr int kPlanThreads = 1024, kPlanEach = (4096 + kPlanThreads - 1) / kPlanThreads;
+// range's place among the partials comes from the requests alone.
+constexpr int kPlanThreads = 1024, kPlanEach = 4;   // 256 threads are enough for 1024 requests
 
 __global__ __launch_bounds__(kPlanThreads) void paged_plan(Work w) {
   const PagedArgs& a = w.a;
   __shared__ int64_t sums[kPlanThreads / 64];
   __shared__ int offs[kPlanThreads / 64], bins[256], cursor[256];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, threads = blockDim.x;
   int q0[kPlanEach], n[kPlanEach], kv[kPlanEach], ranges[kPlanEach], len[kPlanEach];
   int64_t total = 0;
 #pragma unroll
   for (int e = 0; e < kPlanEach; ++e) {
-    const int b = tid * kPlanEach + e;
+    const int b = e * threads + tid;
     q0[e] = n[e] = kv[e] = 0;
     if (b < a.B) request(a, b, q0[e], n[e], kv[e]);
     if (n[e] > 0) total += kv[e];
@@ -145,9 +145,10 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan(Work w) {
   if (tid < 256) bins[tid] = 0;
   __syncthreads();
   total = 0;
-  for (int v = 0; v < kPlanThreads / 64; ++v) total += sums[v];
+  for (int v = 0; v < threads / 64; ++v) total += sums[v];
   const int chunk = chunk_of(w, total);
-  auto bin = [&](int keys) { return 255 - min(255, (int)((int64_t)keys * 256 / (chunk + 1))); };
+  const float per_bin = 255.0f / (float)chunk;
+  auto bin = [&](int keys) { return 255 - min(255, (int)((float)keys * per_bin)); };
   int split = 0;                                  // ranges of this thread's split requests
 #pragma unroll
   for (int e = 0; e < kPlanEach; ++e) {
@@ -194,7 +195,7 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan(Work w) {
 #pragma unroll
   for (int e = 0; e < kPlanEach; ++e) {
     if (n[e] == 0) continue;
-    const int b = tid * kPlanEach + e, full = ranges[e] - 1;
+    const int b = e * threads + tid, full = ranges[e] - 1;
     w.req[b] = make_int2(pid, ranges[e]);
     if (full > 0) {
       const int at = atomicAdd(&cursor[bin(len[e])], full);
@@ -488,17 +489,20 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
 // workgroup share the keys, which pass through three LDS buffers of 32 (one worked
 // on, the others filling straight from memory).  Rows lie there in 16-byte pieces permuted (piece p of
 // row r at p ^ swizzle(r)) so that the K reads (16 rows, one piece) and the transposing V
-// reads (8 rows, two pieces) touch every bank once.  The slots of kWindow keys (small
+// reads (rows 0..7 or rows 0..3 and 8..11, two pieces) touch every bank once.  The slots of kWindow keys (small
 // pages) or groups of 16 keys are looked up ahead into LDS by the whole workgroup.  Few
 // registers and 52 KB of LDS leave room for three workgroups on a compute unit, which
-// cover each other's waits.
+// cover each other's waits.  Bound by memory: 256 requests of 1..17 tokens over up to 4096
+// keys, 32/8 heads of 128, pages of 64: 430 us, 5.3 TB/s; 64 blocks of 16 tokens over
+// 100..4000 keys found slot by slot: 145 us, 3.9 TB/s, where the ranges end unevenly.
 constexpr int kWindow = 1024;
 constexpr int kStages = 3;     // LDS buffers
 
 template <int HD>
 __device__ __forceinline__ int swizzle(int r) {
-  if constexpr (HD == 64) return (((r >> 1) & 3) << 1) | ((r >> 3) & 1);
-  return ((r & 7) << 1) | ((r >> 3) & 1);
+  const int far = (r >> 3) & 1, mid = ((r >> 2) & 1) ^ far;
+  if constexpr (HD == 64) return (mid << 2) | (r & 2) | far;
+  return (mid << 3) | ((r & 3) << 1) | far;
 }
 
 template <int HD>
@@ -923,7 +927,7 @@ Shape shape_of(int B, int max_q, int nh, int nkv, int hd) {
   s.unit = nkv * s.RB;
   // items aimed at: two workgroups on each compute unit (one with heads of 256) draw all
   // that memory gives, and shorter ranges cost more in starting and joining than they
-  // even out: 64 blocks of 16 x 4 rows over 100..4000 keys take 153 us so, 160 at twice
+  // even out: 64 blocks of 16 x 4 rows over 100..4000 keys took 153 us so, 160 at twice
   // and 169 us at three times as many; one row over 131071 keys 101, 105 and 115 us
   s.target = kCus * (hd > 128 ? 1 : 2);
   // A shorter range costs more to start and join than it takes.  A tile of 32 keys takes a
@@ -999,7 +1003,7 @@ hipError_t launch_paged_attention(const PagedArgs& a, int hd, void* workspace, h
   w.G = s.G;
   w.RB = s.RB;
   w.unit = s.unit;
-  w.target = s.target;
+  w.target_log2 = __builtin_ctz((unsigned)s.target);
   w.min_chunk = s.min_chunk;
   w.whole = s.whole;
   w.pid_cap = s.pid_cap;
@@ -1016,7 +1020,7 @@ hipError_t launch_paged_attention(const PagedArgs& a, int hd, void* workspace, h
   const int64_t items = std::min(most, (int64_t)a.B * s.unit + s.target + s.unit);
   if (a.B > 1 && max_kv > s.whole) {
     w.plan = reinterpret_cast<Item*>(base + s.off_plan);
-    hipLaunchKernelGGL(paged_plan, dim3(1), dim3(kPlanThreads), 0, stream, w);
+    hipLaunchKernelGGL(paged_plan, dim3(1), dim3(a.B <= 1024 ? 256 : kPlanThreads), 0, stream, w);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
