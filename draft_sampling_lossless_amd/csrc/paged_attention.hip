@@ -511,10 +511,10 @@ constexpr int shared_lds() {
 }
 
 template <int HD, int RT, bool kSlots, bool kLse>
-__global__ __launch_bounds__(64 * RT, HD > 128 ? (RT == 8 ? 2 : 1) : RT == 2 ? 2 : RT == 8 ? 4 : 3) void paged_shared(Work w) {
+__global__ __launch_bounds__(64 * RT, HD > 128 ? RT / 4 : RT == 8 ? 4 : 3) void paged_shared(Work w) {
   constexpr int ROWB = HD * 2, TILEB = KT * ROWB, PIECES = HD / 8;
   constexpr int LOADS = 2 * TILEB / 1024;         // 1 KB loads of one tile, K then V
-  constexpr int LPW = (LOADS + RT - 1) / RT;      // of a wave (the last wave's may repeat the last load)
+  constexpr int LPW = LOADS / RT;                 // of a wave
   constexpr int LR = 64 / PIECES;                 // rows of one load
   extern __shared__ __attribute__((aligned(16))) char smem[];
   int32_t* slots = reinterpret_cast<int32_t*>(smem + kStages * 2 * TILEB);
@@ -564,7 +564,7 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? (RT == 8 ? 2 : 1) : RT == 2 ? 2
   int half[LPW], row_of[LPW];                     // which 16 keys; this lane's row of the tile
 #pragma unroll
   for (int q = 0; q < LPW; ++q) {
-    const int f = uniform(min(q * RT + wave, LOADS - 1)), fk = f % (LOADS / 2), r = fk * LR + lrow;
+    const int f = uniform(q * RT + wave), fk = f % (LOADS / 2), r = fk * LR + lrow;
     from[q] = f < LOADS / 2 ? kbase : vbase;
     to[q] = f * 1024;
     half[q] = fk * LR >> 4;
@@ -922,7 +922,11 @@ Shape shape_of(int B, int max_q, int nh, int nkv, int hd) {
   Shape s;
   s.G = nh / nkv;
   const int rows = max_q * s.G;
-  s.RT = rows <= 64 ? (rows + 15) / 16 : 8;
+  // Waves of 16 rows a workgroup: 64 requests over 100..4000 keys, 32/8 heads of 128, take
+  // 114 us with 4 rows by paged_rows and 126 by shared tiles, 118 and 130 with 16; 20 rows
+  // 130 us with four waves (two of them only load) and 131 with two, 40 rows 135 with four
+  // and 144 with eight, 68 rows 166 with eight and 190 with four.
+  s.RT = rows <= 16 ? 1 : rows <= 64 ? 4 : 8;
   s.RB = (rows + 16 * s.RT - 1) / (16 * s.RT);
   s.unit = nkv * s.RB;
   // items aimed at: two workgroups on each compute unit (one with heads of 256) draw all
@@ -982,8 +986,6 @@ template <int HD>
 hipError_t launch_rt(const Work& w, int RT, int64_t items, int max_kv, hipStream_t stream) {
   switch (RT) {
     case 1: return launch<HD, 1>(w, items, max_kv, stream);
-    case 2: return launch<HD, 2>(w, items, max_kv, stream);
-    case 3: return launch<HD, 3>(w, items, max_kv, stream);
     case 4: return launch<HD, 4>(w, items, max_kv, stream);
     default: return launch<HD, 8>(w, items, max_kv, stream);
   }
