@@ -13,7 +13,7 @@
 // as they stand.
 //
 // Up to 16 rows (paged_rows): memory-bound, one product hardly fills a matrix instruction.
-// Each of a workgroup's four waves takes tiles of its own straight into registers; V's
+// Each of a workgroup's four or eight waves takes tiles of its own straight into registers; V's
 // operand (eight keys of one dim per lane) comes from loads of 8 consecutive dims of eight
 // keys (16 lanes cover a row, 16 bytes each), transposed by byte permutes, product t then
 // covering the dims 8 c + t.  The waves are joined through LDS at the end.  256 requests of
@@ -39,9 +39,8 @@ namespace {
 // row's first tile and hardly ever after.
 constexpr float kRaise = 8.0f;
 
-constexpr int NW = 4;          // waves per workgroup; they take tiles in turn
 constexpr int KT = 32;         // keys per tile
-constexpr int kStep = KT * NW; // ranges are whole numbers of these
+constexpr int kStep = 4 * KT;  // ranges are whole numbers of these
 constexpr int kCus = 256;      // compute units of the card
 constexpr int kJoinGroups = 2048;   // workgroups of the joining pass aimed at
 
@@ -244,7 +243,7 @@ struct Dims {
 
 // kSlots: pages smaller than 16, so the slot of every key is looked up by a lane of its
 // own; otherwise 16 aligned keys lie in one page and the wave looks up two
-template <int HD, bool kSlots, bool kLse>
+template <int HD, int NW, bool kSlots, bool kLse>
 __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
   using D = Dims<HD>;
   constexpr int ODIM = 16 * D::VD;                // dims of one group
@@ -426,7 +425,7 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
     }
   }
 
-  // join the four waves, one dim group at a time
+  // join the waves, one dim group at a time
   const int tr = threadIdx.x >> 4, tc = threadIdx.x & 15;
   l = groups_sum(l);
   if (kLse) lx = groups_sum(lx);
@@ -445,6 +444,7 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
         *reinterpret_cast<floatx4*>(&obuf[wave][c][D::VD * (4 * g + i) + t]) =
             floatx4{o[y][t][i], o[y][t + 1][i], o[y][t + 2][i], o[y][t + 3][i]};
     __syncthreads();
+    if (tr >= 16) continue;                       // (256 threads join)
     float mm = -INFINITY, ll = 0.0f, xx = 0.0f, f[NW], acc[D::VD];
 #pragma unroll
     for (int v = 0; v < NW; ++v) mm = fmaxf(mm, mbuf[v][tr]);
@@ -963,7 +963,12 @@ hipError_t launch_rows(const Work& w, int grid, hipStream_t stream) {
     }
     hipLaunchKernelGGL((paged_shared<HD, RT, kSlots, kLse>), dim3(grid), dim3(64 * RT), lds, stream, w);
   } else {
-    hipLaunchKernelGGL((paged_rows<HD, kSlots, kLse>), dim3(grid), dim3(64 * NW), 0, stream, w);
+    // Eight waves where no compute unit gets a second workgroup: one token over 517 keys, 32/8
+    // heads of 128, 9.2 us with eight and 10.2 with four, 32 of them 13.6 and 15.4.  Heads of 256
+    // leave registers for four.
+    constexpr int most = HD > 128 ? 4 : 8;
+    if (grid <= kCus) hipLaunchKernelGGL((paged_rows<HD, most, kSlots, kLse>), dim3(grid), dim3(64 * most), 0, stream, w);
+    else hipLaunchKernelGGL((paged_rows<HD, 4, kSlots, kLse>), dim3(grid), dim3(64 * 4), 0, stream, w);
   }
   return hipGetLastError();
 }
