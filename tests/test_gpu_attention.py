@@ -556,6 +556,19 @@ def test_prompt_many_sequences(B):
     check_rows(out, lse, oa.prompt(q, k, v, cu, True, 64 ** -0.5), 64, "prompt")
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_most_sequences(causal):
+    """DSPARK_MAX_SEQS sequences, most of a token or none, the last ones longer."""
+    g = np.random.default_rng(26)
+    lens = g.integers(0, 3, 4096)
+    lens[4094:] = 70, 33
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    T = int(cu[-1])
+    q, k, v = bits(g, T, 2, 64, std=2.0), bits(g, T, 1, 64), bits(g, T, 1, 64)
+    out, lse = run_prompt(q, k, v, cu, causal)
+    check_rows(out, lse, oa.prompt(q, k, v, cu, causal, 64 ** -0.5), 64, "prompt")
+
+
 def test_prompt_unseen_keys_do_not_matter():
     g = np.random.default_rng(21)
     for hd, lens in ((128, [100, 150]), (64, [70, 80]), (256, [90])):
@@ -698,6 +711,55 @@ def test_prompt_then_rounds_over_one_cache():
     used = np.concatenate([table[b, np.arange(n) // page] * page + np.arange(n) % page for b, n in enumerate(total)])
     assert torch.equal(kc2[dev(used.astype(np.int64))], kc[dev(used.astype(np.int64))])
     assert torch.equal(vc2[dev(used.astype(np.int64))], vc[dev(used.astype(np.int64))])
+
+
+def test_decode_steps_captured_once():
+    """Append and attention of one new token per request in one graph, replayed step by
+    step: positions, slots and lengths are advanced by the program between the replays, and
+    a second graph of the same workspace runs in turn with it."""
+    g = np.random.default_rng(33)
+    B, nh, nkv, hd, page, steps = 5, 8, 2, 128, 16, 6
+    start = np.array([0, 15, 40, 600, 1300])
+    width = 90
+    table = g.permutation(B * width).reshape(B, width).astype(np.int32)
+    slot = lambda b, t: int(table[b, t // page]) * page + t % page  # noqa: E731
+    shape = (B * width * page, nkv, hd)
+    old_k, old_v = bits(g, *shape), bits(g, *shape)
+    kc, vc, ke, ve = dev(old_k), dev(old_v), dev(old_k), dev(old_v)
+    q, k, v = (torch.empty((B, h, hd), dtype=torch.int16, device="cuda") for h in (nh, nkv, nkv))
+    qo, out, other = (torch.empty((B, nh, hd), dtype=torch.int16, device="cuda") for _ in range(3))
+    pos, kv = (torch.empty(B, dtype=torch.int32, device="cuda") for _ in range(2))
+    slots, cu, tb = torch.empty(B, dtype=torch.int64, device="cuda"), dev(np.arange(B + 1, dtype=np.int32)), dev(table)
+    ws = torch.empty(dsl.paged_attention_workspace_size(B, B, 1, nh, nkv, hd), dtype=torch.uint8, device="cuda")
+    for t in (q, k, v, pos, kv, slots):
+        t.zero_()
+
+    def step(o, causal):
+        dsl.kv_append(k, v, pos, slots, kc, vc, q=q, q_out=qo)
+        dsl.paged_attention(qo, kc, vc, tb, kv, cu, 1, page, causal=causal, out=o, workspace=ws)
+
+    step(out, True)
+    torch.cuda.synchronize()
+    kc.copy_(ke), vc.copy_(ve)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for gr, o in zip(graphs, (out, other)):
+        with torch.cuda.graph(gr):
+            step(o, o is out)
+    for n in range(steps):
+        at = start + n
+        new = [bits(g, B, h, hd) for h in (nh, nkv, nkv)]
+        for t, x in zip((q, k, v, pos, kv, slots), new + [at.astype(np.int32), (at + 1).astype(np.int32),
+                                                          np.array([slot(b, at[b]) for b in range(B)], np.int64)]):
+            t.copy_(dev(x))
+        for gr in graphs:
+            gr.replay()
+        qe = dsl.kv_append(k, v, pos, slots, ke, ve, q=q)
+        want = dsl.paged_attention(qe, ke, ve, tb, kv, cu, 1, page)
+        assert torch.equal(qo, qe) and torch.equal(kc, ke) and torch.equal(vc, ve), f"step {n}"
+        assert torch.equal(out, want) and torch.equal(other, want), f"step {n}"   # one token sees all: causal or not
+    ref = oa.paged(host(qo).view(np.uint16), host(kc).view(np.uint16), host(vc).view(np.uint16), table, start + steps,
+                   np.arange(B + 1), page, True, hd ** -0.5)
+    check_rows(out, None, ref, hd, "last step")
 
 
 def test_draft_block_over_a_context_kv_cache():
