@@ -931,13 +931,13 @@ Shape shape_of(int B, int max_q, int nh, int nkv, int hd) {
   s.unit = nkv * s.RB;
   // items aimed at: two workgroups on each compute unit (one with heads of 256) draw all
   // that memory gives, and shorter ranges cost more in starting and joining than they
-  // even out: 64 blocks of 16 x 4 rows over 100..4000 keys took 153 us so, 160 at twice
-  // and 169 us at three times as many; one row over 131071 keys 101, 105 and 115 us
+  // even out: 64 blocks of 16 x 4 rows over 100..4000 keys take 145 us so, 150 at twice
+  // and 163 us at four times as many; one token over 131071 keys 104, 110 and 118 us
   s.target = kCus * (hd > 128 ? 1 : 2);
   // A shorter range costs more to start and join than it takes.  A tile of 32 keys takes a
   // workgroup of shared tiles about 0.9 us alone, four tiles the waves of paged_rows; the
   // joining pass, about 5 us.  Calls that leave most of the card idle cut finer: 9 tokens
-  // over 512 keys of one request 12.8 us so and 19.8 us whole, of 64 requests 39 and 30 us.
+  // over 512 keys of one request 11 us so and 18 us whole, of 64 requests 38 and 32 us.
   s.min_chunk = s.RT == 1 ? 512 : B * s.unit <= kCus / 4 ? 128 : 256;
   s.whole = 2 * s.min_chunk;
   // a split request has more keys than a range, so its ranges are fewer than twice its
