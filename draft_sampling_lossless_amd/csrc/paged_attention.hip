@@ -280,7 +280,9 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
   for (int x = 0; x < D::VU; ++x)
 #pragma unroll
     for (int t = 0; t < D::VD; ++t) o[x][t] = floatx4{0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, mb = 0.0f, l = 0.0f, lx = 0.0f;   // mb: m, or 0 while the row has seen nothing; lx: l unrounded
+  // m: running maximum, in units of the row's factor rc; mb: m, or 0 while the row has seen
+  // nothing; lx: l of unrounded weights
+  float m = -INFINITY, mb = 0.0f, l = 0.0f, lx = 0.0f, rc = w.c;
 
   const int32_t* table = a.page_table + (size_t)it.b * a.width;
   const int rstride = a.nkv * HD;                 // elements between slots
@@ -374,9 +376,11 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
     float hi = sc[0][0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) hi = fmaxf(hi, sc[e >> 2][e & 3]);
-    const float tm = groups_max(hi) * w.c;
-    if (uniform(__any(tm > m + kRaise))) {
-      const float mn = tm > m + kRaise ? tm : m;
+    hi = groups_max(hi);
+    const bool up = hi * rc > m + kRaise;
+    if (uniform(__any(up))) {
+      if (up) rc = row_factor(hi, w.c);
+      const float mn = up ? hi * rc : m;
       const float al = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
       m = mn;
       mb = mn == -INFINITY ? 0.0f : mn;
@@ -389,7 +393,7 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
     }
     float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[e >> 2][e & 3], w.c, -mb));
+    for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[e >> 2][e & 3], rc, -mb));
     // the weights' rounding to bf16, the second product's operand type
     const bf16x8 p = pack_weights<kLse>(x, l, lx);
 
@@ -429,6 +433,7 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
   const int tr = threadIdx.x >> 4, tc = threadIdx.x & 15;
   l = groups_sum(l);
   if (kLse) lx = groups_sum(lx);
+  m *= w.c / rc;                                  // in units of c, as the other parts' are
 #pragma unroll
   for (int y = 0; y < D::VU; ++y) {
     if (y) __syncthreads();
@@ -546,7 +551,9 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? RT / 4 : RT == 8 ? 4 : 3) void 
   floatx4 o[HD / 16];                             // dims 16 d + 4 g + i of row c
 #pragma unroll
   for (int d = 0; d < HD / 16; ++d) o[d] = floatx4{0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, mb = 0.0f, l = 0.0f, lx = 0.0f;   // mb: m, or 0 while the row has seen nothing; lx: l unrounded
+  // m: running maximum, in units of the row's factor rc; mb: m, or 0 while the row has seen
+  // nothing; lx: l of unrounded weights
+  float m = -INFINITY, mb = 0.0f, l = 0.0f, lx = 0.0f, rc = w.c;
 
   const int k0 = it.k0, k1 = it.k1;
   const int32_t* table = a.page_table + (size_t)it.b * a.width;
@@ -655,7 +662,7 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? RT / 4 : RT == 8 ? 4 : 3) void 
   auto weights = [&](const floatx4 (&sc)[2], float& sum, float& sumx) {
     float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[e >> 2][e & 3], w.c, -mb));
+    for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[e >> 2][e & 3], rc, -mb));
     return pack_weights<kLse>(x, sum, sumx);
   };
   auto finite = [&](const char* vb) {             // every value of the tile
@@ -687,9 +694,11 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? RT / 4 : RT == 8 ? 4 : 3) void 
     float hi = sc[0][0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) hi = fmaxf(hi, sc[e >> 2][e & 3]);
-    const float tm = groups_max(hi) * w.c;
-    if (uniform(__any(tm > m + kRaise))) {
-      const float mn = tm > m + kRaise ? tm : m;
+    hi = groups_max(hi);
+    const bool up = hi * rc > m + kRaise;
+    if (uniform(__any(up))) {
+      if (up) rc = row_factor(hi, w.c);
+      const float mn = up ? hi * rc : m;
       const float al = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
       m = mn;
       mb = mn == -INFINITY ? 0.0f : mn;
@@ -789,6 +798,7 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? RT / 4 : RT == 8 ? 4 : 3) void 
 
   l = groups_sum(l);
   if (kLse) lx = groups_sum(lx);
+  m *= w.c / rc;                                  // in units of c, as the other parts' are
   if (idle || !ok) return;
   if (it.pid < 0) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;

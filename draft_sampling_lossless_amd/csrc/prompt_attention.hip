@@ -198,7 +198,9 @@ __global__ __launch_bounds__(64 * NW, HD > 128 ? 1 : 2) void prompt_rows(Work w)
   }
 
   floatx16 o[HD / 32];
-  float m = -INFINITY, mb = 0.0f, l = 0.0f, lx = 0.0f;   // mb: m, or 0 while a row has seen nothing; lx: l of unrounded weights
+  // m: running maximum, in units of the row's factor rc; mb: m, or 0 while a row has seen
+  // nothing; lx: l of unrounded weights
+  float m = -INFINITY, mb = 0.0f, l = 0.0f, lx = 0.0f, rc = w.c;
 #pragma unroll
   for (int d = 0; d < HD / 32; ++d) o[d] = floatx16{};
 
@@ -226,7 +228,7 @@ __global__ __launch_bounds__(64 * NW, HD > 128 ? 1 : 2) void prompt_rows(Work w)
       for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[s][e]);
     uint32_t lo, hi;
     halves_pair(__float_as_uint(top), lo, hi);
-    return fmaxf(__uint_as_float(lo), __uint_as_float(hi)) * w.c;
+    return fmaxf(__uint_as_float(lo), __uint_as_float(hi));
   };
   auto mask = [&](floatx16 (&sc)[SB], int t) {
 #pragma unroll
@@ -236,9 +238,11 @@ __global__ __launch_bounds__(64 * NW, HD > 128 ? 1 : 2) void prompt_rows(Work w)
         if (t * KT + 32 * s + 8 * (e >> 2) + 4 * hh + (e & 3) >= lim) sc[s][e] = -INFINITY;
   };
   // raise the maxima that tile t's scores exceed by too much
-  auto raise = [&](float tm) {
-    if (uniform(__any(tm > m + kRaise))) {
-      const float mn = tm > m + kRaise ? tm : m;
+  auto raise = [&](float top) {
+    const bool up = top * rc > m + kRaise;
+    if (uniform(__any(up))) {
+      if (up) rc = row_factor(top, w.c);
+      const float mn = up ? top * rc : m;
       const float al = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
       m = mn;
       mb = mn == -INFINITY ? 0.0f : mn;
@@ -253,7 +257,7 @@ __global__ __launch_bounds__(64 * NW, HD > 128 ? 1 : 2) void prompt_rows(Work w)
   auto weights = [&](const floatx16 (&sc)[SB], int u, int half, uint32_t (&p)[4]) {
     float x[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[u >> 1][8 * (u & 1) + 4 * half + e], w.c, -mb));
+    for (int e = 0; e < 4; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[u >> 1][8 * (u & 1) + 4 * half + e], rc, -mb));
     if (kLse) lx += (x[0] + x[1]) + (x[2] + x[3]);
     p[2 * half] = pack_bf16x2(x[0], x[1]);
     p[2 * half + 1] = pack_bf16x2(x[2], x[3]);
@@ -440,7 +444,7 @@ __global__ __launch_bounds__(64 * NW, HD > 128 ? 1 : 2) void prompt_rows(Work w)
   const float lt = halves_sum(l), lxt = kLse ? halves_sum(lx) : 0.0f;
   const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
   const int at = ok ? (start + row_j) * a.nh + row_h : -1;
-  if (kLse && ok && hh == 0) a.lse[at] = row_lse(m, lxt);
+  if (kLse && ok && hh == 0) a.lse[at] = row_lse(m * (w.c / rc), lxt);
   __syncthreads();
   char* const mine = smem + wave * 32 * ROWB;
 #pragma unroll

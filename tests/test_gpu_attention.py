@@ -408,6 +408,48 @@ def test_paged_large_scores_and_scale():
     check_rows(out, lse, ref_paged(c, True, 0.003), 128)
 
 
+@pytest.mark.parametrize("std", [3e4, 1e6, 1e12])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_scores_beyond_any_exponent(hd, std):
+    """Scores of 1e9 to 1e25: each row takes the value of its largest score.  Keys are
+    multiples of one direction, so that the largest differs from the next by far more than
+    float32 sums are off by."""
+    g = np.random.default_rng(48)
+    n, nh, nkv = 2100, 4, 2
+    base = g.choice([-1.0, 1.0], (nkv, hd)) * g.uniform(0.5, 1.0, (nkv, hd))
+    size = g.permutation(n) / n * 2 - 1                               # distinct multiples, -1 .. 1
+    k = synth.bf16_bits((std * size[:, None, None] * base).astype(np.float32))
+    q = synth.bf16_bits((std * g.choice([-1.0, 1.0], (n, nh, 1)) * np.repeat(base, nh // nkv, 0)).astype(np.float32))
+    v = bits(g, n, nkv, hd)
+    qd, kd, vd = ck.bf16_decode(q), ck.bf16_decode(k), ck.bf16_decode(v)
+
+    def check(out, lse, rows, seen, label):
+        got, ls = value(out), host(lse).astype(np.float64)
+        checked = 0
+        for i, t in enumerate(rows):
+            for h in range(nh):
+                x = (kd[:seen(t), h * nkv // nh] @ qd[t, h]) * hd ** -0.5
+                order = np.argsort(x)
+                if len(x) > 1 and x[order[-1]] - x[order[-2]] < 1e-4 * np.abs(x).max():
+                    continue                          # (two keys rounded alike)
+                checked += 1
+                assert np.array_equal(got[i, h], vd[order[-1], h * nkv // nh]), f"{label} token {t} head {h}"
+                # sums of hd products of one sign, the scaling, the change of base and back
+                assert abs(ls[i, h] - x[order[-1]]) <= ((hd + 4) * 2.0 ** -24 + 2.0 ** -21) * np.abs(x[order[-1]])
+        assert checked > len(rows)
+
+    out, lse = run_prompt(q, k, v, [0, n], True)
+    check(out[::37], lse[::37], range(0, n, 37), lambda t: t + 1, "prompt")
+    table = g.permutation(n).astype(np.int32)
+    kc, vc = np.zeros_like(k), np.zeros_like(v)
+    kc[table], vc[table] = k, v
+    for m in (2, 12):                                 # both kernels, split and joined
+        c = dict(q=q[n - m:], kc=kc, vc=vc, table=table[None], kv=np.array([n], np.int32), cu=np.array([0, m], np.int32),
+                 page=1, hd=hd, max_q=m)
+        out, lse = run_paged(c, True)
+        check(out, lse, range(n - m, n), lambda t: t + 1, f"paged {m}")
+
+
 def test_paged_offsets_beyond_32_bits():
     """A cache of 5 GiB a side, its last pages in use: slot offsets pass 2^32 bytes."""
     g = np.random.default_rng(13)
