@@ -6,7 +6,7 @@
 // product are (token, head) pairs of one kv head, token-major: the nh / nkv heads that
 // share keys share their tiles too.  A workgroup takes 32 NW rows, a wave 32, and keys
 // and values pass through LDS in tiles of KT tokens.  One causal prompt of 8192 tokens, 32/8
-// heads of 128: 525 us, 1050 TFLOP/s (1110 without the mask), bound by the matrix pipe and
+// heads of 128: 528 us, 1040 TFLOP/s (1100 without the mask), bound by the matrix pipe and
 // the exponentials and packing beside it; short sequences by their loads and stores.
 //
 // Scores are formed transposed, S^T = K Q^T, with v_mfma_f32_32x32x16_bf16: lane
