@@ -55,18 +55,27 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // branch around one has to be a scalar branch: its condition goes through here.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// The factor of a row's scores, given its maximum: c = scale * log2 e, but a power of two
-// where the maximum passes 2^30.  score * c - maximum is one fused operation against the
-// rounded maximum, whose half unit in the last place would be the exponent of the largest
-// weight: up to 64 below 2^30, without bound beyond.  There scores that differ at all differ by
-// 64 and more, so that any factor near c leaves the same weights, and a power of two makes
-// the maximum exact.
-__device__ __forceinline__ float row_factor(float top, float c) {
-  return fabsf(top * c) < 0x1p30f ? c : __uint_as_float(__float_as_uint(c) & 0x7F800000u);
+// The least power of two that is not below c (c normal, below 2^127)
+__device__ __forceinline__ float power_above(float c) {
+  return __uint_as_float((__float_as_uint(c) + 0x7FFFFFu) & 0x7F800000u);
 }
 
-// log(sum exp) of a row from its base-2 maximum and sum; -inf for a row that saw nothing
-__device__ __forceinline__ float row_lse(float m, float l) {
+// The factor of a row's scores, given its maximum: c = scale * log2 e, but the power of two
+// above it where the maximum passes 2^30 in magnitude.  score * c - maximum is one fused
+// operation against the rounded maximum, whose half unit in the last place is the exponent of
+// the largest weight: up to 32 below 2^30, without bound beyond.  There scores that differ at
+// all differ by 64 and more, so that any factor near c leaves the same weights, and a power of
+// two makes the maximum exact.  As it is not below c, a maximum of the one factor and one of
+// the other compare as their scores do, and lie 64 and more apart: a row that changes its
+// factor, and waves and ranges of different factors, are rescaled and joined as if there were one.
+__device__ __forceinline__ float row_factor(float top, float c) {
+  return fabsf(top * c) < 0x1p30f ? c : power_above(c);
+}
+
+// log(sum exp) of a row from its base-2 maximum, which is in units of row_factor's, and sum;
+// -inf for a row that saw nothing
+__device__ __forceinline__ float row_lse(float m, float l, float c) {
+  if (fabsf(m) >= 0x1p30f) m *= c / power_above(c);
   return l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : l == 0.0f ? -INFINITY : l;
 }
 

@@ -35,8 +35,8 @@ namespace dspark {
 namespace {
 
 // The running maximum is raised only when a row's scores exceed it by kRaise (weights up
-// to 2^kRaise, which neither float nor bf16 minds): the accumulators are rescaled on a
-// row's first tile and hardly ever after.
+// to 2^kRaise, more where the maximum itself is rounded by more than that, which neither float
+// nor bf16 minds): the accumulators are rescaled on a row's first tile and hardly ever after.
 constexpr float kRaise = 8.0f;
 
 constexpr int KT = 32;         // keys per tile
@@ -433,7 +433,6 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
   const int tr = threadIdx.x >> 4, tc = threadIdx.x & 15;
   l = groups_sum(l);
   if (kLse) lx = groups_sum(lx);
-  m *= w.c / rc;                                  // in units of c, as the other parts' are
 #pragma unroll
   for (int y = 0; y < D::VU; ++y) {
     if (y) __syncthreads();
@@ -477,7 +476,7 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
       uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * HD + ODIM * y + D::VD * tc);
 #pragma unroll
       for (int t = 0; t < D::VW; ++t) dst[t] = pk[t];
-      if (kLse && y == 0 && tc == 0) a.lse[at] = row_lse(mm, xx);
+      if (kLse && y == 0 && tc == 0) a.lse[at] = row_lse(mm, xx, w.c);
     } else {
       const size_t at = ((size_t)it.pid * w.unit + kvh) * 16 + tr;
       float* dst = w.part_o + at * HD + ODIM * y + D::VD * tc;
@@ -798,7 +797,6 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? RT / 4 : RT == 8 ? 4 : 3) void 
 
   l = groups_sum(l);
   if (kLse) lx = groups_sum(lx);
-  m *= w.c / rc;                                  // in units of c, as the other parts' are
   if (idle || !ok) return;
   if (it.pid < 0) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -808,7 +806,7 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? RT / 4 : RT == 8 ? 4 : 3) void 
       *reinterpret_cast<uint2*>(a.out + at * HD + 16 * d + 4 * g) =
           l == 0.0f ? make_uint2(0u, 0u)
                     : make_uint2(pack_bf16x2(o[d][0] * inv, o[d][1] * inv), pack_bf16x2(o[d][2] * inv, o[d][3] * inv));
-    if (kLse && g == 0) a.lse[at] = row_lse(m, lx);
+    if (kLse && g == 0) a.lse[at] = row_lse(m, lx, w.c);
   } else {
     const size_t at = ((size_t)it.pid * w.unit + rest) * (16 * RT) + 16 * wave + c;
 #pragma unroll
@@ -887,7 +885,7 @@ __global__ __launch_bounds__(256) void paged_join(Work w, int step) {
     uint2 pk = make_uint2(0u, 0u);
     if (t.l != 0.0f) pk = make_uint2(pack_bf16x2(t.acc[0] * inv, t.acc[1] * inv), pack_bf16x2(t.acc[2] * inv, t.acc[3] * inv));
     *reinterpret_cast<uint2*>(a.out + at * HD + 4 * d) = pk;
-    if (a.lse && d == 0) a.lse[at] = row_lse(t.m, t.lx);
+    if (a.lse && d == 0) a.lse[at] = row_lse(t.m, t.lx, w.c);
   };
   if (ns <= kFew) {
     for (int r = first + grp; r < last; r += GR) finish(r, join_ranges(w, base + r, stride, ns, 0, 1, HD, d));

@@ -116,8 +116,9 @@ __device__ __forceinline__ float halves_sum(float v) {
 // exponentials of this one (vector pipe).  K is read one tile ahead of V; four LDS buffers
 // of K and two of V are filled straight from memory while the others are in use, with one
 // barrier a tile.  The running maximum is raised only when a row's scores exceed it by
-// kRaise (weights up to 2^kRaise, which neither float nor bf16 minds): the accumulators are
-// rescaled on a row's first tile and hardly ever after.
+// kRaise (weights up to 2^kRaise, more where the maximum itself is rounded by more than that,
+// which neither float nor bf16 minds): the accumulators are rescaled on a row's first tile and
+// hardly ever after.
 constexpr float kRaise = 8.0f;
 
 template <int HD, int NW, int KT, bool kCausal, bool kLse>
@@ -444,7 +445,7 @@ __global__ __launch_bounds__(64 * NW, HD > 128 ? 1 : 2) void prompt_rows(Work w)
   const float lt = halves_sum(l), lxt = kLse ? halves_sum(lx) : 0.0f;
   const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
   const int at = ok ? (start + row_j) * a.nh + row_h : -1;
-  if (kLse && ok && hh == 0) a.lse[at] = row_lse(m * (w.c / rc), lxt);
+  if (kLse && ok && hh == 0) a.lse[at] = row_lse(m, lxt, w.c);
   __syncthreads();
   char* const mine = smem + wave * 32 * ROWB;
 #pragma unroll

@@ -464,8 +464,10 @@ dspark_status dspark_kv_append(const uint16_t* q, int64_t q_stride, const uint16
  *   Products on bf16 MFMA, accumulated in float32; softmax statistics and sums float32.
  *   The softmax weights are rounded to bf16 for the second product (its operand type), and
  *   the row is divided by the sum of the rounded weights; lse takes the unrounded ones.
- *   Weights reach 2^8 before that division: values of magnitude up to 2^119 over the
- *   number of keys stay finite.
+ *   Weights reach 2^9 before that division, 2^32 in a row whose largest |scale * q . k|
+ *   passes 2^24: values of magnitude up to 2^118, 2^95 there, over the number of keys
+ *   stay finite.  A row whose largest score passes 2^30 in magnitude takes the value of
+ *   its largest score; scores up to 2^126 are in range.
  *   Long caches are split over workgroups and joined in a fixed order: results repeat
  *   bit for bit.  workspace >= dspark_paged_attention_workspace_size(...) bytes, device,
  *   16-byte aligned. */

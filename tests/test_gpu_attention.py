@@ -450,6 +450,137 @@ def test_scores_beyond_any_exponent(hd, std):
         check(out, lse, range(n - m, n), lambda t: t + 1, f"paged {m}")
 
 
+# Exact scores.  q = (2^16 u, 2^8 u, u, 0, ..) and k = the three 8-bit digits of an integer N,
+# |N| < 2^24, with its sign: every product and every partial sum of q . k = N u is exact in
+# float32, in any order, so the largest score of a row is known to the last bit.
+
+def exact_scores(g, N, u, hd):
+    """N [n, nkv] and u [nkv], powers of two -> q [nkv, hd] (the query of every token), k, v."""
+    N = np.asarray(N, np.int64)
+    k = np.zeros((*N.shape, hd), np.float32)
+    q = np.zeros((N.shape[1], hd), np.float32)
+    for i, shift in enumerate((16, 8, 0)):
+        k[..., i] = np.sign(N) * ((np.abs(N) >> shift) & 255)
+        q[:, i] = np.asarray(u, np.float64) * 2.0 ** shift
+    assert np.array_equal((k.astype(np.float64) * q).sum(-1), N * np.asarray(u, np.float64)) and np.abs(N).max() < 1 << 24
+    return synth.bf16_bits(q), synth.bf16_bits(k), bits(g, *N.shape, hd)
+
+
+def check_winner(out, lse, N, u, v, rows, hd, label):
+    """Each row is the value of its largest score: the other key lies 64 and more below it as
+    an exponent of two and weighs at most 2^-32 of it (a weight may be up to 2^32 before the
+    division), the filling nothing; dividing the value times its weight by that weight is off
+    by 2^-22, and the value is a bf16.  rows: (row, keys it sees).
+    lse: seven roundings of 2^-24 (the scale, its product with log2 e, the score's with that,
+    the weight's logarithm added, the changes of base): 2^-21 of it."""
+    got, ls = value(out), host(lse).astype(np.float64)
+    vd, checked = ck.bf16_decode(v), 0
+    for i, seen in rows:
+        for h in range(N.shape[1]):
+            x = N[:seen, h]
+            best = int(np.argmax(x))
+            if (x == x[best]).sum() > 1:
+                continue                              # only keys of the filling
+            checked += 1
+            assert np.array_equal(got[i, h], vd[best, h]), f"{label} row {i} head {h}: {got[i, h, :3]} for key {best}"
+            want = hd ** -0.5 * float(x[best]) * u[h]
+            assert abs(ls[i, h] - want) <= 2.0 ** -21 * abs(want), f"{label} row {i} head {h}: lse"
+    assert checked >= N.shape[1]
+
+
+def run_exact(g, N, u, hd, label):
+    """Both attentions on exact scores: prompts in both forms, few and many rows over pages and slots."""
+    n, nkv = N.shape
+    q1, k, v = exact_scores(g, N, u, hd)
+    q = np.ascontiguousarray(np.broadcast_to(q1, (n, nkv, hd)))
+    for causal in (True, False):
+        out, lse = run_prompt(q, k, v, [0, n], causal)
+        rows = [(t, t + 1 if causal else n) for t in range(0, n, 11)] + [(n - 1, n)]
+        check_winner(out, lse, N, u, v, rows, hd, f"{label} prompt causal={causal}")
+    for m in (1, 40, 80):                             # paged_rows; four and eight waves of shared tiles
+        for page in (16, 1):
+            pages = -(-n // page) + 2
+            order = g.permutation(pages)[:-(-n // page)].astype(np.int32)
+            slot = order[np.arange(n) // page].astype(np.int64) * page + np.arange(n) % page
+            kc, vc = np.full((pages * page, nkv, hd), NAN, np.uint16), np.full((pages * page, nkv, hd), NAN, np.uint16)
+            kc[slot], vc[slot] = k, v
+            c = dict(q=q[:m], kc=kc, vc=vc, table=order[None], kv=np.array([n], np.int32),
+                     cu=np.array([0, m], np.int32), page=page, hd=hd, max_q=m)
+            out, lse = run_paged(c, False)
+            check_winner(out, lse, N, u, v, [(t, n) for t in range(m)], hd, f"{label} paged {m} page {page}")
+
+
+# where the two keys lie: one range and one wave's tiles, one tile apart, a range the other's
+# neighbour, ends of a split request; and the larger one first
+PLACES = [(400, 5, 263), (600, 5, 263), (600, 5, 40), (600, 263, 5), (2100, 5, 2000), (2100, 5, 261), (2100, 2000, 5)]
+
+
+@pytest.mark.parametrize("n,first,second", PLACES)
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_maxima_on_both_sides_of_a_large_exponent(hd, n, first, second):
+    """Two keys outweigh the others, one with an exponent a 2^30, the other, larger, with
+    b 2^30: a row's maximum goes from below 2^30 in magnitude to above it or back, within a
+    wave's tiles, between waves and between ranges."""
+    say(f"maxima hd={hd} n={n} at {first}, {second}")
+    pairs = [(0.8, 1.05), (0.95, 1.05), (0.999, 1.005), (0.72, 1.3), (-1.05, -0.99), (-1.005, -0.999), (-1.4, -0.75),
+             (-1.2, 0.999)]
+    per = 2.0 ** 30 / (hd ** -0.5 * np.log2(np.e))    # the score of an exponent of 2^30
+    u = np.full(len(pairs), 2.0 ** np.ceil(np.log2(2.5 * per / (2 ** 24 - 1))))
+    N = np.zeros((n, len(pairs)), np.int64)
+    for h, (a, b) in enumerate(pairs):
+        N[:, h] = 0 if a > 0 else round(-2.4 * per / u[h])
+        N[first, h], N[second, h] = round(a * per / u[h]), round(b * per / u[h])
+    run_exact(np.random.default_rng(hd + n), N, u, hd, f"hd {hd} n {n}")
+
+
+@pytest.mark.parametrize("n,first,second", PLACES)
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_neighbouring_maxima_beyond_a_large_exponent(hd, n, first, second):
+    """Two keys whose scores are neighbours in float32, with exponents beyond 2^30 in
+    magnitude: 64 and more apart, so the larger one's value is the row's."""
+    say(f"neighbours hd={hd} n={n} at {first}, {second}")
+    per = 2.0 ** 30 / (hd ** -0.5 * np.log2(np.e))
+    start = int(0.9 * 2 ** 24)
+    u = np.full(16, 2.0 ** np.ceil(np.log2(per / start)))
+    N = np.zeros((n, 16), np.int64)
+    for h in range(16):
+        at = start + 7 * (h // 2)
+        if h % 2:
+            N[:, h], N[first, h], N[second, h] = 1 - 2 ** 24, -at - 1, -at
+        else:
+            N[first, h], N[second, h] = at, at + 1
+    run_exact(np.random.default_rng(hd + n), N, u, hd, f"hd {hd} n {n}")
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_values_up_to_the_stated_size_stay_finite(hd):
+    """Maxima of 2^27 to 2^30 in magnitude, as exponents, leave weights of up to 2^32 before the
+    division; values up to 2^95 over the number of keys, here 2^86, stay finite."""
+    n, nkv = 400, 16
+    per = 2.0 ** 30 / (hd ** -0.5 * np.log2(np.e))
+    g = np.random.default_rng(hd)
+    u = np.full(nkv, 2.0 ** np.ceil(np.log2(per / (2 ** 24 - 1))))
+    N = np.zeros((n, nkv), np.int64)
+    for h in range(nkv):
+        top = int(per * g.uniform(0.125, 0.999) / u[h])
+        N[:, h] = top if h % 2 else -top
+    q1, k, _ = exact_scores(g, N, u, hd)
+    q = np.ascontiguousarray(np.broadcast_to(q1, (n, nkv, hd)))
+    v = synth.bf16_bits((2.0 ** 86 * g.choice([-1.0, 1.0], (n, nkv, hd))).astype(np.float32))
+    order = np.arange(n // 16, dtype=np.int32)
+    for m in (1, 40, n):
+        if m == n:
+            out, _ = run_prompt(q, k, v, [0, n], False)
+        else:
+            out, _ = run_paged(dict(q=q[:m], kc=k, vc=v, table=order[None], kv=np.array([n], np.int32),
+                                    cu=np.array([0, m], np.int32), page=16, hd=hd, max_q=m), False)
+        # equal scores: the mean of the values, whose weights are equal and so their roundings too;
+        # the sums of n terms are off by n 2^-24 of n 2^86 each, the output's rounding by 2^-8
+        want = ck.bf16_decode(v).mean(0)
+        tol = 2.0 ** -8 * np.abs(want) + 2.0 ** 86 * (2 * n + 8) * 2.0 ** -24
+        assert np.all(np.abs(value(out) - want) <= tol), f"{m} rows"
+
+
 def test_paged_offsets_beyond_32_bits():
     """A cache of 5 GiB a side, its last pages in use: slot offsets pass 2^32 bytes."""
     g = np.random.default_rng(13)
