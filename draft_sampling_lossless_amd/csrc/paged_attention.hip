@@ -851,7 +851,7 @@ __device__ __forceinline__ Joined join_ranges(const Work& w, size_t at0, size_t 
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const float f = __builtin_amdgcn_exp2f(ml[q][0] - ms);
-      if (f != 0.0f) {                            // (a range behind the last has weight 0, whatever lies there)
+      if (s0 + q * hop < ns) {                    // (a range of weight 0 too: its sums may be NaN)
         t.l += ml[q][1] * f;
         t.lx += ml[q][2] * f;
         t.acc += v[q] * f;

@@ -342,6 +342,55 @@ def test_paged_values_that_are_not_finite_reach_the_rows_that_see_them():
     assert np.isfinite(np.delete(got, 5, axis=2)).all()
 
 
+@pytest.mark.parametrize("kv", [1500, 3001, 20001])     # a few ranges, and more than one group joins
+@pytest.mark.parametrize("m", [1, 3, 12, 24])           # paged_rows; four and eight waves of shared tiles
+def test_paged_nan_in_a_split_request(m, kv):
+    """What is not finite reaches the rows that see it whichever range it lies in: in a
+    query, in every key of a range, in one key or value of a range whose other scores lie so
+    far below that its weight is zero in the join.  The other kv head's rows do not change."""
+    say(f"paged NaN m={m} kv={kv}")
+    g = np.random.default_rng(kv + m)
+    nh, nkv, hd, page = 8, 2, 64, 16
+    c = paged_case(g, nh, nkv, hd, page, [m], [kv])
+    c["q"][:, :4] = synth.bf16_bits(np.full((m, 4, hd), 2.0, np.float32))
+    slot = c["table"][0, np.arange(kv) // page].astype(np.int64) * page + np.arange(kv) % page
+    clean, clean_lse = run_paged(c, True)
+    check_rows(clean, clean_lse, ref_paged(c, True), hd, "clean")
+
+    def check(d, label, rows, dims=slice(None)):
+        out, lse = run_paged(d, True)
+        bad = np.zeros((m, nh), bool)
+        bad[rows] = True
+        assert torch.equal(out[dev(~bad)], clean[dev(~bad)]) and torch.equal(lse[dev(~bad)], clean_lse[dev(~bad)]), label
+        assert not np.isfinite(value(out)[bad][:, dims]).any(), label
+        return value(out)[bad], host(lse)[bad]
+
+    q = c["q"].copy()
+    q[m - 1, 3, 5] = NAN
+    out, lse = check(dict(c, q=q), "query", (m - 1, 3))
+    assert np.isnan(out).all() and np.isnan(lse).all()
+    mid = slot[kv // 4:3 * kv // 4]                       # holds whole ranges
+    first = np.s_[:, :4]
+    kc = c["kc"].copy()
+    kc[mid, 0] = NAN
+    out, lse = check(dict(c, kc=kc), "keys of a range", first)
+    assert np.isnan(out).all() and np.isnan(lse).all()
+    kc[mid, 0] = synth.bf16_bits(np.full((len(mid), hd), -8.0, np.float32))   # exponents 185 below 0
+    low = dict(c, kc=kc)
+    clean, clean_lse = run_paged(low, True)
+    check_rows(clean, clean_lse, ref_paged(low, True), hd, "low")
+    kc = kc.copy()
+    kc[slot[kv // 2], 0, 7] = NAN
+    out, lse = check(dict(c, kc=kc), "key of a low range", first)
+    assert np.isnan(out).all() and np.isnan(lse).all()
+    vc = c["vc"].copy()
+    vc[slot[kv // 2], 0, 5] = INF
+    out, lse = check(dict(low, vc=vc), "value of a low range", first, 5)
+    want = value(clean)[:, :4].reshape(-1, hd)
+    assert np.array_equal(np.delete(out, 5, 1), np.delete(want, 5, 1))
+    assert np.array_equal(lse, host(clean_lse)[:, :4].reshape(-1))
+
+
 def test_paged_pages_outside_the_cache_hide_their_keys():
     g = np.random.default_rng(10)
     for page in (1, 16, 64):
