@@ -520,6 +520,8 @@ dspark_status attention_shape(int T, int B, int nh, int nkv, int hd, float scale
   REQUIRE(hd > 0 && hd % 2 == 0, DSPARK_ERR_INVALID, "hd must be positive and even (got %d)", hd);
   REQUIRE(hd == 64 || hd == 128 || hd == 256, DSPARK_ERR_UNSUPPORTED, "hd must be 64, 128 or 256 (got %d)", hd);
   REQUIRE(scale > 0.0f && std::isfinite(scale), DSPARK_ERR_INVALID, "scale must be finite and > 0");
+  // (the kernels' factor is the next power of two above scale * log2 e)
+  REQUIRE(scale <= 0x1p126f, DSPARK_ERR_UNSUPPORTED, "scale must be <= 2^126 (got %g)", (double)scale);
   REQUIRE((int64_t)T * nh < ((int64_t)1 << 30), DSPARK_ERR_UNSUPPORTED, "T * nh must be < 2^30");
   return DSPARK_OK;
 }

@@ -459,7 +459,7 @@ dspark_status dspark_kv_append(const uint16_t* q, int64_t q_stride, const uint16
  *   every row; kv_len is taken as at most max_pages * page_size and at least 0.
  *   page_size a power of two; hd in {64, 128, 256}; nh % nkv == 0; nh <= 1024;
  *   1 <= B <= DSPARK_MAX_SEQS; 1 <= max_q <= DSPARK_MAX_BLOCK; num_pages * page_size < 2^31;
- *   max_pages * page_size <= 2^30; T * nh < 2^30; scale > 0 and finite; T == 0
+ *   max_pages * page_size <= 2^30; T * nh < 2^30; 0 < scale <= 2^126; T == 0
  *   enqueues nothing.
  *   Products on bf16 MFMA, accumulated in float32; softmax statistics and sums float32.
  *   The softmax weights are rounded to bf16 for the second product (its operand type), and
@@ -490,8 +490,8 @@ dspark_status dspark_paged_attention(const uint16_t* q, int64_t q_stride, const 
  *   elements apart (each % 8 == 0 and at least one row; k_stride, v_stride < 2^24), device,
  *   16-byte aligned; cu_seqlens [B + 1] int32 ascending from 0, device; out [T, nh, hd] bf16, 16-byte
  *   aligned; lse [T, nh] float32 or NULL.
- *   hd in {64, 128, 256}; nh % nkv == 0; nh <= 1024; 1 <= B <= DSPARK_MAX_SEQS; scale > 0
- *   and finite; T * nh < 2^30; T == 0 enqueues nothing.  Arithmetic as
+ *   hd in {64, 128, 256}; nh % nkv == 0; nh <= 1024; 1 <= B <= DSPARK_MAX_SEQS;
+ *   0 < scale <= 2^126; T * nh < 2^30; T == 0 enqueues nothing.  Arithmetic as
  *   dspark_paged_attention's.  No workspace. */
 dspark_status dspark_prompt_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
                                       const uint16_t* v, int64_t v_stride, const int32_t* cu_seqlens, uint16_t* out,

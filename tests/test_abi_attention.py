@@ -99,6 +99,13 @@ def test_prompt_validation(dspark_lib):
         assert _prompt(**{name: FAKE_ODD}) == INVALID and "aligned" in _err()
 
 
+@pytest.mark.parametrize("call", [_paged, _prompt])
+def test_scales_whose_factor_is_no_float_are_refused(dspark_lib, call):
+    for scale in (2.0 ** 126.1, 2.0 ** 127, 2.5e38, 3.4e38):
+        assert call(scale=scale) == UNSUPPORTED and "2^126" in _err()
+    assert call(scale=2.0 ** 126, T=0) == OK and call(scale=1e-45, T=0) == OK
+
+
 def test_binding_refuses_host_tensors_and_wrong_types(dspark_lib):
     x = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
     i = torch.zeros(2, dtype=torch.int32)
