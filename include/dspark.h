@@ -445,10 +445,11 @@ dspark_status dspark_kv_append(const uint16_t* q, int64_t q_stride, const uint16
  * with kv head h / (nh / nkv), query t = cu_q[b] + j:
  *   out[t, h] = sum_s p_s v_s,  p = softmax_s(scale * q[t, h] . k_s)
  *   over s < kv_len[b], and s <= kv_len[b] - n_b + j where causal is set.
- *   A row that sees no key gets zeros.  Keys a row does not see have no influence on
- *   it, whatever their values (NaN and infinities included).
- *   lse[t, h] (optional, NULL = none) = log sum_s exp(scale * q . k_s), -inf for a row
- *   that sees no key: what a caller needs to join the result with another part's.
+ *   A row that sees no key, or none whose score is above -infinity, gets zeros.  Keys a
+ *   row does not see have no influence on it, whatever their values (NaN and infinities
+ *   included).
+ *   lse[t, h] (optional, NULL = none) = log sum_s exp(scale * q . k_s), -inf for such a
+ *   row: what a caller needs to join the result with another part's.
  *   q [T, nh, hd] bf16 bits, rows q_stride elements apart (% 8 == 0, >= nh * hd), device,
  *   16-byte aligned; k_cache, v_cache [num_pages * page_size, nkv, hd] bf16, 16-byte
  *   aligned (a layer of dspark_context_kv's caches; page_size 1: the table holds slots);

@@ -630,6 +630,43 @@ def test_values_up_to_the_stated_size_stay_finite(hd):
         assert np.all(np.abs(value(out) - want) <= tol), f"{m} rows"
 
 
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_rows_whose_every_score_is_minus_infinity(hd):
+    """They get zeros and a log-sum-exp of -inf, as rows without keys do, cut into ranges or
+    not; a score among them that is not a number reaches the row."""
+    g = np.random.default_rng(hd)
+    for n in (90, 2100):
+        q, k, v = bits(g, n, 4, hd), bits(g, n, 2, hd), bits(g, n, 2, hd)
+        k[:, :, 0] = synth.bf16_bits(np.abs(g.normal(1, 0.2, (n, 2))).astype(np.float32) + np.float32(0.1))
+        q[:, 1, 0] = 0xFF80
+        k[40, 0, 0] = 0xFF80                              # (-inf)^2: the head's largest score
+        order = np.arange(n, dtype=np.int32)
+
+        def check(out, lse, rows):
+            out, lse = value(out), host(lse)
+            for i, seen in rows:
+                if seen <= 40:
+                    assert not out[i, 1].any() and np.isneginf(lse[i, 1]), f"n {n} row {i}"
+                else:
+                    assert np.isnan(out[i, 1]).all()      # an infinite maximum
+                assert np.isfinite(out[i, 2:]).all() and np.isfinite(lse[i, 2:]).all()
+
+        out, lse = run_prompt(q, k, v, [0, n], True)
+        check(out, lse, [(t, t + 1) for t in range(0, n, 7)])
+        k[40, 0, 0] = synth.bf16_bits(np.ones(1, np.float32))[0]
+        for m in (2, 20, 40):
+            c = dict(q=q[:m], kc=k, vc=v, table=order[None], kv=np.array([n], np.int32), cu=np.array([0, m], np.int32),
+                     page=1, hd=hd, max_q=m)
+            out, lse = run_paged(c, False)
+            assert not value(out)[:, 1].any() and np.isneginf(host(lse)[:, 1]).all()
+            assert value(out)[:, 0].any() and np.isfinite(value(out)).all()
+            one = dict(c, kc=k.copy())
+            one["kc"][n // 2, 0, 0] = 0                   # -inf * 0: NaN reaches the row
+            out, lse = run_paged(one, False)
+            assert np.isnan(value(out)[:, 1]).all() and np.isnan(host(lse)[:, 1]).all()
+            assert np.isfinite(value(out)[:, [0, 2, 3]]).all()
+
+
 def test_paged_offsets_beyond_32_bits():
     """A cache of 5 GiB a side, its last pages in use: slot offsets pass 2^32 bytes."""
     g = np.random.default_rng(13)
