@@ -37,6 +37,10 @@ __device__ __forceinline__ shortx4 lds_read_tr(const char* p) {
 // lds + 16 i (base and lds uniform).  Written in assembly because the compiler otherwise
 // makes every later LDS read wait for every such load; the callers wait themselves
 // (s_waitcnt vmcnt, then a barrier) before a buffer is read.  It has no register result.
+// The compiler warns that it does not keep m0 across the statement: it has nothing there, LDS
+// instructions of gfx950 do not read m0, and nothing else in the kernels that use this writes it.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_to_lds16(const char* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
                : "memory", "m0");
@@ -45,6 +49,7 @@ __device__ __forceinline__ void load_to_lds16(const char* base, uint32_t off, ui
 __device__ __forceinline__ void load_to_lds16(const char* src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 __device__ __forceinline__ uint32_t lds_address(const char* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
 }
