@@ -1029,7 +1029,10 @@ hipError_t launch_paged_attention(const PagedArgs& a, int hd, void* workspace, h
   w.part_o = reinterpret_cast<float*>(base + s.off_o);
   w.plan = nullptr;
   w.count = reinterpret_cast<int*>(base + s.off_count);
-  // at most one range per request, plus the ones the balancing adds
+  // at most one range per request, plus the ones the balancing adds.  The table's width is the
+  // host's only bound on the lengths, so that a wide one costs the plan, the join and surplus
+  // workgroups: one token over 517 keys 8.7 us under a table of that length and 11.0 under one of
+  // 131072 keys, 64 requests of up to 512 keys 15.8 and 21.7.
   const int max_kv = a.width << a.page_shift;
   const int64_t most = (int64_t)a.B * s.unit * (max_kv <= s.whole ? 1 : (max_kv + s.min_chunk - 1) / s.min_chunk);
   const int64_t items = std::min(most, (int64_t)a.B * s.unit + s.target + s.unit);

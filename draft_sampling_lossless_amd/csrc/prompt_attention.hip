@@ -6,8 +6,9 @@
 // product are (token, head) pairs of one kv head, token-major: the nh / nkv heads that
 // share keys share their tiles too.  A workgroup takes 32 NW rows, a wave 32, and keys
 // and values pass through LDS in tiles of KT tokens.  One causal prompt of 8192 tokens, 32/8
-// heads of 128: 528 us, 1040 TFLOP/s (1100 without the mask), bound by the matrix pipe and
-// the exponentials and packing beside it; short sequences by their loads and stores.
+// heads of 128: 530 to 565 us by the machine, 1040 to 975 TFLOP/s (1100 to 1015 without the
+// mask), bound by the matrix pipe and the exponentials and packing beside it; short sequences
+// by their loads and stores.
 //
 // Scores are formed transposed, S^T = K Q^T, with v_mfma_f32_32x32x16_bf16: lane
 // (h, n) = (lane / 32, lane % 32) holds row n and the keys 8 (i / 4) + 4 h + i % 4 of
@@ -499,7 +500,9 @@ hipError_t launch_prompt_attention(const PromptArgs& a, int hd, hipStream_t stre
   // long: half the tiles to load.  32/8 heads of 128, causal, four waves against eight: 192
   // sequences of 64 59 and 76 us, 24 of 512 107 and 112, 12 of 1024 170 and 161, one of 8192
   // 611 and 536; 16/2 heads of 64: 64 of 256 35 and 36 us, one of 1024 18 and 23, two of 4096
-  // 100 and 92.  Heads of 256 leave registers for four waves only.
+  // 100 and 92.  Heads of 256 leave registers for four waves only.  The host knows the mean
+  // length alone, and these were equal lengths: one of 8192 among 31 of some 100 takes 641 us by
+  // four waves, 560 alone by eight and the others 23.
   switch (hd) {
     case 64: return a.T <= (int64_t)1024 * a.B ? launch<64, 4, 64>(w, stream) : launch<64, 8, 64>(w, stream);
     case 128: return a.T <= (int64_t)512 * a.B ? launch<128, 4, 32>(w, stream) : launch<128, 8, 64>(w, stream);
