@@ -17,6 +17,14 @@ The layers around them share one key-value cache:
   kv_append         a layer's new tokens into it, normed and rotated
   paged_attention   a round's few query tokens per request over its pages
   prompt_attention  attention over whole packed prompts
+                    (both also under a sliding window with sinks)
+  tree_mask         a drafted tree's parents to masks and positions
+  tree_attention    a tree's nodes over the pages and their own ancestors
+  kv_compact        the accepted path of a tree moved together
+and one pool of its pages, kept on the device:
+  pages_resize      pages taken and given back as requests grow and shrink
+  pages_select      requests forked, reordered and freed
+  kv_copy_pages     the copies that growing into a shared page asks for
 plus build_inverse_map (reduced vocabulary), philox_blocks and
 race_exponentials (bit-exact access to the random numbers).
 """
@@ -35,6 +43,7 @@ __all__ = [
     "markov_sample_deferred", "verify_deferred", "verify_deferred_workspace_size",
     "context_kv", "context_kv_workspace_size",
     "kv_append", "paged_attention", "paged_attention_workspace_size", "prompt_attention",
+    "tree_mask", "tree_attention", "kv_compact", "pages_resize", "pages_select", "kv_copy_pages",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdspark.so")
@@ -82,6 +91,17 @@ _SIGS = {
                                + [ctypes.c_float, _c_void_p, _c_size, _c_void_p]),
     "dspark_prompt_attention": (_c_int, [_c_void_p, _c_i64] * 3 + [_c_void_p] * 3 + [_c_int] * 6
                                 + [ctypes.c_float, _c_void_p]),
+    "dspark_paged_attention_window": (_c_int, [_c_void_p, _c_i64] + [_c_void_p] * 7 + [_c_int] * 12
+                                      + [ctypes.c_float, _c_void_p, _c_size, _c_void_p]),
+    "dspark_prompt_attention_window": (_c_int, [_c_void_p, _c_i64] * 3 + [_c_void_p] * 3 + [_c_int] * 7
+                                       + [ctypes.c_float, _c_void_p]),
+    "dspark_tree_mask": (_c_int, [_c_void_p] * 5 + [_c_int] * 3 + [_c_void_p]),
+    "dspark_tree_attention": (_c_int, [_c_void_p, _c_i64] + [_c_void_p] * 8 + [_c_int] * 9
+                              + [ctypes.c_float, _c_void_p, _c_size, _c_void_p]),
+    "dspark_kv_compact": (_c_int, [_c_void_p] * 8 + [_c_int] * 8 + [_c_void_p]),
+    "dspark_kv_copy_pages": (_c_int, [_c_void_p] * 3 + [_c_int] * 6 + [_c_void_p]),
+    "dspark_pages_resize": (_c_int, [_c_void_p] * 6 + [_c_int] * 4 + [_c_void_p]),
+    "dspark_pages_select": (_c_int, [_c_void_p] * 6 + [_c_int] * 5 + [_c_void_p]),
     "dspark_verify_deferred": (_c_int, [_c_void_p] * 8 + [_c_int] + [_c_void_p] * 3 + [_c_u64, _c_void_p, _c_void_p]
                                + [_c_int] * 3 + [_c_void_p, _c_size, _c_void_p]),
     "dspark_choose_k": (_c_int, [_c_void_p, _c_int, _c_int, _c_void_p, _c_int, _c_void_p, _c_void_p, _c_void_p]),
@@ -528,13 +548,13 @@ def _arg(t: Optional[torch.Tensor], name: str, dtypes, dev: int, shape) -> Optio
     return _ptr(t, name, dtypes, torch.device("cuda", dev), shape)
 
 
-def _device_of(t: torch.Tensor, name: str) -> int:
+def _device_of(t: torch.Tensor, name: str, dims: str = "[tokens, heads, hd]") -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device (cuda/hip) tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, hd], got shape {tuple(t.shape)}")
+    if t.dim() != dims.count(",") + 1:
+        raise ValueError(f"{name} must be {dims}, got shape {tuple(t.shape)}")
     return t.get_device()
 
 
@@ -594,16 +614,12 @@ def paged_attention_workspace_size(T: int, B: int, max_q: int, nh: int, nkv: int
     return load().dspark_paged_attention_workspace_size(T, B, max_q, nh, nkv, hd)
 
 
-def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
-                    kv_len: torch.Tensor, cu_q: torch.Tensor, max_q: int, page_size: int, causal: bool = True,
-                    scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
-                    lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """Attention of each request's few query tokens over its cache (dspark_paged_attention).
-    q [T, nh, hd] bf16, the tokens cu_q[b] .. cu_q[b+1] - 1 (cu_q [B+1] int32) of request b
-    being the last of its kv_len[b] (int32) cached ones; page p of k_cache, v_cache
-    [num_slots, nkv, hd] is the slots p * page_size .. and page_table [B, max_pages] int32
-    lists a request's pages.  scale defaults to hd ** -0.5.  lse [T, nh] float32, if given,
-    receives each row's log sum of exponentials.  Returns out [T, nh, hd]."""
+def _paged(name: str, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+           kv_len: torch.Tensor, cu_q: torch.Tensor, max_q: int, page_size: int, mask: Optional[torch.Tensor],
+           rule: tuple, scale: Optional[float], out: Optional[torch.Tensor], lse: Optional[torch.Tensor],
+           workspace: Optional[torch.Tensor]) -> torch.Tensor:
+    """The attentions over pages: what they share of checks and arguments; rule: the integers that
+    say what a row sees (mask: where a tree's mask does)."""
     dev = _device_of(q, "q")
     T, nh, hd = q.shape
     qs = _rows(q, "q", dev, T, nh, hd)
@@ -623,24 +639,86 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                          dtype=torch.uint8, device=q.device)
     elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{dev}")
-    _on(dev, "dspark_paged_attention", lib.dspark_paged_attention,
+    masks = () if name != "dspark_tree_attention" else (_arg(mask, "mask", _U32, dev, (T, 4)),)
+    _on(dev, name, getattr(lib, name),
         q.data_ptr(), qs, _arg(k_cache, "k_cache", _BF16, dev, (S, nkv, hd)),
         _arg(v_cache, "v_cache", _BF16, dev, (S, nkv, hd)), _arg(page_table, "page_table", _I32, dev, (B, width)),
-        _arg(kv_len, "kv_len", _I32, dev, (B,)), _arg(cu_q, "cu_q", _I32, dev, (B + 1,)),
+        _arg(kv_len, "kv_len", _I32, dev, (B,)), _arg(cu_q, "cu_q", _I32, dev, (B + 1,)), *masks,
         _arg(out, "out", _BF16, dev, (T, nh, hd)), _arg(lse, "lse", _F32, dev, (T, nh)), T, B, max_q, nh, nkv, hd,
-        page_size, width, S // page_size, 1 if causal else 0, hd ** -0.5 if scale is None else scale,
-        ws.data_ptr(), ws.numel())
+        page_size, width, S // page_size, *rule, hd ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel())
     return out
+
+
+def _window(window: Optional[int], sinks: int) -> tuple:
+    """window and sinks as the C ABI takes them, in 32 bits; () without a window."""
+    if window is None:
+        if sinks:
+            raise ValueError("sinks need a window")
+        return ()
+    return max(-1, min(window, 2 ** 31 - 1)), max(-1, min(sinks, 2 ** 31 - 1))
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                    kv_len: torch.Tensor, cu_q: torch.Tensor, max_q: int, page_size: int, causal: bool = True,
+                    scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    window: Optional[int] = None, sinks: int = 0) -> torch.Tensor:
+    """Attention of each request's few query tokens over its cache (dspark_paged_attention).
+    q [T, nh, hd] bf16, the tokens cu_q[b] .. cu_q[b+1] - 1 (cu_q [B+1] int32) of request b
+    being the last of its kv_len[b] (int32) cached ones; page p of k_cache, v_cache
+    [num_slots, nkv, hd] is the slots p * page_size .. and page_table [B, max_pages] int32
+    lists a request's pages.  scale defaults to hd ** -0.5.  lse [T, nh] float32, if given,
+    receives each row's log sum of exponentials.  With a window (dspark_paged_attention_window)
+    a token sees the last window keys up to its own place and the first sinks; the pages
+    between them may be gone from the table.  Returns out [T, nh, hd]."""
+    rule = _window(window, sinks)
+    return _paged("dspark_paged_attention_window" if rule else "dspark_paged_attention", q, k_cache, v_cache, page_table,
+                  kv_len, cu_q, max_q, page_size, None, (1 if causal else 0,) + rule, scale, out, lse, workspace)
+
+
+def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                   kv_len: torch.Tensor, cu_q: torch.Tensor, mask: torch.Tensor, max_q: int, page_size: int,
+                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_attention for blocks that are drafted trees (dspark_tree_attention): a query token
+    sees the context before the block, and the block's tokens that its mask [T, 4] int32 (128
+    bits, as tree_mask writes them) names.  The workspace is paged_attention's."""
+    return _paged("dspark_tree_attention", q, k_cache, v_cache, page_table, kv_len, cu_q, max_q, page_size, mask, (),
+                  scale, out, lse, workspace)
+
+
+def tree_mask(parent: torch.Tensor, kv_len: torch.Tensor, cu_q: torch.Tensor, max_q: int,
+              mask: Optional[torch.Tensor] = None,
+              positions: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Masks and places of drafted trees (dspark_tree_mask): parent [T] int32 is each node's
+    parent among its request's nodes cu_q[b] .. cu_q[b+1] - 1 (-1: it hangs on the context).
+    Returns mask [T, 4] int32, what each node sees of the block, and positions [T] int32, for
+    kv_append."""
+    dev = _device_of(parent, "parent", "[nodes]")
+    T = parent.shape[0]
+    if not isinstance(kv_len, torch.Tensor):
+        raise TypeError("kv_len must be a torch.Tensor")
+    B = kv_len.numel()
+    if mask is None:
+        mask = torch.empty((T, 4), dtype=torch.int32, device=parent.device)
+    if positions is None:
+        positions = torch.empty(T, dtype=torch.int32, device=parent.device)
+    _on(dev, "dspark_tree_mask", load().dspark_tree_mask,
+        _arg(parent, "parent", _I32, dev, (T,)), _arg(kv_len, "kv_len", _I32, dev, (B,)),
+        _arg(cu_q, "cu_q", _I32, dev, (B + 1,)), _arg(mask, "mask", _U32, dev, (T, 4)),
+        _arg(positions, "positions", _I32, dev, (T,)), T, B, max_q)
+    return mask, positions
 
 
 def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
                      causal: bool = True, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
-                     lse: Optional[torch.Tensor] = None) -> torch.Tensor:
+                     lse: Optional[torch.Tensor] = None, window: Optional[int] = None, sinks: int = 0) -> torch.Tensor:
     """Attention over packed prompts (dspark_prompt_attention): q [T, nh, hd], k and v
     [T, nkv, hd] bf16 (each may be a column range of one product), sequence b the tokens
     cu_seqlens[b] .. cu_seqlens[b+1] - 1 (int32 [B+1]).  scale defaults to hd ** -0.5.
-    lse [T, nh] float32, if given, receives each row's log sum of exponentials.
-    Returns out [T, nh, hd]."""
+    lse [T, nh] float32, if given, receives each row's log sum of exponentials.  With a window
+    (dspark_prompt_attention_window; causal only) a token sees the last window tokens up to
+    itself and the first sinks.  Returns out [T, nh, hd]."""
     dev = _device_of(q, "q")
     T, nh, hd = q.shape
     _device_of(k, "k")
@@ -650,10 +728,107 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     if not isinstance(cu_seqlens, torch.Tensor):
         raise TypeError("cu_seqlens must be a torch.Tensor")
     B = cu_seqlens.numel() - 1
+    rule = _window(window, sinks)
+    if rule and not causal:
+        raise ValueError("a window needs causal attention")
     if out is None:
         out = torch.empty((T, nh, hd), dtype=q.dtype, device=q.device)
-    _on(dev, "dspark_prompt_attention", load().dspark_prompt_attention,
+    name = "dspark_prompt_attention_window" if rule else "dspark_prompt_attention"
+    _on(dev, name, getattr(load(), name),
         q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _arg(cu_seqlens, "cu_seqlens", _I32, dev, (B + 1,)),
         _arg(out, "out", _BF16, dev, (T, nh, hd)), _arg(lse, "lse", _F32, dev, (T, nh)), T, B, nh, nkv, hd,
-        1 if causal else 0, hd ** -0.5 if scale is None else scale)
+        *(rule or (1 if causal else 0,)), hd ** -0.5 if scale is None else scale)
     return out
+
+
+# ---------------------------------------------------------------- rows and pages
+
+def _layers(k_cache: torch.Tensor, v_cache: torch.Tensor, dev: int, page_size: int):
+    """Caches of every layer [L, num_slots, nkv, hd], or of one without the first dimension."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() not in (3, 4):
+        raise ValueError("k_cache must be a tensor [L, num_slots, nkv, hd] or [num_slots, nkv, hd]")
+    S, nkv, hd = k_cache.shape[-3:]
+    if page_size < 1 or S % page_size:
+        raise ValueError(f"num_slots ({S}) must be a multiple of page_size ({page_size})")
+    return (_arg(k_cache, "k_cache", _BF16, dev, k_cache.shape), _arg(v_cache, "v_cache", _BF16, dev, k_cache.shape),
+            k_cache.shape[0] if k_cache.dim() == 4 else 1, nkv, hd, S // page_size)
+
+
+def _table(page_table: torch.Tensor) -> Tuple[int, int, int]:
+    return _device_of(page_table, "page_table", "[B, max_pages]"), page_table.shape[0], page_table.shape[1]
+
+
+def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
+               cu_q: torch.Tensor, path: torch.Tensor, accepted: torch.Tensor, page_size: int,
+               new_len: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The accepted path of each request's tree moved together, in place, in every layer of the
+    caches [L, num_slots, nkv, hd] (dspark_kv_compact): path [B, max_path] int32 lists the
+    accepted nodes, ascending, accepted [B] int32 says how many.  Returns new_len [B], the
+    context's length with them; kv_len stays as it is."""
+    dev, B, width = _table(page_table)
+    kp, vp, L, nkv, hd, pages = _layers(k_cache, v_cache, dev, page_size)
+    if not isinstance(path, torch.Tensor) or path.dim() != 2:
+        raise ValueError("path must be a tensor [B, max_path]")
+    if new_len is None:
+        new_len = torch.empty(B, dtype=torch.int32, device=page_table.device)
+    _on(dev, "dspark_kv_compact", load().dspark_kv_compact,
+        kp, vp, _arg(page_table, "page_table", _I32, dev, (B, width)), _arg(kv_len, "kv_len", _I32, dev, (B,)),
+        _arg(cu_q, "cu_q", _I32, dev, (B + 1,)), _arg(path, "path", _I32, dev, (B, path.shape[1])),
+        _arg(accepted, "accepted", _I32, dev, (B,)), _arg(new_len, "new_len", _I32, dev, (B,)), B, L, nkv, hd,
+        page_size, width, pages, path.shape[1])
+    return new_len
+
+
+def kv_copy_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, copies: torch.Tensor, page_size: int) -> None:
+    """Page copies[i, 0] copied to page copies[i, 1] in every layer of both caches
+    (dspark_kv_copy_pages); a pair with a negative side is passed over, as pages_resize
+    writes them."""
+    dev = _device_of(copies, "copies", "[n, 2]")
+    kp, vp, L, nkv, hd, pages = _layers(k_cache, v_cache, dev, page_size)
+    n = copies.shape[0]
+    _on(dev, "dspark_kv_copy_pages", load().dspark_kv_copy_pages,
+        kp, vp, _arg(copies, "copies", _I32, dev, (n, 2)), n, L, nkv, hd, page_size, pages)
+
+
+def pages_resize(page_table: torch.Tensor, kv_len: torch.Tensor, new_len: torch.Tensor, refs: torch.Tensor,
+                 page_size: int, copies: Optional[torch.Tensor] = None,
+                 served: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Every request brought to new_len [B] int32 tokens, in place (dspark_pages_resize):
+    page_table [B, max_pages], kv_len [B] and refs [num_pages], the entries that name each
+    page, int32, are updated.  Returns copies [B, 2], the pages to copy by kv_copy_pages before
+    anything is appended, and served [B], 0 where the free pages did not last."""
+    dev, B, width = _table(page_table)
+    _device_of(refs, "refs", "[num_pages]")
+    if copies is None:
+        copies = torch.empty((B, 2), dtype=torch.int32, device=page_table.device)
+    if served is None:
+        served = torch.empty(B, dtype=torch.int32, device=page_table.device)
+    _on(dev, "dspark_pages_resize", load().dspark_pages_resize,
+        _arg(page_table, "page_table", _I32, dev, (B, width)), _arg(kv_len, "kv_len", _I32, dev, (B,)),
+        _arg(new_len, "new_len", _I32, dev, (B,)), _arg(refs, "refs", _I32, dev, (refs.numel(),)),
+        _arg(copies, "copies", _I32, dev, (B, 2)), _arg(served, "served", _I32, dev, (B,)), B, page_size, width,
+        refs.numel())
+    return copies, served
+
+
+def pages_select(page_table: torch.Tensor, kv_len: torch.Tensor, src: torch.Tensor, refs: torch.Tensor,
+                 page_size: int, new_table: Optional[torch.Tensor] = None,
+                 new_len: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """A new table whose row r is row src[r] of the old (dspark_pages_select): a row taken twice
+    is forked, one not taken is freed, src[r] = -1 leaves row r empty.  refs count the new
+    table afterwards; the old one is done with.  Returns new_table [rows, max_pages] and
+    new_len [rows]."""
+    dev, B, width = _table(page_table)
+    _device_of(src, "src", "[rows]")
+    _device_of(refs, "refs", "[num_pages]")
+    rows = src.numel()
+    if new_table is None:
+        new_table = torch.empty((rows, width), dtype=torch.int32, device=page_table.device)
+    if new_len is None:
+        new_len = torch.empty(rows, dtype=torch.int32, device=page_table.device)
+    _on(dev, "dspark_pages_select", load().dspark_pages_select,
+        _arg(page_table, "page_table", _I32, dev, (B, width)), _arg(kv_len, "kv_len", _I32, dev, (B,)),
+        _arg(src, "src", _I32, dev, (rows,)), _arg(new_table, "new_table", _I32, dev, (rows, width)),
+        _arg(new_len, "new_len", _I32, dev, (rows,)), _arg(refs, "refs", _I32, dev, (refs.numel(),)), B, rows,
+        page_size, width, refs.numel())
+    return new_table, new_len

@@ -525,42 +525,53 @@ dspark_status attention_shape(int T, int B, int nh, int nkv, int hd, float scale
   REQUIRE((int64_t)T * nh < ((int64_t)1 << 30), DSPARK_ERR_UNSUPPORTED, "T * nh must be < 2^30");
   return DSPARK_OK;
 }
-}  // namespace
 
-extern "C" {
-
-dspark_status dspark_paged_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k_cache,
-                                     const uint16_t* v_cache, const int32_t* page_table, const int32_t* kv_len,
-                                     const int32_t* cu_q, uint16_t* out, float* lse, int T, int B, int max_q,
-                                     int nh, int nkv, int hd, int page_size, int max_pages, int num_pages,
-                                     int causal, float scale, void* workspace, size_t workspace_bytes,
-                                     void* stream) {
-  const dspark_status st = attention_shape(T, B, nh, nkv, hd, scale);
-  if (st != DSPARK_OK) return st;
-  REQUIRE(q_stride >= (int64_t)nh * hd && q_stride % 8 == 0, DSPARK_ERR_INVALID,
-          "q_stride must be a multiple of 8 and >= nh * hd (got %lld)", (long long)q_stride);
-  REQUIRE(max_q >= 1, DSPARK_ERR_INVALID, "max_q must be >= 1 (got %d)", max_q);
-  REQUIRE(max_q <= DSPARK_MAX_BLOCK, DSPARK_ERR_UNSUPPORTED, "max_q must be <= %d (got %d)", DSPARK_MAX_BLOCK, max_q);
+// what the calls on a page table check alike
+dspark_status table_shape(int page_size, int max_pages, int num_pages) {
   REQUIRE(page_size >= 1, DSPARK_ERR_INVALID, "page_size must be >= 1 (got %d)", page_size);
   REQUIRE((page_size & (page_size - 1)) == 0, DSPARK_ERR_UNSUPPORTED, "page_size must be a power of two (got %d)",
           page_size);
   REQUIRE(max_pages >= 1 && num_pages >= 1, DSPARK_ERR_INVALID, "max_pages and num_pages must be >= 1");
   REQUIRE((int64_t)max_pages * page_size <= ((int64_t)1 << 30) && (int64_t)num_pages * page_size < ((int64_t)1 << 31),
           DSPARK_ERR_UNSUPPORTED, "max_pages * page_size must be <= 2^30 and num_pages * page_size < 2^31");
-  REQUIRE(causal == 0 || causal == 1, DSPARK_ERR_INVALID, "causal must be 0 or 1 (got %d)", causal);
-  if (T == 0) return ok();
-  REQUIRE_PTR16(q, "q");
-  REQUIRE_PTR16(k_cache, "k_cache");
-  REQUIRE_PTR16(v_cache, "v_cache");
-  REQUIRE_PTR(page_table, "page_table");
-  REQUIRE_PTR(kv_len, "kv_len");
-  REQUIRE_PTR(cu_q, "cu_q");
-  REQUIRE_PTR16(out, "out");
-  const size_t need = dspark::paged_attention_workspace_bytes(T, B, max_q, nh, nkv, hd);
+  return DSPARK_OK;
+}
+
+// The attentions over pages: `a` complete but for what follows from these arguments.
+dspark_status paged_call(dspark::PagedArgs& a, int hd, int page_size, void* workspace, size_t workspace_bytes,
+                         hipError_t (*launch)(const dspark::PagedArgs&, int, void*, hipStream_t), const char* name,
+                         void* stream) {
+  dspark_status st = attention_shape(a.T, a.B, a.nh, a.nkv, hd, a.scale);
+  if (st != DSPARK_OK) return st;
+  REQUIRE(a.q_stride >= (int64_t)a.nh * hd && a.q_stride % 8 == 0, DSPARK_ERR_INVALID,
+          "q_stride must be a multiple of 8 and >= nh * hd (got %lld)", (long long)a.q_stride);
+  REQUIRE(a.max_q >= 1, DSPARK_ERR_INVALID, "max_q must be >= 1 (got %d)", a.max_q);
+  REQUIRE(a.max_q <= DSPARK_MAX_BLOCK, DSPARK_ERR_UNSUPPORTED, "max_q must be <= %d (got %d)", DSPARK_MAX_BLOCK,
+          a.max_q);
+  st = table_shape(page_size, a.width, a.num_pages);
+  if (st != DSPARK_OK) return st;
+  REQUIRE(a.causal == 0 || a.causal == 1, DSPARK_ERR_INVALID, "causal must be 0 or 1 (got %d)", a.causal);
+  if (a.T == 0) return ok();
+  REQUIRE_PTR16(a.q, "q");
+  REQUIRE_PTR16(a.k_cache, "k_cache");
+  REQUIRE_PTR16(a.v_cache, "v_cache");
+  REQUIRE_PTR(a.page_table, "page_table");
+  REQUIRE_PTR(a.kv_len, "kv_len");
+  REQUIRE_PTR(a.cu_q, "cu_q");
+  REQUIRE_PTR16(a.out, "out");
+  const size_t need = dspark::paged_attention_workspace_bytes(a.T, a.B, a.max_q, a.nh, a.nkv, hd);
   REQUIRE(workspace != nullptr, DSPARK_ERR_WORKSPACE, "workspace must not be NULL (%zu bytes needed)", need);
   REQUIRE(aligned16(workspace), DSPARK_ERR_INVALID, "workspace must be 16-byte aligned");
   REQUIRE(workspace_bytes >= need, DSPARK_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", workspace_bytes,
           need);
+  a.page_shift = __builtin_ctz((unsigned)page_size);
+  return hip_status(launch(a, hd, workspace, (hipStream_t)stream), name);
+}
+
+dspark::PagedArgs paged_args(const uint16_t* q, int64_t q_stride, const uint16_t* k_cache, const uint16_t* v_cache,
+                             const int32_t* page_table, const int32_t* kv_len, const int32_t* cu_q, uint16_t* out,
+                             float* lse, int T, int B, int max_q, int nh, int nkv, int max_pages, int num_pages,
+                             float scale) {
   dspark::PagedArgs a;
   a.q = q;
   a.k_cache = k_cache;
@@ -576,33 +587,46 @@ dspark_status dspark_paged_attention(const uint16_t* q, int64_t q_stride, const 
   a.max_q = max_q;
   a.nh = nh;
   a.nkv = nkv;
-  a.page_shift = __builtin_ctz((unsigned)page_size);
   a.width = max_pages;
   a.num_pages = num_pages;
-  a.causal = causal;
   a.scale = scale;
-  return hip_status(dspark::launch_paged_attention(a, hd, workspace, (hipStream_t)stream), "paged_attention");
+  return a;
 }
 
-dspark_status dspark_prompt_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
-                                      const uint16_t* v, int64_t v_stride, const int32_t* cu_seqlens, uint16_t* out,
-                                      float* lse, int T, int B, int nh, int nkv, int hd, int causal, float scale,
-                                      void* stream) {
-  const dspark_status st = attention_shape(T, B, nh, nkv, hd, scale);
+dspark_status window_shape(int window, int sinks) {
+  REQUIRE(window >= 1, DSPARK_ERR_INVALID, "window must be >= 1 (got %d)", window);
+  REQUIRE(sinks >= 0, DSPARK_ERR_INVALID, "sinks must be >= 0 (got %d)", sinks);
+  return DSPARK_OK;
+}
+
+// no length passes 2^30: a longer window or more sinks say the same
+int bounded(int v) { return v < (1 << 30) ? v : (1 << 30); }
+
+dspark_status prompt_call(dspark::PromptArgs& a, int hd,
+                          hipError_t (*launch)(const dspark::PromptArgs&, int, hipStream_t), const char* name,
+                          void* stream) {
+  const dspark_status st = attention_shape(a.T, a.B, a.nh, a.nkv, hd, a.scale);
   if (st != DSPARK_OK) return st;
-  const int64_t qrow = (int64_t)nh * hd, krow = (int64_t)nkv * hd;
-  REQUIRE(q_stride >= qrow && q_stride % 8 == 0, DSPARK_ERR_INVALID,
-          "q_stride must be a multiple of 8 and >= nh * hd (got %lld)", (long long)q_stride);
-  REQUIRE(k_stride >= krow && k_stride % 8 == 0 && v_stride >= krow && v_stride % 8 == 0, DSPARK_ERR_INVALID,
+  const int64_t qrow = (int64_t)a.nh * hd, krow = (int64_t)a.nkv * hd;
+  REQUIRE(a.q_stride >= qrow && a.q_stride % 8 == 0, DSPARK_ERR_INVALID,
+          "q_stride must be a multiple of 8 and >= nh * hd (got %lld)", (long long)a.q_stride);
+  REQUIRE(a.k_stride >= krow && a.k_stride % 8 == 0 && a.v_stride >= krow && a.v_stride % 8 == 0, DSPARK_ERR_INVALID,
           "k_stride and v_stride must be multiples of 8 and >= nkv * hd");
-  REQUIRE(k_stride < (1 << 24) && v_stride < (1 << 24), DSPARK_ERR_UNSUPPORTED, "k_stride and v_stride must be < 2^24");
-  REQUIRE(causal == 0 || causal == 1, DSPARK_ERR_INVALID, "causal must be 0 or 1 (got %d)", causal);
-  if (T == 0) return ok();
-  REQUIRE_PTR16(q, "q");
-  REQUIRE_PTR16(k, "k");
-  REQUIRE_PTR16(v, "v");
-  REQUIRE_PTR(cu_seqlens, "cu_seqlens");
-  REQUIRE_PTR16(out, "out");
+  REQUIRE(a.k_stride < (1 << 24) && a.v_stride < (1 << 24), DSPARK_ERR_UNSUPPORTED,
+          "k_stride and v_stride must be < 2^24");
+  REQUIRE(a.causal == 0 || a.causal == 1, DSPARK_ERR_INVALID, "causal must be 0 or 1 (got %d)", a.causal);
+  if (a.T == 0) return ok();
+  REQUIRE_PTR16(a.q, "q");
+  REQUIRE_PTR16(a.k, "k");
+  REQUIRE_PTR16(a.v, "v");
+  REQUIRE_PTR(a.cu_seqlens, "cu_seqlens");
+  REQUIRE_PTR16(a.out, "out");
+  return hip_status(launch(a, hd, (hipStream_t)stream), name);
+}
+
+dspark::PromptArgs prompt_args(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                               const uint16_t* v, int64_t v_stride, const int32_t* cu_seqlens, uint16_t* out,
+                               float* lse, int T, int B, int nh, int nkv, int causal, float scale) {
   dspark::PromptArgs a;
   a.q = q;
   a.k = k;
@@ -619,7 +643,254 @@ dspark_status dspark_prompt_attention(const uint16_t* q, int64_t q_stride, const
   a.nkv = nkv;
   a.causal = causal;
   a.scale = scale;
-  return hip_status(dspark::launch_prompt_attention(a, hd, (hipStream_t)stream), "prompt_attention");
+  return a;
+}
+
+// the caches of every layer, moved by rows or pages of whole 16-byte pieces
+dspark_status cache_rows(const uint16_t* k_cache, const uint16_t* v_cache, int L, int nkv, int hd) {
+  REQUIRE(nkv >= 1 && hd >= 1 && ((int64_t)nkv * hd) % 8 == 0, DSPARK_ERR_INVALID,
+          "nkv * hd must be a positive multiple of 8 (got nkv=%d, hd=%d)", nkv, hd);
+  REQUIRE((int64_t)nkv * hd <= (1 << 18), DSPARK_ERR_UNSUPPORTED, "nkv * hd must be <= 2^18");
+  REQUIRE(L >= 1, DSPARK_ERR_INVALID, "L must be >= 1 (got %d)", L);
+  REQUIRE(L <= 1024, DSPARK_ERR_UNSUPPORTED, "L must be <= 1024 (got %d)", L);
+  REQUIRE_PTR16(k_cache, "k_cache");
+  REQUIRE_PTR16(v_cache, "v_cache");
+  return DSPARK_OK;
+}
+
+dspark_status batch_of(int B, const char* name) {
+  REQUIRE(B >= 1, DSPARK_ERR_INVALID, "%s must be >= 1 (got %d)", name, B);
+  REQUIRE(B <= DSPARK_MAX_SEQS, DSPARK_ERR_UNSUPPORTED, "%s must be <= %d (got %d)", name, DSPARK_MAX_SEQS, B);
+  return DSPARK_OK;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+}  // namespace
+
+extern "C" {
+
+dspark_status dspark_paged_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k_cache,
+                                     const uint16_t* v_cache, const int32_t* page_table, const int32_t* kv_len,
+                                     const int32_t* cu_q, uint16_t* out, float* lse, int T, int B, int max_q,
+                                     int nh, int nkv, int hd, int page_size, int max_pages, int num_pages,
+                                     int causal, float scale, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  dspark::PagedArgs a = paged_args(q, q_stride, k_cache, v_cache, page_table, kv_len, cu_q, out, lse, T, B, max_q, nh,
+                                   nkv, max_pages, num_pages, scale);
+  a.causal = causal;
+  return paged_call(a, hd, page_size, workspace, workspace_bytes, dspark::launch_paged_attention, "paged_attention",
+                    stream);
+}
+
+dspark_status dspark_paged_attention_window(const uint16_t* q, int64_t q_stride, const uint16_t* k_cache,
+                                            const uint16_t* v_cache, const int32_t* page_table,
+                                            const int32_t* kv_len, const int32_t* cu_q, uint16_t* out, float* lse,
+                                            int T, int B, int max_q, int nh, int nkv, int hd, int page_size,
+                                            int max_pages, int num_pages, int causal, int window, int sinks,
+                                            float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  const dspark_status st = window_shape(window, sinks);
+  if (st != DSPARK_OK) return st;
+  dspark::PagedArgs a = paged_args(q, q_stride, k_cache, v_cache, page_table, kv_len, cu_q, out, lse, T, B, max_q, nh,
+                                   nkv, max_pages, num_pages, scale);
+  a.causal = causal;
+  a.window = bounded(window);
+  a.sinks = bounded(sinks);
+  a.sink_keys = (a.sinks + 31) / 32 * 32;
+  return paged_call(a, hd, page_size, workspace, workspace_bytes, dspark::launch_paged_window,
+                    "paged_attention_window", stream);
+}
+
+dspark_status dspark_tree_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k_cache,
+                                    const uint16_t* v_cache, const int32_t* page_table, const int32_t* kv_len,
+                                    const int32_t* cu_q, const uint32_t* mask, uint16_t* out, float* lse, int T,
+                                    int B, int max_q, int nh, int nkv, int hd, int page_size, int max_pages,
+                                    int num_pages, float scale, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  if (T > 0) REQUIRE_PTR16(mask, "mask");
+  dspark::PagedArgs a = paged_args(q, q_stride, k_cache, v_cache, page_table, kv_len, cu_q, out, lse, T, B, max_q, nh,
+                                   nkv, max_pages, num_pages, scale);
+  a.mask = mask;
+  return paged_call(a, hd, page_size, workspace, workspace_bytes, dspark::launch_tree_attention, "tree_attention",
+                    stream);
+}
+
+dspark_status dspark_prompt_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                      const uint16_t* v, int64_t v_stride, const int32_t* cu_seqlens, uint16_t* out,
+                                      float* lse, int T, int B, int nh, int nkv, int hd, int causal, float scale,
+                                      void* stream) {
+  dspark::PromptArgs a =
+      prompt_args(q, q_stride, k, k_stride, v, v_stride, cu_seqlens, out, lse, T, B, nh, nkv, causal, scale);
+  return prompt_call(a, hd, dspark::launch_prompt_attention, "prompt_attention", stream);
+}
+
+dspark_status dspark_prompt_attention_window(const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                                             int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                                             const int32_t* cu_seqlens, uint16_t* out, float* lse, int T, int B,
+                                             int nh, int nkv, int hd, int window, int sinks, float scale,
+                                             void* stream) {
+  const dspark_status st = window_shape(window, sinks);
+  if (st != DSPARK_OK) return st;
+  dspark::PromptArgs a =
+      prompt_args(q, q_stride, k, k_stride, v, v_stride, cu_seqlens, out, lse, T, B, nh, nkv, 1, scale);
+  a.window = bounded(window);
+  a.sinks = bounded(sinks);
+  return prompt_call(a, hd, dspark::launch_prompt_window, "prompt_attention_window", stream);
+}
+
+dspark_status dspark_tree_mask(const int32_t* parent, const int32_t* kv_len, const int32_t* cu_q, uint32_t* mask,
+                               int32_t* positions, int T, int B, int max_q, void* stream) {
+  REQUIRE(T >= 0, DSPARK_ERR_INVALID, "T must be >= 0 (got %d)", T);
+  const dspark_status st = batch_of(B, "B");
+  if (st != DSPARK_OK) return st;
+  REQUIRE(max_q >= 1, DSPARK_ERR_INVALID, "max_q must be >= 1 (got %d)", max_q);
+  REQUIRE(max_q <= DSPARK_MAX_BLOCK, DSPARK_ERR_UNSUPPORTED, "max_q must be <= %d (got %d)", DSPARK_MAX_BLOCK, max_q);
+  if (T == 0) return ok();
+  REQUIRE_PTR(parent, "parent");
+  REQUIRE_PTR(kv_len, "kv_len");
+  REQUIRE_PTR(cu_q, "cu_q");
+  REQUIRE_PTR16(mask, "mask");
+  dspark::TreeArgs a;
+  a.parent = parent;
+  a.kv_len = kv_len;
+  a.cu_q = cu_q;
+  a.mask = mask;
+  a.positions = positions;
+  a.T = T;
+  a.B = B;
+  a.max_q = max_q;
+  return hip_status(dspark::launch_tree_mask(a, (hipStream_t)stream), "tree_mask");
+}
+
+dspark_status dspark_kv_compact(uint16_t* k_cache, uint16_t* v_cache, const int32_t* page_table,
+                                const int32_t* kv_len, const int32_t* cu_q, const int32_t* path,
+                                const int32_t* accepted, int32_t* new_len, int B, int L, int nkv, int hd,
+                                int page_size, int max_pages, int num_pages, int max_path, void* stream) {
+  dspark_status st = batch_of(B, "B");
+  if (st == DSPARK_OK) st = table_shape(page_size, max_pages, num_pages);
+  if (st == DSPARK_OK) st = cache_rows(k_cache, v_cache, L, nkv, hd);
+  if (st != DSPARK_OK) return st;
+  REQUIRE(max_path >= 1, DSPARK_ERR_INVALID, "max_path must be >= 1 (got %d)", max_path);
+  REQUIRE(max_path <= DSPARK_MAX_BLOCK, DSPARK_ERR_UNSUPPORTED, "max_path must be <= %d (got %d)", DSPARK_MAX_BLOCK,
+          max_path);
+  REQUIRE_PTR(page_table, "page_table");
+  REQUIRE_PTR(kv_len, "kv_len");
+  REQUIRE_PTR(cu_q, "cu_q");
+  REQUIRE_PTR(path, "path");
+  REQUIRE_PTR(accepted, "accepted");
+  REQUIRE(!overlap(new_len, 4 * (size_t)B, kv_len, 4 * (size_t)B), DSPARK_ERR_INVALID, "new_len must not be kv_len");
+  dspark::CompactArgs a;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.page_table = page_table;
+  a.kv_len = kv_len;
+  a.cu_q = cu_q;
+  a.path = path;
+  a.accepted = accepted;
+  a.new_len = new_len;
+  a.row_pieces = (uint32_t)nkv * hd / 8;
+  a.layer_pieces = (int64_t)num_pages * page_size * a.row_pieces;
+  a.B = B;
+  a.layers = L;
+  a.page_shift = __builtin_ctz((unsigned)page_size);
+  a.width = max_pages;
+  a.num_pages = num_pages;
+  a.max_path = max_path;
+  return hip_status(dspark::launch_kv_compact(a, (hipStream_t)stream), "kv_compact");
+}
+
+dspark_status dspark_kv_copy_pages(uint16_t* k_cache, uint16_t* v_cache, const int32_t* copies, int n, int L,
+                                   int nkv, int hd, int page_size, int num_pages, void* stream) {
+  REQUIRE(n >= 0, DSPARK_ERR_INVALID, "n must be >= 0 (got %d)", n);
+  REQUIRE(n <= (1 << 20), DSPARK_ERR_UNSUPPORTED, "n must be <= 2^20 (got %d)", n);
+  dspark_status st = table_shape(page_size, 1, num_pages);
+  if (st == DSPARK_OK) st = cache_rows(k_cache, v_cache, L, nkv, hd);
+  if (st != DSPARK_OK) return st;
+  if (n == 0) return ok();
+  REQUIRE_PTR(copies, "copies");
+  REQUIRE((reinterpret_cast<uintptr_t>(copies) & 7u) == 0, DSPARK_ERR_INVALID, "copies must be 8-byte aligned");
+  dspark::CopyArgs a;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.copies = copies;
+  a.page_pieces = (int64_t)page_size * nkv * hd / 8;
+  a.layer_pieces = (int64_t)num_pages * a.page_pieces;
+  a.n = n;
+  a.layers = L;
+  a.num_pages = num_pages;
+  return hip_status(dspark::launch_kv_copy_pages(a, (hipStream_t)stream), "kv_copy_pages");
+}
+
+dspark_status dspark_pages_select(const int32_t* page_table, const int32_t* kv_len, const int32_t* src,
+                                  int32_t* new_table, int32_t* new_len, int32_t* refs, int B, int rows,
+                                  int page_size, int max_pages, int num_pages, void* stream) {
+  dspark_status st = batch_of(B, "B");
+  if (st == DSPARK_OK) st = batch_of(rows, "rows");
+  if (st == DSPARK_OK) st = table_shape(page_size, max_pages, num_pages);
+  if (st != DSPARK_OK) return st;
+  REQUIRE_PTR(page_table, "page_table");
+  REQUIRE_PTR(kv_len, "kv_len");
+  REQUIRE_PTR(src, "src");
+  REQUIRE_PTR(new_table, "new_table");
+  REQUIRE_PTR(new_len, "new_len");
+  REQUIRE_PTR(refs, "refs");
+  const size_t was = 4 * (size_t)B, now = 4 * (size_t)rows;
+  REQUIRE(!overlap(page_table, was * max_pages, new_table, now * max_pages), DSPARK_ERR_INVALID,
+          "new_table must not overlap page_table");
+  REQUIRE(!overlap(kv_len, was, new_len, now) && !overlap(src, now, new_len, now), DSPARK_ERR_INVALID,
+          "new_len must not overlap kv_len or src");
+  dspark::SelectArgs a;
+  a.page_table = page_table;
+  a.kv_len = kv_len;
+  a.src = src;
+  a.new_table = new_table;
+  a.new_len = new_len;
+  a.refs = refs;
+  a.B = B;
+  a.rows = rows;
+  a.page_shift = __builtin_ctz((unsigned)page_size);
+  a.width = max_pages;
+  a.num_pages = num_pages;
+  return hip_status(dspark::launch_pages_select(a, (hipStream_t)stream), "pages_select");
+}
+
+dspark_status dspark_pages_resize(int32_t* page_table, int32_t* kv_len, const int32_t* new_len, int32_t* refs,
+                                  int32_t* copies, int32_t* served, int B, int page_size, int max_pages,
+                                  int num_pages, void* stream) {
+  dspark_status st = batch_of(B, "B");
+  if (st == DSPARK_OK) st = table_shape(page_size, max_pages, num_pages);
+  if (st != DSPARK_OK) return st;
+  REQUIRE_PTR(page_table, "page_table");
+  REQUIRE_PTR(kv_len, "kv_len");
+  REQUIRE_PTR(new_len, "new_len");
+  REQUIRE_PTR16(refs, "refs");
+  REQUIRE((reinterpret_cast<uintptr_t>(copies) & 7u) == 0, DSPARK_ERR_INVALID, "copies must be 8-byte aligned");
+  const size_t n = 4 * (size_t)B;
+  const struct {
+    const void* p;
+    size_t bytes;
+    const char* name;
+  } arrays[] = {{page_table, n * max_pages, "page_table"}, {kv_len, n, "kv_len"},
+                {new_len, n, "new_len"},                   {refs, 4 * (size_t)num_pages, "refs"},
+                {copies, 2 * n, "copies"},                 {served, n, "served"}};
+  for (int x = 0; x < 6; ++x)
+    for (int y = x + 1; y < 6; ++y)
+      REQUIRE(!overlap(arrays[x].p, arrays[x].bytes, arrays[y].p, arrays[y].bytes), DSPARK_ERR_INVALID,
+              "%s must not overlap %s", arrays[y].name, arrays[x].name);
+  dspark::ResizeArgs a;
+  a.page_table = page_table;
+  a.kv_len = kv_len;
+  a.new_len = new_len;
+  a.refs = refs;
+  a.copies = copies;
+  a.served = served;
+  a.B = B;
+  a.page_shift = __builtin_ctz((unsigned)page_size);
+  a.width = max_pages;
+  a.num_pages = num_pages;
+  return hip_status(dspark::launch_pages_resize(a, (hipStream_t)stream), "pages_resize");
 }
 
 dspark_status dspark_admit(const float* cond_accept, int B, int N, int K, float* survival, int32_t* admit_len,

@@ -170,9 +170,13 @@ struct PagedArgs {
   int page_shift = 0, width = 0, num_pages = 0;
   int causal = 0;
   float scale = 0.0f;
+  int window = 0, sinks = 0, sink_keys = 0;   // window attention; sink_keys: sinks up to whole tiles of 32
+  const uint32_t* mask = nullptr;     // tree attention: [T, 4], bit i of a node's 128: it sees node i of its block
 };
 size_t paged_attention_workspace_bytes(int T, int B, int max_q, int nh, int nkv, int hd);
 hipError_t launch_paged_attention(const PagedArgs& a, int hd, void* workspace, hipStream_t stream);
+hipError_t launch_paged_window(const PagedArgs& a, int hd, void* workspace, hipStream_t stream);
+hipError_t launch_tree_attention(const PagedArgs& a, int hd, void* workspace, hipStream_t stream);
 
 struct PromptArgs {
   const uint16_t* q = nullptr;        // [T, nh, hd] bf16, rows q_stride apart
@@ -185,8 +189,68 @@ struct PromptArgs {
   int T = 0, B = 0, nh = 0, nkv = 0;
   int causal = 0;
   float scale = 0.0f;
+  int window = 0, sinks = 0;          // window attention
 };
 hipError_t launch_prompt_attention(const PromptArgs& a, int hd, hipStream_t stream);
+hipError_t launch_prompt_window(const PromptArgs& a, int hd, hipStream_t stream);
+
+// ---- drafted trees, and the cache's rows and pages
+struct TreeArgs {
+  const int32_t* parent = nullptr;    // [T], of a request's own nodes; -1: none
+  const int32_t* kv_len = nullptr;    // [B]
+  const int32_t* cu_q = nullptr;      // [B + 1]
+  uint32_t* mask = nullptr;           // [T, 4]
+  int32_t* positions = nullptr;       // [T] or null
+  int T = 0, B = 0, max_q = 0;
+};
+hipError_t launch_tree_mask(const TreeArgs& a, hipStream_t stream);
+
+constexpr int kMaxPath = 128;
+struct CompactArgs {
+  uint16_t* k_cache = nullptr;        // [layers, num_pages << page_shift, row], in pieces of 16 bytes
+  uint16_t* v_cache = nullptr;
+  const int32_t* page_table = nullptr;  // [B, width]
+  const int32_t* kv_len = nullptr;    // [B]
+  const int32_t* cu_q = nullptr;      // [B + 1]
+  const int32_t* path = nullptr;      // [B, max_path]
+  const int32_t* accepted = nullptr;  // [B]
+  int32_t* new_len = nullptr;         // [B] or null; not kv_len
+  int64_t layer_pieces = 0;
+  uint32_t row_pieces = 0;
+  int B = 0, layers = 0, page_shift = 0, width = 0, num_pages = 0, max_path = 0;
+};
+hipError_t launch_kv_compact(const CompactArgs& a, hipStream_t stream);
+
+struct CopyArgs {
+  uint16_t* k_cache = nullptr;
+  uint16_t* v_cache = nullptr;
+  const int32_t* copies = nullptr;    // [n, 2]
+  int64_t layer_pieces = 0, page_pieces = 0;
+  int n = 0, layers = 0, num_pages = 0;
+};
+hipError_t launch_kv_copy_pages(const CopyArgs& a, hipStream_t stream);
+
+struct SelectArgs {
+  const int32_t* page_table = nullptr;  // [B, width]
+  const int32_t* kv_len = nullptr;    // [B]
+  const int32_t* src = nullptr;       // [rows]
+  int32_t* new_table = nullptr;       // [rows, width]
+  int32_t* new_len = nullptr;         // [rows]
+  int32_t* refs = nullptr;            // [num_pages]
+  int B = 0, rows = 0, page_shift = 0, width = 0, num_pages = 0;
+};
+hipError_t launch_pages_select(const SelectArgs& a, hipStream_t stream);
+
+struct ResizeArgs {
+  int32_t* page_table = nullptr;      // [B, width]
+  int32_t* kv_len = nullptr;          // [B]
+  const int32_t* new_len = nullptr;   // [B]
+  int32_t* refs = nullptr;            // [num_pages], 16-byte aligned
+  int32_t* copies = nullptr;          // [B, 2] or null
+  int32_t* served = nullptr;          // [B] or null
+  int B = 0, page_shift = 0, width = 0, num_pages = 0;
+};
+hipError_t launch_pages_resize(const ResizeArgs& a, hipStream_t stream);
 
 // launch_verify with the library's static per-device scratch array as workspace
 constexpr size_t kVerifyScratchBytes = (size_t)4 << 20;

@@ -18,6 +18,13 @@
  *   dspark_kv_append      a layer's new tokens into that cache, normed and rotated
  *   dspark_paged_attention  a round's few query tokens over the pages of that cache
  *   dspark_prompt_attention attention over whole packed prompts
+ *   dspark_paged_attention_window, dspark_prompt_attention_window
+ *                          both under a sliding window with sinks
+ *   dspark_tree_mask, dspark_tree_attention
+ *                          a drafted tree's masks, and its nodes' attention over the cache
+ *   dspark_kv_compact      the accepted path of a tree moved together in the cache
+ *   dspark_pages_resize, dspark_pages_select, dspark_kv_copy_pages
+ *                          pages taken, given back, shared and copied
  *
  * Conventions shared by every call
  *   Memory     Every pointer argument is device memory (HBM) unless stated otherwise.
@@ -498,6 +505,123 @@ dspark_status dspark_prompt_attention(const uint16_t* q, int64_t q_stride, const
                                       const uint16_t* v, int64_t v_stride, const int32_t* cu_seqlens, uint16_t* out,
                                       float* lse, int T, int B, int nh, int nkv, int hd, int causal, float scale,
                                       void* stream);
+
+/* ---------------------------------------------------------------- windows with sinks
+ * The two attentions above for layers that look back a limited way: of the keys that a row
+ * sees there, the one at place p = kv_len[b] - n_b + j (of a prompt: its token's place) sees
+ * those with s > p - window, and those with s < sinks (the first tokens, which keep drawing
+ * weight however far the window has moved).  Everything else, errors, layouts, arithmetic,
+ * workspace and lse included, is as dspark_paged_attention and dspark_prompt_attention say; a
+ * window that reaches past the beginning gives their results.
+ *   Only the keys that some row of a request sees are read.  The pages behind the windows,
+ *   but for the sinks', may have been given back: their table entries may be -1.
+ *   causal 0: keys behind the row's place are seen as before, the window limits those before
+ *   it.  Prompts under a window are causal.
+ *   window >= 1; sinks >= 0 (both may pass the length). */
+dspark_status dspark_paged_attention_window(const uint16_t* q, int64_t q_stride, const uint16_t* k_cache,
+                                            const uint16_t* v_cache, const int32_t* page_table,
+                                            const int32_t* kv_len, const int32_t* cu_q, uint16_t* out, float* lse,
+                                            int T, int B, int max_q, int nh, int nkv, int hd, int page_size,
+                                            int max_pages, int num_pages, int causal, int window, int sinks,
+                                            float scale, void* workspace, size_t workspace_bytes, void* stream);
+dspark_status dspark_prompt_attention_window(const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                                             int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                                             const int32_t* cu_seqlens, uint16_t* out, float* lse, int T, int B,
+                                             int nh, int nkv, int hd, int window, int sinks, float scale,
+                                             void* stream);
+
+/* ---------------------------------------------------------------- drafted trees
+ * A round may draft a tree instead of a chain: several continuations of one prefix, verified
+ * in one forward.  Its nodes are the request's query tokens cu_q[b] .. cu_q[b+1] - 1, node 0
+ * usually the anchor, every node behind its parent.
+ *
+ * dspark_tree_mask, once a round: parent[t] is the index among the request's nodes of t's
+ * parent, -1 for a node that hangs on the context itself (a parent outside 0 .. j - 1 of
+ * node j counts as -1).
+ *   mask[t]: 128 bits, words lowest first; bit i: node i is t itself or above it.
+ *   positions[t] = kv_len[b] - n_b + (nodes above t): its place in the sequence, for
+ *   dspark_kv_append's rotation.  NULL: not wanted.
+ *   parent, positions [T] int32; mask [T, 4] 32-bit words, 16-byte aligned; kv_len, cu_q,
+ *   max_q, B, T as dspark_paged_attention's.  Rows of tokens beyond max_q or behind
+ *   cu_q[B] are left as they were.
+ *
+ * dspark_tree_attention, once a layer, after the nodes' keys and values are in the cache:
+ * dspark_paged_attention with the rule that node j of request b sees every key of the
+ * context, s < kv_len[b] - n_b, and of the block's keys kv_len[b] - n_b + i those whose bit
+ * i of mask is set (any 128 bits, trees or not; bits of nodes that do not exist count for
+ * nothing).  The workspace is dspark_paged_attention's. */
+dspark_status dspark_tree_mask(const int32_t* parent, const int32_t* kv_len, const int32_t* cu_q, uint32_t* mask,
+                               int32_t* positions, int T, int B, int max_q, void* stream);
+dspark_status dspark_tree_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k_cache,
+                                    const uint16_t* v_cache, const int32_t* page_table, const int32_t* kv_len,
+                                    const int32_t* cu_q, const uint32_t* mask, uint16_t* out, float* lse, int T,
+                                    int B, int max_q, int nh, int nkv, int hd, int page_size, int max_pages,
+                                    int num_pages, float scale, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* ---------------------------------------------------------------- rows of accepted paths
+ * After a tree's verification: the keys and values of the accepted path, which lie among the
+ * rejected nodes', move together behind the context, in every layer.
+ *   token kv_len[b] - n_b + i takes the rows of token kv_len[b] - n_b + path[b, i]
+ *   for i < accepted[b]; new_len[b] = kv_len[b] - n_b + accepted[b] (NULL: not wanted).
+ *   path [B, max_path] int32, the accepted nodes from the first on: ascending, each in
+ *   0 .. n_b - 1.  It ends before the first entry that is not (accepted counts as many then).
+ *   accepted [B] int32, taken as at most max_path and at least 0; new_len [B] int32, another
+ *   array than kv_len.
+ *   k_cache, v_cache [L, num_pages * page_size, nkv, hd] bf16, 16-byte aligned, every layer
+ *   under the same page_table; page_table, kv_len, cu_q as dspark_paged_attention's.  A row
+ *   whose place, old or new, has no page is left out.  Pages that are written must belong to
+ *   one request (dspark_pages_resize sees to that).  Other rows keep their values.
+ *   nkv * hd % 8 == 0 and <= 2^18; 1 <= L <= 1024; 1 <= max_path <= DSPARK_MAX_BLOCK. */
+dspark_status dspark_kv_compact(uint16_t* k_cache, uint16_t* v_cache, const int32_t* page_table,
+                                const int32_t* kv_len, const int32_t* cu_q, const int32_t* path,
+                                const int32_t* accepted, int32_t* new_len, int B, int L, int nkv, int hd,
+                                int page_size, int max_pages, int num_pages, int max_path, void* stream);
+
+/* ---------------------------------------------------------------- pages
+ * A pool of num_pages pages, kept on the device, so that a captured round can take and give
+ * back pages.  refs[p] [num_pages] int32 is the number of table entries that name page p; a
+ * page with refs 0 is free.  A request of kv_len tokens holds the first
+ * ceil(kv_len / page_size) entries of its table row; the others mean nothing, and the calls
+ * write -1 where an entry ends.  An entry outside [0, num_pages) is passed over (a page
+ * dropped behind a window: set it to -1 and count it off).  Lengths are taken as at least 0
+ * and at most max_pages * page_size.  Results do not depend on the order in which the device
+ * works.
+ *
+ * dspark_pages_resize brings every request to new_len tokens, in place.
+ *   Shorter: the pages behind the new end are given back, before anything else is done.
+ *   Longer, request after request: a last page that is not full but shared (refs > 1) is
+ *   replaced by a free page of the request's own; copies[b] = (shared page, own page), the
+ *   copy that the caller carries out by dspark_kv_copy_pages before it appends.  The last of
+ *   the requests that share a page and grow keeps it.  Further pages follow.  Free pages are
+ *   taken lowest first.
+ *   If they run out, that request and all behind it that need a page, or grow into a shared
+ *   one, are not served: their rows and lengths stay (served[b] = 0).
+ *   copies [B, 2] int32, (-1, -1) where nothing is to be copied, or NULL; served [B] int32, 0
+ *   or 1, or NULL; refs 16-byte aligned, copies 8-byte aligned; no array may overlap another.
+ *
+ * dspark_pages_select makes a new table out of rows of the old: row r of new_table is row
+ * src[r] of page_table, new_len[r] its length; a row number outside [0, B) gives an empty
+ * row.  Afterwards refs count the new table in place of the old one, whose rows mean nothing
+ * any more.  A row taken twice is a fork, a row not taken is freed, a permutation reorders:
+ * beams, samples, a batch closed up.
+ *   page_table [B, max_pages], new_table [rows, max_pages], not overlapping; kv_len [B],
+ *   new_len [rows], src [rows].  1 <= rows <= DSPARK_MAX_SEQS.
+ *
+ * dspark_kv_copy_pages copies pages of every layer: page copies[i, 0] to copies[i, 1], for
+ * both caches.  A pair with a side outside [0, num_pages) is passed over.  A page may be the
+ * source of several pairs, the destination of one; no page may be both.
+ *   copies [n, 2] int32, 8-byte aligned; caches as dspark_kv_compact's; n == 0 enqueues
+ *   nothing.  n <= 2^20.
+ *   page_size a power of two, num_pages * page_size < 2^31, max_pages * page_size <= 2^30. */
+dspark_status dspark_pages_resize(int32_t* page_table, int32_t* kv_len, const int32_t* new_len, int32_t* refs,
+                                  int32_t* copies, int32_t* served, int B, int page_size, int max_pages,
+                                  int num_pages, void* stream);
+dspark_status dspark_pages_select(const int32_t* page_table, const int32_t* kv_len, const int32_t* src,
+                                  int32_t* new_table, int32_t* new_len, int32_t* refs, int B, int rows,
+                                  int page_size, int max_pages, int num_pages, void* stream);
+dspark_status dspark_kv_copy_pages(uint16_t* k_cache, uint16_t* v_cache, const int32_t* copies, int n, int L,
+                                   int nkv, int hd, int page_size, int num_pages, void* stream);
 
 /* ---------------------------------------------------------------- end of a round
  * The next round's anchors ["DSpark 的实现和测评" §2.1: the anchor of a request is the

@@ -1,4 +1,5 @@
-"""Cache append, paged attention and prompt attention by their definitions, in float64.
+"""Cache append and the attentions (paged, of drafted trees, of prompts; with windows) by their
+definitions, in float64.
 
 Inputs and caches are bf16 bit patterns (uint16), as the library takes them; outputs are
 float64, with nothing rounded.  Besides each output row the attention functions return
@@ -10,7 +11,7 @@ import numpy as np
 
 from .context_kv import bf16_decode
 
-__all__ = ["append", "paged", "prompt"]
+__all__ = ["append", "paged", "prompt", "tree", "tree_mask"]
 
 
 def append(x_bits, norm_w_bits, positions, eps, theta):
@@ -48,9 +49,10 @@ def _fill(r, t, h, *row):
     r["out"][t, h], r["lse"][t, h], r["mag"][t, h], r["dot"][t, h] = row
 
 
-def paged(q_bits, k_cache, v_cache, page_table, kv_len, cu_q, page_size, causal, scale):
+def _over_pages(q_bits, k_cache, v_cache, page_table, kv_len, cu_q, page_size, sees, scale):
     """Rows of request b: the tokens cu_q[b] .. cu_q[b+1] - 1, the last of kv_len[b] cached
-    ones; a page outside the cache hides its keys."""
+    ones; a page outside the cache hides its keys.  sees(t, keys, place, context): which of the
+    keys the token t sees, whose own place is place."""
     q = bf16_decode(q_bits)
     T, nh, hd = q.shape
     S, nkv, _ = k_cache.shape
@@ -59,13 +61,14 @@ def paged(q_bits, k_cache, v_cache, page_table, kv_len, cu_q, page_size, causal,
     for b in range(len(kv_len)):
         n = int(cu_q[b + 1]) - int(cu_q[b])
         kv = min(max(int(kv_len[b]), 0), width * page_size)
-        pages = page_table[b][np.arange(kv) // page_size].astype(np.int64)
+        keys = np.arange(kv)
+        pages = page_table[b][keys // page_size].astype(np.int64)
         there = (pages >= 0) & (pages < S // page_size)
-        slots = np.where(there, pages * page_size + np.arange(kv) % page_size, 0)
+        slots = np.where(there, pages * page_size + keys % page_size, 0)
         k, v = bf16_decode(k_cache[slots]), bf16_decode(v_cache[slots])
         for j in range(n):
             t = int(cu_q[b]) + j
-            seen = there & (np.arange(kv) <= kv - n + j) if causal else there
+            seen = there & sees(t, keys, kv - n + j, kv - n)
             r["keys"][t], r["written"][t] = seen.sum(), True
             for h in range(nh):
                 g = h // (nh // nkv)
@@ -73,7 +76,47 @@ def paged(q_bits, k_cache, v_cache, page_table, kv_len, cu_q, page_size, causal,
     return r
 
 
-def prompt(q_bits, k_bits, v_bits, cu_seqlens, causal, scale):
+def _recent(keys, place, window, sinks):
+    """Those of the keys that a window up to `place`, and the sinks, leave."""
+    return np.ones(len(keys), bool) if window is None else (keys > place - window) | (keys < sinks)
+
+
+def paged(q_bits, k_cache, v_cache, page_table, kv_len, cu_q, page_size, causal, scale, window=None, sinks=0):
+    return _over_pages(q_bits, k_cache, v_cache, page_table, kv_len, cu_q, page_size,
+                       lambda t, keys, place, ctx: (keys <= place if causal else True) & _recent(keys, place, window, sinks),
+                       scale)
+
+
+def tree(q_bits, k_cache, v_cache, page_table, kv_len, cu_q, mask, page_size, scale):
+    """mask [T, 4] uint32: bit i of a token's 128 says that it sees token i of its block."""
+    bits = (np.asarray(mask, np.uint32)[:, :, None] >> np.arange(32, dtype=np.uint32)) & 1
+    bits = np.concatenate([bits.reshape(len(mask), 128).astype(bool), np.zeros((len(mask), 1), bool)], 1)
+
+    def sees(t, keys, place, ctx):
+        return (keys < ctx) | bits[t, np.clip(keys - ctx, 0, 128)]
+
+    return _over_pages(q_bits, k_cache, v_cache, page_table, kv_len, cu_q, page_size, sees, scale)
+
+
+def tree_mask(parent, kv_len, cu_q):
+    """-> mask [T, 4] uint32 and positions [T]: the sets of a node and what is above it, walked
+    up node by node."""
+    T = len(parent)
+    mask, positions = np.zeros((T, 4), np.uint32), np.zeros(T, np.int64)
+    for b in range(len(kv_len)):
+        lo, n = int(cu_q[b]), int(cu_q[b + 1]) - int(cu_q[b])
+        for j in range(n):
+            i, above = j, -1
+            while i >= 0:
+                mask[lo + j, i // 32] |= np.uint32(1 << i % 32)
+                above += 1
+                p = int(parent[lo + i])
+                i = p if 0 <= p < i else -1
+            positions[lo + j] = int(kv_len[b]) - n + above
+    return mask, positions
+
+
+def prompt(q_bits, k_bits, v_bits, cu_seqlens, causal, scale, window=None, sinks=0):
     q, k, v = bf16_decode(q_bits), bf16_decode(k_bits), bf16_decode(v_bits)
     T, nh, hd = q.shape
     nkv = k.shape[1]
@@ -82,8 +125,9 @@ def prompt(q_bits, k_bits, v_bits, cu_seqlens, causal, scale):
         lo, hi = int(cu_seqlens[b]), int(cu_seqlens[b + 1])
         for t in range(lo, hi):
             end = t + 1 if causal else hi
-            r["keys"][t], r["written"][t] = end - lo, True
+            seen = lo + np.flatnonzero(_recent(np.arange(end - lo), t - lo, window, sinks))
+            r["keys"][t], r["written"][t] = len(seen), True
             for h in range(nh):
                 g = h // (nh // nkv)
-                _fill(r, t, h, *_row(q[t, h], k[lo:end, g], v[lo:end, g], scale))
+                _fill(r, t, h, *_row(q[t, h], k[seen, g], v[seen, g], scale))
     return r
