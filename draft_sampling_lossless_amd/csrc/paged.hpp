@@ -919,6 +919,445 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? RT / 4 : RT == 8 ? 4 : 3) void 
   }
 }
 
+// ------------------------------------------------------------------ large trees, long contexts
+// The same work where it is the products that bound it: a wave takes 32 rows
+// (v_mfma_f32_32x32x16_bf16; lane (h, n) = (lane / 32, lane % 32) holds row n and the keys
+// 8 (i / 4) + 4 h + i % 4 of each 32), a workgroup 256, so that one reading of the cache serves
+// a tree of 64 nodes with four heads on a kv head.  Tiles are of 64 keys.  A wave holds the weights
+// of one tile and the scores of the next at once, so that the first product of the next tile runs
+// beside the exponentials of this one.  K is read one tile ahead of V; four LDS buffers of K and
+// three of V are filled straight from memory, two tiles ahead of their use.  The tiles of the
+// context, which every row sees whole, come first; the tree's own, masked, last.
+// 64 trees of 64 nodes over 4096 keys each, 32/8 heads of 128: 400 us, 0.68 PFLOP/s, 500 by shared
+// tiles; the matrix units are busy a third of the time, a third of the waves' goes by at barriers
+// and loads, a third waiting for the product before.
+template <int HD>
+__device__ __forceinline__ int swizzle32(int r) {
+  if constexpr (HD == 64) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+  return ((r & 3) << 2) | ((r >> 2) & 3);
+}
+
+__device__ __forceinline__ float halves_sum(float v) {
+  uint32_t lo, hi;
+  halves_pair(__float_as_uint(v), lo, hi);
+  return __uint_as_float(lo) + __uint_as_float(hi);
+}
+
+constexpr int kWideWaves = 8, kWideTile = 64;
+template <int HD>
+constexpr int wide_lds() { return 7 * kWideTile * HD * 2 + kWindow * 4; }
+
+template <int HD, bool kSlots, bool kLse>
+__global__ __launch_bounds__(64 * kWideWaves, 2) void paged_wide(Work w) {
+  constexpr int NW = kWideWaves, WT = kWideTile, SB = WT / 32, UG = WT / 16, kWideRows = 32 * NW;
+  constexpr int ROWB = HD * 2, TILEB = WT * ROWB, PIECES = HD / 8;
+  constexpr int LOADS = TILEB / 1024 / NW;        // 1 KB loads of a wave for one tile of K (or V)
+  constexpr int LR = 64 / PIECES;                 // rows of one load
+  extern __shared__ __attribute__((aligned(16))) char smem[];   // four K tiles, three V tiles, slots
+  int32_t* slots = reinterpret_cast<int32_t*>(smem + 7 * TILEB);
+  const PagedArgs& a = w.a;
+  const int u = blockIdx.x / w.unit, rest = blockIdx.x % w.unit;
+  const int kvh = rest % a.nkv, rb = rest / a.nkv;
+  Item it;
+  if (!find_item<kTree>(w, u, it)) return;
+  const int nq = min(it.n, a.max_q), row0 = rb * kWideRows;
+  if (nq * w.G <= row0) return;                   // (no row of this block exists)
+  if (it.pid >= w.pid_cap) return;                // (the workspace holds every range)
+
+  const int lane = threadIdx.x & 63, col = lane & 31, hh = lane >> 5;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int r0 = row0 + 32 * wave, j = (r0 + col) / w.G, h = kvh * w.G + (r0 + col) % w.G;
+  const bool idle = uniform(r0 >= nq * w.G) != 0;  // a wave without rows only loads
+  const bool ok = j < nq;
+  const Row row = row_of<kTree>(a, it, j, ok);
+  const int ctx = it.kv - it.n;
+  bf16x8 qf[HD / 16];
+  {
+    const uint16_t* src = a.q + (size_t)(it.q0 + (ok ? j : 0)) * a.q_stride + (size_t)(ok ? h : 0) * HD;
+#pragma unroll
+    for (int kk = 0; kk < HD / 16; ++kk) {
+      const uint4 v = *reinterpret_cast<const uint4*>(src + 16 * kk + 8 * hh);
+      qf[kk] = __builtin_bit_cast(bf16x8, ok ? v : make_uint4(0, 0, 0, 0));
+    }
+  }
+  floatx16 o[HD / 32];                            // dims 32 d + 8 (i / 4) + 4 h + i % 4 of row n
+#pragma unroll
+  for (int d = 0; d < HD / 32; ++d) o[d] = floatx16{};
+  // m: running maximum, in units of the row's factor rc; mb: m, or 0 while the row has seen
+  // nothing; lx: l of unrounded weights
+  float m = -INFINITY, mb = 0.0f, l = 0.0f, lx = 0.0f, rc = w.c;
+
+  const int32_t* table = a.page_table + (size_t)it.b * a.width;
+  const int64_t rbytes = (int64_t)a.nkv * ROWB;   // bytes between slots
+  const int pmask = (1 << a.page_shift) - 1;
+  const char* kbase = reinterpret_cast<const char*>(a.k_cache + kvh * HD);
+  const char* vbase = reinterpret_cast<const char*>(a.v_cache + kvh * HD);
+  const uint32_t lds0 = lds_address(smem);
+  int gaps = 0;                                   // a key of the window has no slot
+
+  // This wave's loads of a tile: load q takes LR rows of one group of 16.  Where the rows of a
+  // tile lie is found once, for K; V's loads of that tile follow a tile later.
+  uint32_t off[LOADS];                            // byte offset behind the group's first slot
+  int group[LOADS], tile_row[LOADS];
+#pragma unroll
+  for (int q = 0; q < LOADS; ++q) {
+    const int f = uniform(q * NW + wave), r = f * LR + lane / PIECES;
+    group[q] = f * LR >> 4;
+    tile_row[q] = r;
+    off[q] = (uint32_t)(lane % PIECES ^ swizzle32<HD>(r)) << 4;
+    if (!kSlots) off[q] += (uint32_t)(r & 15) * (uint32_t)rbytes;
+  }
+  struct Place {
+    int slot[LOADS];                              // the group's first (kSlots: a lane's own row's), or below 0
+  };
+  auto find = [&](int key0, int win0, int win1) {  // (read a while before it is settled)
+    Place p;
+#pragma unroll
+    for (int q = 0; q < LOADS; ++q)
+      p.slot[q] = kSlots ? slots[min(key0 + tile_row[q], win1 - 1) - win0] : slots[(min(key0 + 16 * group[q], win1 - 1) - win0) >> 4];
+    return p;
+  };
+  auto settle = [&](Place p) {
+#pragma unroll
+    for (int q = 0; q < LOADS; ++q)
+      if (!kSlots) p.slot[q] = uniform(p.slot[q]);
+    return p;
+  };
+  auto issue = [&](const char* base, const Place& p, int q, int key0, uint32_t tile) {
+    const uint32_t lds = uniform(tile + (q * NW + wave) * 1024);
+    const char* at = base + (int64_t)max(p.slot[q], 0) * rbytes;
+    uint32_t o = off[q];
+    if constexpr (kSlots) {
+      load_to_lds16(at + o, lds);
+    } else {
+      if (uniform(gaps || key0 + WT > it.kv)) {   // a key that does not exist reads an existing row
+        const int r = tile_row[q] & 15;
+        o -= (uint32_t)max(r - (p.slot[q] < 0 ? 0 : clampi(it.kv - 1 - key0 - 16 * group[q], 0, 15)), 0) * (uint32_t)rbytes;
+      }
+      load_to_lds16(at, o, lds);
+    }
+  };
+  auto kbuf_of = [&](int t) { return (t & 3) * TILEB; };
+  auto vbuf_of = [&](int t) { return (4 + t % 3) * TILEB; };
+
+  int koff = col * ROWB + ((hh ^ swizzle32<HD>(col)) << 4);   // K operand kk of 32 rows: this lane's row, piece 2 kk + hh
+  int voff[2];                                    // V operand (u, d): keys 16 u + 8 e + 4 hh .. + 3, dim 32 d + col
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = 8 * e + 4 * hh + ((lane & 15) >> 2), dim = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    voff[e] = r * ROWB + (((dim >> 3) ^ swizzle32<HD>(r)) << 4) + ((dim & 4) << 1);
+  }
+  union VFrag {
+    shortx4 s[2];
+    uint32_t w[4];
+    bf16x8 v;
+  };
+  auto key_frag = [&](const char* kb, int s, int kk) {
+    return *reinterpret_cast<const bf16x8*>(kb + ((koff ^ (kk << 5)) + 32 * s * ROWB));
+  };
+  auto value_frag = [&](const char* vb, int u, int d) {
+    VFrag f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) f.s[e] = lds_read_tr(vb + ((voff[e] ^ (d << 6)) + 16 * u * ROWB));
+    return f;
+  };
+  auto scores = [&](floatx16 (&sc)[SB], const char* kb) {
+#pragma unroll
+    for (int s = 0; s < SB; ++s) {
+      sc[s] = floatx16{};
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; ++kk)
+        sc[s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_frag(kb, s, kk), qf[kk], sc[s], 0, 0, 0);
+    }
+  };
+  auto row_max = [&](const floatx16 (&sc)[SB]) {
+    float top = sc[0][0];
+#pragma unroll
+    for (int s = 0; s < SB; ++s)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[s][e]);
+    uint32_t lo, hi;
+    halves_pair(__float_as_uint(top), lo, hi);
+    return fmaxf(__uint_as_float(lo), __uint_as_float(hi));
+  };
+  // raise the maxima that the scores exceed by too much
+  auto raise = [&](float top) {
+    const bool up = top * rc > m + kRaise;
+    if (uniform(__any(up))) {
+      if (up) rc = row_factor(top, w.c);
+      const float mn = up ? top * rc : m;
+      const float al = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      mb = mn == -INFINITY ? 0.0f : mn;
+      l *= al;
+      lx *= al;
+#pragma unroll
+      for (int d = 0; d < HD / 32; ++d) o[d] *= al;
+    }
+  };
+  // weights of keys 16 u + 8 half .. of the tile, rounded to bf16 (the second product's operand
+  // type), and their sums
+  auto weights = [&](const floatx16 (&sc)[SB], int u, int half, uint32_t (&p)[4]) {
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(sc[u >> 1][8 * (u & 1) + 4 * half + e], rc, -mb));
+    if (kLse) lx += (x[0] + x[1]) + (x[2] + x[3]);
+    p[2 * half] = pack_bf16x2(x[0], x[1]);
+    p[2 * half + 1] = pack_bf16x2(x[2], x[3]);
+    l = add_bf16x2(p[2 * half + 1], add_bf16x2(p[2 * half], l));
+    asm volatile("" : "+v"(p[2 * half]), "+v"(p[2 * half + 1]));
+  };
+  auto as_frag = [](const uint32_t (&p)[4]) { return __builtin_bit_cast(bf16x8, make_uint4(p[0], p[1], p[2], p[3])); };
+
+  constexpr int wkeys = kSlots ? kWindow : kWindow * 16;
+  for (int win0 = it.k0; win0 < it.k1; win0 += wkeys) {
+    const int win1 = min(it.k1, win0 + wkeys);
+    __syncthreads();
+    {
+      const int entries = kSlots ? win1 - win0 : (win1 - win0 + 15) >> 4;
+      int missing = 0;
+      for (int e = threadIdx.x; e < entries; e += 64 * NW) {
+        const int key = win0 + (kSlots ? e : e << 4), page = table[key >> a.page_shift];
+        const int slot = page >= 0 && page < a.num_pages ? (page << a.page_shift) + (key & pmask) : -1;
+        slots[e] = slot;
+        missing |= slot < 0;
+      }
+      gaps = uniform(__syncthreads_or(missing));
+    }
+    const int nt = (win1 - win0 + WT - 1) / WT;
+    const int nfull = gaps ? 0 : clampi((min(win1, ctx) - win0) / WT, 0, nt);
+    int t = 0;
+    // At tile t the loads of K t + 3 and V t + 2 are issued; those of the tile before may be on
+    // their way, older ones (K t + 1 and V t, and all before) have landed, everyone's after the
+    // barrier, and everyone is done with the tile before.
+    auto open_tile = [&]() {
+      if (uniform(t + 2 < nt)) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * LOADS) : "memory");
+      else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      lds_barrier();
+    };
+    Place next, last;                             // of K t + 3, of V t + 2
+    {
+      const Place p0 = settle(find(win0, win0, win1)), p1 = settle(find(win0 + WT, win0, win1));
+      next = settle(find(win0 + 2 * WT, win0, win1));
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q) issue(kbase, p0, q, win0 + 0 * WT, lds0 + kbuf_of(0));
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q)
+        if (nt > 1) issue(kbase, p1, q, win0 + 1 * WT, lds0 + kbuf_of(1));
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q) issue(vbase, p0, q, win0 + 0 * WT, lds0 + vbuf_of(0));
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q)
+        if (nt > 2) issue(kbase, next, q, win0 + 2 * WT, lds0 + kbuf_of(2));
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q)
+        if (nt > 1) issue(vbase, p1, q, win0 + 1 * WT, lds0 + vbuf_of(1));
+      last = next;
+      next = settle(find(win0 + 3 * WT, win0, win1));
+    }
+    auto issue_k = [&](int q) {
+      if (uniform(t + 3 < nt)) issue(kbase, next, q, win0 + (t + 3) * WT, lds0 + kbuf_of(t + 3));
+    };
+    auto issue_v = [&](int q) {
+      if (uniform(t + 2 < nt)) issue(vbase, last, q, win0 + (t + 2) * WT, lds0 + vbuf_of(t + 2));
+    };
+    auto advance = [&](const Place& found) {
+      ++t;
+      last = next;
+      next = settle(found);
+    };
+    auto find_next = [&]() { return find(win0 + (t + 4) * WT, win0, win1); };
+
+    // tiles that every row sees whole: cur holds tile t's scores, nxt takes the next tile's (of no
+    // use after the last)
+    constexpr int KG = SB * (HD / 16) / 4, VG = HD / 32;
+    auto step = [&](floatx16 (&cur)[SB], floatx16 (&nxt)[SB]) {
+      open_tile();
+      const Place found = find_next();
+      asm volatile("" : "+v"(koff), "+v"(voff[0]), "+v"(voff[1]));   // (flipped offsets are cheaper than registers)
+      const char* kb = smem + kbuf_of(t + 1);
+      const char* vb = smem + vbuf_of(t);
+      bf16x8 kf[2][KG];
+      uint32_t p[UG][4];
+      VFrag vf[2][VG];
+#pragma unroll
+      for (int i = 0; i < KG; ++i) kf[0][i] = key_frag(kb, i % SB, i / SB);
+#pragma unroll
+      for (int gq = 0; gq < 4; ++gq) {
+        if (gq < 3) {
+#pragma unroll
+          for (int i = 0; i < KG; ++i) {
+            const int f = (gq + 1) * KG + i;
+            kf[(gq + 1) & 1][i] = key_frag(kb, f % SB, f / SB);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < VG; ++i) vf[0][i] = value_frag(vb, 0, i);
+        }
+        if (gq == 0)
+#pragma unroll
+          for (int s = 0; s < SB; ++s) nxt[s] = floatx16{};
+        weights(cur, gq >> 1, gq & 1, p[gq >> 1]);
+#pragma unroll
+        for (int i = 0; i < KG; ++i) {
+          const int f = gq * KG + i;
+          nxt[f % SB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[gq & 1][i], qf[f / SB], nxt[f % SB], 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int q = 0; q < LOADS; ++q)
+          if (q * 4 / LOADS == gq) issue_k(q);
+      }
+      float tm = 0.0f;
+#pragma unroll
+      for (int u = 0; u < UG; ++u) {
+        if (u < UG - 1)
+#pragma unroll
+          for (int i = 0; i < VG; ++i) vf[(u + 1) & 1][i] = value_frag(vb, u + 1, i);
+        if (UG > 2 && u == 0) {
+          weights(cur, 2, 0, p[2]);
+          weights(cur, 2, 1, p[2]);
+        } else if (UG > 2 && u < 3) {
+          weights(cur, 3, u - 1, p[3]);
+        }
+        if (u == UG - 1) tm = row_max(nxt);
+#pragma unroll
+        for (int i = 0; i < VG; ++i)
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[u & 1][i].v, as_frag(p[u]), o[i], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int q = 0; q < LOADS; ++q)
+          if (q * UG / LOADS == u) issue_v(q);
+      }
+      advance(found);
+      if (uniform(t < nfull)) raise(tm);          // (the scores of a tile seen in part are formed again, masked)
+    };
+    auto only_load = [&]() {
+      open_tile();
+      const Place found = find_next();
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q) {
+        issue_k(q);
+        issue_v(q);
+      }
+      advance(found);
+    };
+    if (idle) {
+      if (nfull > 0) open_tile();
+      while (t < nt) only_load();
+      continue;
+    }
+    floatx16 sa[SB];
+    if (uniform(nfull > 0)) {
+      floatx16 sb[SB];
+      open_tile();
+      scores(sa, smem + kbuf_of(0));
+      raise(row_max(sa));
+      while (true) {
+        step(sa, sb);
+        if (uniform(t >= nfull)) break;
+        step(sb, sa);
+        if (uniform(t >= nfull)) break;
+      }
+    }
+    // the others, one product after the other
+    while (t < nt) {
+      const int key0 = win0 + t * WT;
+      const char* kb = smem + kbuf_of(t);
+      const char* vb = smem + vbuf_of(t);
+      open_tile();
+      const Place found = find_next();
+#pragma unroll
+      for (int q = 0; q < LOADS; ++q) {
+        issue_k(q);
+        issue_v(q);
+      }
+      scores(sa, kb);
+      uint32_t held[SB], sees[SB];                // bit i of block s: key 32 s + i exists, the row sees it
+#pragma unroll
+      for (int s = 0; s < SB; ++s) {
+        const int x = key0 + 32 * s, e = max(min(x + (lane & 31), it.kv - 1) - win0, 0);
+        const bool there = x + (lane & 31) < it.kv && slots[kSlots ? e : e >> 4] >= 0;
+        held[s] = (uint32_t)uniform((int)(uint32_t)__ballot(there));
+        sees[s] = held[s] & seen_of<kTree>(a, row, x);
+        const uint32_t mine = sees[s] >> (4 * hh);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (!((mine >> (8 * (e >> 2) + (e & 3))) & 1u)) sa[s][e] = -INFINITY;
+      }
+      raise(row_max(sa));
+#pragma unroll
+      for (int u = 0; u < UG; ++u) {
+        const uint32_t hold = held[u >> 1] >> (16 * (u & 1)), see = sees[u >> 1] >> (16 * (u & 1));
+        if (!uniform((int)(hold & 0xFFFFu))) continue;
+        VFrag f[VG];
+        uint32_t pw[4], top = 0;                  // top: the largest exponent, in the high half
+        weights(sa, u, 0, pw);
+        weights(sa, u, 1, pw);
+        const bf16x8 p = as_frag(pw);
+#pragma unroll
+        for (int d = 0; d < VG; ++d) f[d] = value_frag(vb, u, d);
+        // a value that is not finite must not meet the zero weight of a row that does not see it
+#pragma unroll
+        for (int d = 0; d < VG; ++d)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t e = f[d].w[k] & 0x7F807F80u;
+            top = max(top, max(e, e << 16));
+          }
+        if (!uniform(__any(top >= 0x7F800000u))) {
+#pragma unroll
+          for (int d = 0; d < VG; ++d) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[d].v, p, o[d], 0, 0, 0);
+        } else {
+          // key by key, added only to the rows that see it
+#pragma unroll 1
+          for (int k = 0; k < 16; ++k) {
+            if (!((hold >> k) & 1u)) continue;
+            const int jj = (k & 3) | ((k >> 3) << 2);
+            const uint32_t half = jj & 1 ? 0xFFFF0000u : 0x0000FFFFu;
+            const uint32_t keep = hh == ((k >> 2) & 1) ? half : 0u;
+#pragma unroll
+            for (int d = 0; d < VG; ++d) {
+              const bf16x8 one = __builtin_bit_cast(
+                  bf16x8, make_uint4(jj / 2 == 0 ? f[d].w[0] & keep : 0u, jj / 2 == 1 ? f[d].w[1] & keep : 0u,
+                                     jj / 2 == 2 ? f[d].w[2] & keep : 0u, jj / 2 == 3 ? f[d].w[3] & keep : 0u));
+              const floatx16 add = __builtin_amdgcn_mfma_f32_32x32x16_bf16(one, p, floatx16{}, 0, 0, 0);
+              if ((see >> k) & 1u) o[d] += add;
+            }
+          }
+        }
+      }
+      advance(found);
+    }
+  }
+
+  l = halves_sum(l);
+  if (kLse) lx = halves_sum(lx);
+  if (idle || !ok) return;
+  if (it.pid < 0) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const size_t at = (size_t)(it.q0 + j) * a.nh + h;
+#pragma unroll
+    for (int d = 0; d < HD / 32; ++d)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint2*>(a.out + at * HD + 32 * d + 8 * q + 4 * hh) =
+            l == 0.0f ? make_uint2(0u, 0u)
+                      : make_uint2(pack_bf16x2(o[d][4 * q] * inv, o[d][4 * q + 1] * inv),
+                                   pack_bf16x2(o[d][4 * q + 2] * inv, o[d][4 * q + 3] * inv));
+    if (kLse && hh == 0) a.lse[at] = row_lse(m, lx, w.c);
+  } else {
+    const size_t at = ((size_t)it.pid * w.unit + rest) * kWideRows + 32 * wave + col;
+#pragma unroll
+    for (int d = 0; d < HD / 32; ++d)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<floatx4*>(w.part_o + at * HD + 32 * d + 8 * q + 4 * hh) =
+            floatx4{o[d][4 * q], o[d][4 * q + 1], o[d][4 * q + 2], o[d][4 * q + 3]};
+    if (hh == 0) w.part_ml[at] = floatx4{m, l, lx, 0.0f};
+  }
+}
+
 // The ranges of split requests, joined in their order.  A workgroup takes `step` rows of one
 // (request, row block, kv head); hd / 4 threads take a row, four dims each.  Up to kFew
 // ranges they do so alone, every row of the workgroup at once; of more ranges the
@@ -1025,11 +1464,13 @@ __global__ __launch_bounds__(256) void paged_join(Work w, int step) {
 }
 
 struct Shape {
+  bool wide;
   int RT, RB, G, unit, target, min_chunk, whole, pid_cap;
   size_t off_o, off_ml, off_req, off_plan, off_count, bytes;
 };
 
-Shape shape_of(int B, int max_q, int nh, int nkv, int hd) {
+template <int kSeen>
+Shape shape_of(int B, int max_q, int nh, int nkv, int hd, int64_t keys) {
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   Shape s;
   s.G = nh / nkv;
@@ -1039,6 +1480,14 @@ Shape shape_of(int B, int max_q, int nh, int nkv, int hd) {
   // 130 us with four waves (two of them only load) and 131 with two, 40 rows 135 with four
   // and 144 with eight, 68 rows 166 with eight and 190 with four.
   s.RT = rows <= 16 ? 1 : rows <= 64 ? 4 : 8;
+  // Large trees: workgroups of 256 rows (paged_wide) where there may be 2048 keys for every
+  // compute unit.  They take longer to start and to end, and go faster in between.  Against shared
+  // tiles, 32/8 heads of 128, in us: trees of 64 nodes, 64 requests of 4096 keys 422 and 504, of 2048
+  // 236 and 281, of 1024 150 and 154, of 512 100 and 78; one request of 65536 keys 122 and 140, of
+  // 8192 48 and 35.  Trees of 32 nodes (128 rows) gained 6% at most by them.  Heads of 256 leave no
+  // registers.
+  s.wide = kSeen == kTree && hd <= 128 && rows > 128 && keys * nkv >= (int64_t)2048 * kCus;
+  if (s.wide) s.RT = 16;
   s.RB = (rows + 16 * s.RT - 1) / (16 * s.RT);
   s.unit = nkv * s.RB;
   // items aimed at: two workgroups on each compute unit (one with heads of 256) draw all
@@ -1046,6 +1495,7 @@ Shape shape_of(int B, int max_q, int nh, int nkv, int hd) {
   // even out: 64 blocks of 16 x 4 rows over 100..4000 keys take 145 us so, 150 at twice
   // and 163 us at four times as many; one token over 131071 keys 104, 110 and 118 us
   s.target = kCus * (hd > 128 ? 1 : 2);
+  if (s.wide) s.target = kCus;
   // A shorter range costs more to start and join than it takes.  A tile of 32 keys takes a
   // workgroup of shared tiles about 0.9 us alone, four tiles the waves of paged_rows; the
   // joining pass, about 5 us.  Calls that leave most of the card idle cut finer: 9 tokens
@@ -1064,9 +1514,19 @@ Shape shape_of(int B, int max_q, int nh, int nkv, int hd) {
   return s;
 }
 
-template <int HD, int RT, bool kSlots, bool kLse, int kSeen>
+template <int HD, int RT, bool kWide, bool kSlots, bool kLse, int kSeen>
 hipError_t launch_rows(const Work& w, int grid, hipStream_t stream) {
-  if constexpr (RT > 1) {
+  if constexpr (kWide) {
+    static_assert(kSeen == kTree, "the only rule whose keys are seen whole from the first on");
+    static_assert(16 * RT == 32 * kWideWaves, "rows of a block");
+    constexpr int lds = wide_lds<HD>();
+    if (lds > 64 * 1024) {
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&paged_wide<HD, kSlots, kLse>),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+      if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((paged_wide<HD, kSlots, kLse>), dim3(grid), dim3(64 * kWideWaves), lds, stream, w);
+  } else if constexpr (RT > 1) {
     constexpr int lds = shared_lds<HD>();
     if (lds > 64 * 1024) {
       const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&paged_shared<HD, RT, kSlots, kLse, kSeen>),
@@ -1085,12 +1545,12 @@ hipError_t launch_rows(const Work& w, int grid, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int HD, int RT, int kSeen>
+template <int HD, int RT, bool kWide, int kSeen>
 hipError_t launch(const Work& w, int grid, hipStream_t stream) {
   const bool slots = w.a.page_shift < 4, lse = w.a.lse != nullptr;
-  const hipError_t e = slots ? lse ? launch_rows<HD, RT, true, true, kSeen>(w, grid, stream) : launch_rows<HD, RT, true, false, kSeen>(w, grid, stream)
-                       : lse ? launch_rows<HD, RT, false, true, kSeen>(w, grid, stream)
-                             : launch_rows<HD, RT, false, false, kSeen>(w, grid, stream);
+  const hipError_t e = slots ? lse ? launch_rows<HD, RT, kWide, true, true, kSeen>(w, grid, stream) : launch_rows<HD, RT, kWide, true, false, kSeen>(w, grid, stream)
+                       : lse ? launch_rows<HD, RT, kWide, false, true, kSeen>(w, grid, stream)
+                             : launch_rows<HD, RT, kWide, false, false, kSeen>(w, grid, stream);
   if (e != hipSuccess || !w.cut) return e;
   const int rows = std::min(16 * RT, w.a.max_q * w.G);
   const int step = std::max(1, std::min(rows, (int)((int64_t)w.a.B * w.unit * rows / kJoinGroups)));
@@ -1099,17 +1559,19 @@ hipError_t launch(const Work& w, int grid, hipStream_t stream) {
 }
 
 template <int HD, int kSeen>
-hipError_t launch_rt(const Work& w, int RT, int grid, hipStream_t stream) {
-  switch (RT) {
-    case 1: return launch<HD, 1, kSeen>(w, grid, stream);
-    case 4: return launch<HD, 4, kSeen>(w, grid, stream);
-    default: return launch<HD, 8, kSeen>(w, grid, stream);
+hipError_t launch_rt(const Work& w, const Shape& s, int grid, hipStream_t stream) {
+  if constexpr (kSeen == kTree && HD <= 128)
+    if (s.wide) return launch<HD, 16, true, kSeen>(w, grid, stream);
+  switch (s.RT) {
+    case 1: return launch<HD, 1, false, kSeen>(w, grid, stream);
+    case 4: return launch<HD, 4, false, kSeen>(w, grid, stream);
+    default: return launch<HD, 8, false, kSeen>(w, grid, stream);
   }
 }
 
 template <int kSeen>
 hipError_t launch_seen(const PagedArgs& a, int hd, void* workspace, hipStream_t stream) {
-  const Shape s = shape_of(a.B, a.max_q, a.nh, a.nkv, hd);
+  const Shape s = shape_of<kSeen>(a.B, a.max_q, a.nh, a.nkv, hd, (int64_t)a.B * ((int64_t)a.width << a.page_shift));
   Work w;
   w.a = a;
   w.G = s.G;
@@ -1145,9 +1607,9 @@ hipError_t launch_seen(const PagedArgs& a, int hd, void* workspace, hipStream_t 
     if (e != hipSuccess) return e;
   }
   switch (hd) {
-    case 64: return launch_rt<64, kSeen>(w, s.RT, (int)items, stream);
-    case 128: return launch_rt<128, kSeen>(w, s.RT, (int)items, stream);
-    case 256: return launch_rt<256, kSeen>(w, s.RT, (int)items, stream);
+    case 64: return launch_rt<64, kSeen>(w, s, (int)items, stream);
+    case 128: return launch_rt<128, kSeen>(w, s, (int)items, stream);
+    case 256: return launch_rt<256, kSeen>(w, s, (int)items, stream);
     default: return hipErrorInvalidValue;
   }
 }

@@ -5,7 +5,9 @@ namespace dspark {
 
 size_t paged_attention_workspace_bytes(int T, int B, int max_q, int nh, int nkv, int hd) {
   (void)T;
-  return shape_of(B, max_q, nh, nkv, hd).bytes;
+  // (a tree's call has shapes of its own, by the keys that there may be)
+  return std::max({shape_of<kBlock>(B, max_q, nh, nkv, hd, 0).bytes, shape_of<kTree>(B, max_q, nh, nkv, hd, 0).bytes,
+                   shape_of<kTree>(B, max_q, nh, nkv, hd, (int64_t)1 << 40).bytes});
 }
 
 hipError_t launch_paged_attention(const PagedArgs& a, int hd, void* workspace, hipStream_t stream) {

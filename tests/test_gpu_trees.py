@@ -77,6 +77,14 @@ def run(c, mask, lse=True, max_q=None):
     return out, ls
 
 
+def widen(c):
+    """The same call under a table for long contexts, which lets large trees take workgroups of
+    256 rows (from 2^19 keys times kv heads that the tables have room for)."""
+    B, have = c["table"].shape
+    width = -(-2 ** 19 // (c["kc"].shape[1] * B * c["page"]))
+    return dict(c, table=np.concatenate([c["table"], np.full((B, max(0, width - have)), -1, np.int32)], 1))
+
+
 def ref(c, mask):
     return oa.tree(c["q"], c["kc"], c["vc"], c["table"], c["kv"], c["cu"], mask, c["page"], c["hd"] ** -0.5)
 
@@ -105,6 +113,11 @@ def masks(g, c):
     (8, 2, 128, 16, [20, 3, 1], [7, 0, 2]),                   # fewer keys than nodes, none
     (16, 1, 128, 16, [40], [200]),                            # 640 rows
     (8, 2, 128, 16, [16] * 70, [200] * 70),
+    (16, 2, 128, 16, [30, 17, 32], [3000, 520, 700]),         # blocks of 256 rows: one, two, part of one
+    (16, 2, 64, 64, [40, 33], [2600, 700]),
+    (16, 2, 128, 1, [20, 17], [2300, 90]),                    # more slots than are looked up at once
+    (16, 2, 64, 2, [24, 128], [1100, 1500]),
+    (6, 2, 128, 32, [64, 5], [18000, 300]),                  # more groups of 16 than are looked up at once
 ])
 def test_tree_attention(nh, nkv, hd, page, qlen, kvlen):
     say(f"tree nh={nh} nkv={nkv} hd={hd} page={page} q={qlen[:4]} kv={kvlen[:4]}")
@@ -115,9 +128,14 @@ def test_tree_attention(nh, nkv, hd, page, qlen, kvlen):
     r = check_rows(out, lse, ref(c, mask), hd, "tree")
     say(f"  worst error at {r:.2f} of its bound")
     assert torch.equal(out, run(c, mask)[0]) and torch.equal(out, run(c, mask, lse=False)[0])
+    c = widen(c)
+    out, lse = run(c, mask)
+    r = check_rows(out, lse, ref(c, mask), hd, "wide")
+    say(f"  worst error at {r:.2f} of its bound")
+    assert torch.equal(out, run(c, mask)[0]) and torch.equal(out, run(c, mask, lse=False)[0])
 
 
-@pytest.mark.parametrize("nh,n", [(4, 3), (4, 40), (1, 128)])
+@pytest.mark.parametrize("nh,n", [(4, 3), (4, 40), (1, 128), (2, 100)])
 def test_any_mask(nh, n):
     """Masks that are no trees: random bits, none (rows that see the context alone, or nothing at
     all), bits of nodes that do not exist."""
@@ -126,15 +144,16 @@ def test_any_mask(nh, n):
         c = paged_case(g, nh, 1, 128, 16, [n], [kv])
         mask = g.integers(0, 2 ** 32, (n, 4), dtype=np.uint32)
         mask[::3] = 0
+        out, lse = run(widen(c), mask)
+        check_rows(out, lse, ref(c, mask), 128, f"wide, kv {kv}")
         out, lse = run(c, mask)
         check_rows(out, lse, ref(c, mask), 128, f"kv {kv}")
         if kv == n:
             assert (host(out)[::3] == 0).all() and np.isneginf(host(lse)[::3]).all()
     mask[:] = 2 ** 32 - 1                          # everything: paged attention without a causal mask
-    out, _ = run(c, mask)
-    full = dsl.paged_attention(dev(c["q"]), dev(c["kc"]), dev(c["vc"]), dev(c["table"]), dev(c["kv"]), dev(c["cu"]),
-                               c["max_q"], 16, causal=False)
-    assert torch.equal(out, full)
+    out, lse = run(c, mask)
+    full = oa.paged(c["q"], c["kc"], c["vc"], c["table"], c["kv"], c["cu"], 16, False, 128 ** -0.5)
+    check_rows(out, lse, full, 128, "full")
 
 
 def test_every_place_of_a_block_in_a_tile():
@@ -145,6 +164,9 @@ def test_every_place_of_a_block_in_a_tile():
             mask = masks(g, c)
             out, lse = run(c, mask)
             check_rows(out, lse, ref(c, mask), 64, f"context {ctx}")
+            c = widen(paged_case(g, 4, 1, 128, page, [37], [2 * ctx + 37]))
+            out, lse = run(c, mask)
+            check_rows(out, lse, ref(c, mask), 128, f"wide, context {2 * ctx}")
 
 
 def test_a_chain_is_causal_attention():
@@ -152,17 +174,16 @@ def test_a_chain_is_causal_attention():
     for nh, qlen, kvlen, page in ((4, [3, 2], [400, 90], 16), (8, [20, 33], [1300, 40], 1), (8, [17], [3000], 64)):
         c = paged_case(g, nh, 2, 128, page, qlen, kvlen)
         parent = np.concatenate([np.arange(-1, n - 1) for n in qlen])
-        out, _ = run(c, oa.tree_mask(parent, c["kv"], c["cu"])[0])
-        want = dsl.paged_attention(dev(c["q"]), dev(c["kc"]), dev(c["vc"]), dev(c["table"]), dev(c["kv"]), dev(c["cu"]),
-                                   c["max_q"], page)
-        assert torch.equal(out, want)
+        out, lse = run(c, oa.tree_mask(parent, c["kv"], c["cu"])[0])
+        chain = oa.paged(c["q"], c["kc"], c["vc"], c["table"], c["kv"], c["cu"], page, True, 128 ** -0.5)
+        check_rows(out, lse, chain, 128, "chain")
 
 
 def test_branches_do_not_see_each_others_infinities():
     g = np.random.default_rng(8)
     parent = [-1, 0, 0, 1, 2, 1, 4]
-    for nh, page in ((2, 16), (8, 16), (8, 1)):    # both kernels
-        c = paged_case(g, nh, 1, 128, page, [7], [60])
+    for nh, page in ((2, 16), (8, 16), (8, 1), (32, 16), (32, 1)):   # every kernel
+        c = widen(paged_case(g, nh, 1, 128, page, [7], [60]))
         mask = oa.tree_mask(parent, c["kv"], c["cu"])[0]
         at = 53 + 2                                # node 2, seen by 2, 4 and 6
         slot = int(c["table"][0, at // page]) * page + at % page
@@ -190,6 +211,10 @@ def test_tree_rows_left_alone_hidden_pages_and_two_streams():
     c["table"][0, 37], c["table"][1, 1] = -1, 10 ** 9      # a page of the block, one of the context
     out, lse = run(c, mask)
     check_rows(out, lse, ref(c, mask), 128, "hidden")
+    d = widen(paged_case(g, 16, 2, 128, 16, [25, 18], [613, 90]))
+    d["table"][0, [0, 37]], d["table"][1, 1] = -1, 10 ** 9
+    m = masks(g, d)
+    check_rows(*run(d, m), ref(d, m), 128, "hidden, wide")
     args = [dev(c[k]) for k in ("q", "kc", "vc", "table", "kv", "cu")] + [dev(mask)]
     outs = [torch.empty_like(out) for _ in range(2)]
     streams = [torch.cuda.Stream() for _ in outs]
