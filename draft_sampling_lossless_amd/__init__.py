@@ -614,12 +614,39 @@ def paged_attention_workspace_size(T: int, B: int, max_q: int, nh: int, nkv: int
     return load().dspark_paged_attention_workspace_size(T, B, max_q, nh, nkv, hd)
 
 
-def _paged(name: str, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
-           kv_len: torch.Tensor, cu_q: torch.Tensor, max_q: int, page_size: int, mask: Optional[torch.Tensor],
-           rule: tuple, scale: Optional[float], out: Optional[torch.Tensor], lse: Optional[torch.Tensor],
-           workspace: Optional[torch.Tensor]) -> torch.Tensor:
-    """The attentions over pages: what they share of checks and arguments; rule: the integers that
-    say what a row sees (mask: where a tree's mask does)."""
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                    kv_len: torch.Tensor, cu_q: torch.Tensor, max_q: int, page_size: int, causal: bool = True,
+                    scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    window: Optional[int] = None, sinks: int = 0) -> torch.Tensor:
+    """Attention of each request's few query tokens over its cache (dspark_paged_attention).
+    q [T, nh, hd] bf16, the tokens cu_q[b] .. cu_q[b+1] - 1 (cu_q [B+1] int32) of request b
+    being the last of its kv_len[b] (int32) cached ones; page p of k_cache, v_cache
+    [num_slots, nkv, hd] is the slots p * page_size .. and page_table [B, max_pages] int32
+    lists a request's pages.  scale defaults to hd ** -0.5.  lse [T, nh] float32, if given,
+    receives each row's log sum of exponentials.  With a window (dspark_paged_attention_window)
+    a token sees the last window keys up to its own place and the first sinks; the pages
+    between them may be gone from the table.  Returns out [T, nh, hd]."""
+    return _paged(q, k_cache, v_cache, page_table, kv_len, cu_q, max_q, page_size, causal, scale, out, lse, workspace,
+                  window, sinks)
+
+
+def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                   kv_len: torch.Tensor, cu_q: torch.Tensor, mask: torch.Tensor, max_q: int, page_size: int,
+                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_attention for blocks that are drafted trees (dspark_tree_attention): a query token
+    sees the context before the block, and the block's tokens that its mask [T, 4] int32 (128
+    bits, as tree_mask writes them) names.  The workspace is paged_attention's."""
+    if mask is None:
+        raise ValueError("mask must be a tensor [T, 4]")
+    return _paged(q, k_cache, v_cache, page_table, kv_len, cu_q, max_q, page_size, True, scale, out, lse, workspace,
+                  None, 0, mask)
+
+
+def _paged(q, k_cache, v_cache, page_table, kv_len, cu_q, max_q, page_size, causal, scale, out, lse, workspace, window,
+           sinks, mask=None) -> torch.Tensor:
+    """The attentions over pages, under one of three rules: mask, window, neither."""
     dev = _device_of(q, "q")
     T, nh, hd = q.shape
     qs = _rows(q, "q", dev, T, nh, hd)
@@ -639,52 +666,32 @@ def _paged(name: str, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
                          dtype=torch.uint8, device=q.device)
     elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{dev}")
-    masks = () if name != "dspark_tree_attention" else (_arg(mask, "mask", _U32, dev, (T, 4)),)
-    _on(dev, name, getattr(lib, name),
-        q.data_ptr(), qs, _arg(k_cache, "k_cache", _BF16, dev, (S, nkv, hd)),
-        _arg(v_cache, "v_cache", _BF16, dev, (S, nkv, hd)), _arg(page_table, "page_table", _I32, dev, (B, width)),
-        _arg(kv_len, "kv_len", _I32, dev, (B,)), _arg(cu_q, "cu_q", _I32, dev, (B + 1,)), *masks,
-        _arg(out, "out", _BF16, dev, (T, nh, hd)), _arg(lse, "lse", _F32, dev, (T, nh)), T, B, max_q, nh, nkv, hd,
-        page_size, width, S // page_size, *rule, hd ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel())
+    scale = hd ** -0.5 if scale is None else scale
+    qp, kp = q.data_ptr(), _arg(k_cache, "k_cache", _BF16, dev, (S, nkv, hd))
+    vp, tp = _arg(v_cache, "v_cache", _BF16, dev, (S, nkv, hd)), _arg(page_table, "page_table", _I32, dev, (B, width))
+    np, cp = _arg(kv_len, "kv_len", _I32, dev, (B,)), _arg(cu_q, "cu_q", _I32, dev, (B + 1,))
+    op, lp = _arg(out, "out", _BF16, dev, (T, nh, hd)), _arg(lse, "lse", _F32, dev, (T, nh))
+    if mask is not None:
+        _on(dev, "dspark_tree_attention", lib.dspark_tree_attention,
+            qp, qs, kp, vp, tp, np, cp, _arg(mask, "mask", _U32, dev, (T, 4)), op, lp, T, B, max_q, nh, nkv, hd,
+            page_size, width, S // page_size, scale, ws.data_ptr(), ws.numel())
+    elif window is not None:
+        _on(dev, "dspark_paged_attention_window", lib.dspark_paged_attention_window,
+            qp, qs, kp, vp, tp, np, cp, op, lp, T, B, max_q, nh, nkv, hd,
+            page_size, width, S // page_size, 1 if causal else 0, _int32(window), _int32(sinks), scale, ws.data_ptr(),
+            ws.numel())
+    elif sinks:
+        raise ValueError("sinks need a window")
+    else:
+        _on(dev, "dspark_paged_attention", lib.dspark_paged_attention,
+            qp, qs, kp, vp, tp, np, cp, op, lp, T, B, max_q, nh, nkv, hd,
+            page_size, width, S // page_size, 1 if causal else 0, scale, ws.data_ptr(), ws.numel())
     return out
 
 
-def _window(window: Optional[int], sinks: int) -> tuple:
-    """window and sinks as the C ABI takes them, in 32 bits; () without a window."""
-    if window is None:
-        if sinks:
-            raise ValueError("sinks need a window")
-        return ()
-    return max(-1, min(window, 2 ** 31 - 1)), max(-1, min(sinks, 2 ** 31 - 1))
-
-
-def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
-                    kv_len: torch.Tensor, cu_q: torch.Tensor, max_q: int, page_size: int, causal: bool = True,
-                    scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
-                    lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                    window: Optional[int] = None, sinks: int = 0) -> torch.Tensor:
-    """Attention of each request's few query tokens over its cache (dspark_paged_attention).
-    q [T, nh, hd] bf16, the tokens cu_q[b] .. cu_q[b+1] - 1 (cu_q [B+1] int32) of request b
-    being the last of its kv_len[b] (int32) cached ones; page p of k_cache, v_cache
-    [num_slots, nkv, hd] is the slots p * page_size .. and page_table [B, max_pages] int32
-    lists a request's pages.  scale defaults to hd ** -0.5.  lse [T, nh] float32, if given,
-    receives each row's log sum of exponentials.  With a window (dspark_paged_attention_window)
-    a token sees the last window keys up to its own place and the first sinks; the pages
-    between them may be gone from the table.  Returns out [T, nh, hd]."""
-    rule = _window(window, sinks)
-    return _paged("dspark_paged_attention_window" if rule else "dspark_paged_attention", q, k_cache, v_cache, page_table,
-                  kv_len, cu_q, max_q, page_size, None, (1 if causal else 0,) + rule, scale, out, lse, workspace)
-
-
-def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
-                   kv_len: torch.Tensor, cu_q: torch.Tensor, mask: torch.Tensor, max_q: int, page_size: int,
-                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
-                   lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """paged_attention for blocks that are drafted trees (dspark_tree_attention): a query token
-    sees the context before the block, and the block's tokens that its mask [T, 4] int32 (128
-    bits, as tree_mask writes them) names.  The workspace is paged_attention's."""
-    return _paged("dspark_tree_attention", q, k_cache, v_cache, page_table, kv_len, cu_q, max_q, page_size, mask, (),
-                  scale, out, lse, workspace)
+def _int32(v: int) -> int:
+    """A length as the C ABI takes it: what passes 32 bits is as good as the largest, or as bad as -1."""
+    return max(-1, min(v, 2 ** 31 - 1))
 
 
 def tree_mask(parent: torch.Tensor, kv_len: torch.Tensor, cu_q: torch.Tensor, max_q: int,
@@ -728,16 +735,22 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     if not isinstance(cu_seqlens, torch.Tensor):
         raise TypeError("cu_seqlens must be a torch.Tensor")
     B = cu_seqlens.numel() - 1
-    rule = _window(window, sinks)
-    if rule and not causal:
-        raise ValueError("a window needs causal attention")
     if out is None:
         out = torch.empty((T, nh, hd), dtype=q.dtype, device=q.device)
-    name = "dspark_prompt_attention_window" if rule else "dspark_prompt_attention"
-    _on(dev, name, getattr(load(), name),
-        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _arg(cu_seqlens, "cu_seqlens", _I32, dev, (B + 1,)),
-        _arg(out, "out", _BF16, dev, (T, nh, hd)), _arg(lse, "lse", _F32, dev, (T, nh)), T, B, nh, nkv, hd,
-        *(rule or (1 if causal else 0,)), hd ** -0.5 if scale is None else scale)
+    cp, op = _arg(cu_seqlens, "cu_seqlens", _I32, dev, (B + 1,)), _arg(out, "out", _BF16, dev, (T, nh, hd))
+    lp, scale = _arg(lse, "lse", _F32, dev, (T, nh)), hd ** -0.5 if scale is None else scale
+    if window is not None:
+        if not causal:
+            raise ValueError("a window needs causal attention")
+        _on(dev, "dspark_prompt_attention_window", load().dspark_prompt_attention_window,
+            q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cp, op, lp, T, B, nh, nkv, hd, _int32(window),
+            _int32(sinks), scale)
+    elif sinks:
+        raise ValueError("sinks need a window")
+    else:
+        _on(dev, "dspark_prompt_attention", load().dspark_prompt_attention,
+            q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cp, op, lp, T, B, nh, nkv, hd, 1 if causal else 0,
+            scale)
     return out
 
 

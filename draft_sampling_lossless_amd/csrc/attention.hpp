@@ -60,6 +60,15 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // branch around one has to be a scalar branch: its condition goes through here.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// bits below n
+__device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// v where bit `at` (a constant) of word is set, else -inf: two instructions, without a condition
+__device__ __forceinline__ float where_bit(uint32_t word, int at, float v) {
+  const uint32_t keep = (uint32_t)((int32_t)(word << (31 - at)) >> 31);
+  return __uint_as_float((__float_as_uint(v) & keep) | (0xFF800000u & ~keep));
+}
+
 // The least power of two that is not below c (c normal, below 2^127)
 __device__ __forceinline__ float power_above(float c) {
   return __uint_as_float((__float_as_uint(c) + 0x7FFFFFu) & 0x7F800000u);

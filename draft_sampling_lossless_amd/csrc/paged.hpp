@@ -260,9 +260,6 @@ __device__ __forceinline__ Row row_of(const PagedArgs& a, const Item& it, int j,
   return r;
 }
 
-// bits below n
-__device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
-
 // bit i: the row sees the key key0 + i (key0 uniform), if it exists
 template <int kSeen>
 __device__ __forceinline__ uint32_t seen_of(const PagedArgs& a, const Row& r, int key0) {
@@ -461,8 +458,7 @@ __global__ __launch_bounds__(64 * NW) void paged_rows(Work w) {
       sees = held & seen_of<kSeen>(a, row, key0);
       const uint32_t mine = sees >> (4 * g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (!((mine >> (16 * (e >> 2) + (e & 3))) & 1u)) sc[e >> 2][e & 3] = -INFINITY;
+      for (int e = 0; e < 8; ++e) sc[e >> 2][e & 3] = where_bit(mine, 16 * (e >> 2) + (e & 3), sc[e >> 2][e & 3]);
 #pragma unroll
       for (int y = 0; y < D::VU; ++y)
 #pragma unroll
@@ -754,8 +750,7 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? RT / 4 : RT == 8 ? 4 : 3) void 
   auto mask = [&](floatx4 (&sc)[2], uint32_t sees) {
     sees >>= 4 * g;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (!((sees >> (16 * (e >> 2) + (e & 3))) & 1u)) sc[e >> 2][e & 3] = -INFINITY;
+    for (int e = 0; e < 8; ++e) sc[e >> 2][e & 3] = where_bit(sees, 16 * (e >> 2) + (e & 3), sc[e >> 2][e & 3]);
   };
   // weights, rounded to bf16 (the second product's operand type), added to two sums
   auto weights = [&](const floatx4 (&sc)[2], float& sum, float& sumx) {
@@ -1282,8 +1277,7 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void paged_wide(Work w) {
         sees[s] = held[s] & seen_of<kTree>(a, row, x);
         const uint32_t mine = sees[s] >> (4 * hh);
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (!((mine >> (8 * (e >> 2) + (e & 3))) & 1u)) sa[s][e] = -INFINITY;
+        for (int e = 0; e < 16; ++e) sa[s][e] = where_bit(mine, 8 * (e >> 2) + (e & 3), sa[s][e]);
       }
       raise(row_max(sa));
 #pragma unroll

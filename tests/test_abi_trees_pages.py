@@ -159,8 +159,8 @@ def test_select_validation(dspark_lib):
 def test_binding_refusals(dspark_lib):
     x, i = torch.zeros(2, 2, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
     t = torch.zeros(2, 2, dtype=torch.int32)
-    with pytest.raises(ValueError, match="sinks"):
-        dsl.paged_attention(x, x, x, t, i, i, 1, 1, sinks=4)
+    with pytest.raises(ValueError, match="mask"):
+        dsl.tree_attention(x, x, x, t, i, i, None, 1, 1)
     for call in (lambda: dsl.tree_attention(x, x, x, t, i, i, t, 1, 1), lambda: dsl.tree_mask(i, i, i, 1),
                  lambda: dsl.kv_compact(x, x, t, i, i, t, i, 1), lambda: dsl.kv_copy_pages(x, x, t, 1),
                  lambda: dsl.pages_resize(t, i, i, i, 1), lambda: dsl.pages_select(t, i, i, i, 1),

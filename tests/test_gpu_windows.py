@@ -289,3 +289,15 @@ def test_windows_in_a_graph_follow_the_lengths():
         assert torch.equal(got, eager)
         c["kv"] = np.array(kv, np.int32)
         check_rows(got, None, ref(c, True, window, sinks), 128, str(kv))
+
+
+def test_refusals():
+    x, i = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    t = torch.zeros(1, 2, dtype=torch.int32, device="cuda")
+    for kw in (dict(sinks=4), dict(window=0), dict(window=-2 ** 40), dict(window=4, sinks=-1)):
+        with pytest.raises((ValueError, dsl.DSparkError)):
+            dsl.paged_attention(x, x, x, t, i[:1], i, 2, 1, **kw)
+        with pytest.raises((ValueError, dsl.DSparkError)):
+            dsl.prompt_attention(x, x, x, i, **kw)
+    with pytest.raises(ValueError, match="causal"):
+        dsl.prompt_attention(x, x, x, i, causal=False, window=4)
