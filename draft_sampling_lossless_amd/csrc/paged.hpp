@@ -1591,6 +1591,16 @@ hipError_t launch_seen(const PagedArgs& a, int hd, void* workspace, hipStream_t 
     return kSeen != kRecent ? held : (int)std::min<int64_t>(held, (int64_t)a.sink_keys + a.window + block + 16);
   };
   w.cut = bound(a.max_q) > s.whole;
+  if (kSeen == kRecent) {
+    // Under a window requests are about as long as each other, and where they alone fill the card,
+    // cutting them costs the plan and the join for nothing: 16 requests of one token under a window of
+    // 2048, 32/8 heads of 128, 26 us whole and 32 cut, 64 of 17 tokens under one of 512 40 and 44, of 2048
+    // 133 and 138; but 4 of one token under 2048 23 and 17, 32 of 17 tokens under 2048 101 and 80,
+    // 16 of one token under 8192 128 and 108, and 256 of 17 tokens under 4096 941 and 902 (lengths from 1 on).
+    const int64_t groups = (int64_t)a.B * s.unit, span = bound(a.max_q);
+    const bool fill = s.RT == 1 ? span <= 32 * groups : span <= 2 * groups || groups >= 2 * kCus;
+    if (fill && groups * span <= (5 << 20)) w.cut = 0;
+  }
   // at most one range per request, plus the ones the balancing adds
   const int64_t most = (int64_t)a.B * s.unit * (w.cut ? (bound(a.T) + s.min_chunk - 1) / s.min_chunk : 1);
   const int64_t items = std::min(most, (int64_t)a.B * s.unit + s.target + s.unit);
