@@ -713,7 +713,7 @@ def tree_mask(parent: torch.Tensor, kv_len: torch.Tensor, cu_q: torch.Tensor, ma
     _on(dev, "dspark_tree_mask", load().dspark_tree_mask,
         _arg(parent, "parent", _I32, dev, (T,)), _arg(kv_len, "kv_len", _I32, dev, (B,)),
         _arg(cu_q, "cu_q", _I32, dev, (B + 1,)), _arg(mask, "mask", _U32, dev, (T, 4)),
-        _arg(positions, "positions", _I32, dev, (T,)), T, B, max_q)
+        _arg(positions, "positions", _I32, dev, (T,)), T, B, _int32(max_q))
     return mask, positions
 
 
@@ -819,7 +819,7 @@ def pages_resize(page_table: torch.Tensor, kv_len: torch.Tensor, new_len: torch.
     _on(dev, "dspark_pages_resize", load().dspark_pages_resize,
         _arg(page_table, "page_table", _I32, dev, (B, width)), _arg(kv_len, "kv_len", _I32, dev, (B,)),
         _arg(new_len, "new_len", _I32, dev, (B,)), _arg(refs, "refs", _I32, dev, (refs.numel(),)),
-        _arg(copies, "copies", _I32, dev, (B, 2)), _arg(served, "served", _I32, dev, (B,)), B, page_size, width,
+        _arg(copies, "copies", _I32, dev, (B, 2)), _arg(served, "served", _I32, dev, (B,)), B, _int32(page_size), width,
         refs.numel())
     return copies, served
 
@@ -843,5 +843,5 @@ def pages_select(page_table: torch.Tensor, kv_len: torch.Tensor, src: torch.Tens
         _arg(page_table, "page_table", _I32, dev, (B, width)), _arg(kv_len, "kv_len", _I32, dev, (B,)),
         _arg(src, "src", _I32, dev, (rows,)), _arg(new_table, "new_table", _I32, dev, (rows, width)),
         _arg(new_len, "new_len", _I32, dev, (rows,)), _arg(refs, "refs", _I32, dev, (refs.numel(),)), B, rows,
-        page_size, width, refs.numel())
+        _int32(page_size), width, refs.numel())
     return new_table, new_len

@@ -664,9 +664,21 @@ dspark_status batch_of(int B, const char* name) {
   return DSPARK_OK;
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + nb && y < x + na;
+// an array of a call: the first `written` of a list overlap no other of it
+struct Array {
+  const void* p;
+  size_t bytes;
+  const char* name;
+};
+template <int N>
+dspark_status apart(const Array (&arrays)[N], int written) {
+  for (int x = 0; x < written; ++x)
+    for (int y = x + 1; y < N; ++y) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(arrays[x].p), b = reinterpret_cast<uintptr_t>(arrays[y].p);
+      REQUIRE(!a || !b || a >= b + arrays[y].bytes || b >= a + arrays[x].bytes, DSPARK_ERR_INVALID,
+              "%s must not overlap %s", arrays[x].name, arrays[y].name);
+    }
+  return DSPARK_OK;
 }
 }  // namespace
 
@@ -752,6 +764,14 @@ dspark_status dspark_tree_mask(const int32_t* parent, const int32_t* kv_len, con
   REQUIRE_PTR(kv_len, "kv_len");
   REQUIRE_PTR(cu_q, "cu_q");
   REQUIRE_PTR16(mask, "mask");
+  const size_t nodes = 4 * (size_t)T, requests = 4 * (size_t)B;
+  const dspark_status st2 = apart({{mask, 4 * nodes, "mask"},
+                                   {positions, nodes, "positions"},
+                                   {parent, nodes, "parent"},
+                                   {kv_len, requests, "kv_len"},
+                                   {cu_q, requests + 4, "cu_q"}},
+                                  2);
+  if (st2 != DSPARK_OK) return st2;
   dspark::TreeArgs a;
   a.parent = parent;
   a.kv_len = kv_len;
@@ -780,7 +800,17 @@ dspark_status dspark_kv_compact(uint16_t* k_cache, uint16_t* v_cache, const int3
   REQUIRE_PTR(cu_q, "cu_q");
   REQUIRE_PTR(path, "path");
   REQUIRE_PTR(accepted, "accepted");
-  REQUIRE(!overlap(new_len, 4 * (size_t)B, kv_len, 4 * (size_t)B), DSPARK_ERR_INVALID, "new_len must not be kv_len");
+  const size_t n = 4 * (size_t)B, cache = (size_t)L * num_pages * page_size * nkv * hd * 2;
+  st = apart({{k_cache, cache, "k_cache"},
+              {v_cache, cache, "v_cache"},
+              {new_len, n, "new_len"},
+              {kv_len, n, "kv_len"},
+              {cu_q, n + 4, "cu_q"},
+              {accepted, n, "accepted"},
+              {path, n * max_path, "path"},
+              {page_table, n * max_pages, "page_table"}},
+             3);
+  if (st != DSPARK_OK) return st;
   dspark::CompactArgs a;
   a.k_cache = k_cache;
   a.v_cache = v_cache;
@@ -811,6 +841,9 @@ dspark_status dspark_kv_copy_pages(uint16_t* k_cache, uint16_t* v_cache, const i
   if (n == 0) return ok();
   REQUIRE_PTR(copies, "copies");
   REQUIRE((reinterpret_cast<uintptr_t>(copies) & 7u) == 0, DSPARK_ERR_INVALID, "copies must be 8-byte aligned");
+  const size_t cache = (size_t)L * num_pages * page_size * nkv * hd * 2;
+  st = apart({{k_cache, cache, "k_cache"}, {v_cache, cache, "v_cache"}, {copies, 8 * (size_t)n, "copies"}}, 2);
+  if (st != DSPARK_OK) return st;
   dspark::CopyArgs a;
   a.k_cache = k_cache;
   a.v_cache = v_cache;
@@ -837,10 +870,14 @@ dspark_status dspark_pages_select(const int32_t* page_table, const int32_t* kv_l
   REQUIRE_PTR(new_len, "new_len");
   REQUIRE_PTR(refs, "refs");
   const size_t was = 4 * (size_t)B, now = 4 * (size_t)rows;
-  REQUIRE(!overlap(page_table, was * max_pages, new_table, now * max_pages), DSPARK_ERR_INVALID,
-          "new_table must not overlap page_table");
-  REQUIRE(!overlap(kv_len, was, new_len, now) && !overlap(src, now, new_len, now), DSPARK_ERR_INVALID,
-          "new_len must not overlap kv_len or src");
+  st = apart({{new_table, now * max_pages, "new_table"},
+              {new_len, now, "new_len"},
+              {refs, 4 * (size_t)num_pages, "refs"},
+              {page_table, was * max_pages, "page_table"},
+              {kv_len, was, "kv_len"},
+              {src, now, "src"}},
+             3);
+  if (st != DSPARK_OK) return st;
   dspark::SelectArgs a;
   a.page_table = page_table;
   a.kv_len = kv_len;
@@ -864,21 +901,19 @@ dspark_status dspark_pages_resize(int32_t* page_table, int32_t* kv_len, const in
   if (st != DSPARK_OK) return st;
   REQUIRE_PTR(page_table, "page_table");
   REQUIRE_PTR(kv_len, "kv_len");
+  REQUIRE((int64_t)B * max_pages < ((int64_t)1 << 31), DSPARK_ERR_UNSUPPORTED, "B * max_pages must be < 2^31");
   REQUIRE_PTR(new_len, "new_len");
   REQUIRE_PTR16(refs, "refs");
   REQUIRE((reinterpret_cast<uintptr_t>(copies) & 7u) == 0, DSPARK_ERR_INVALID, "copies must be 8-byte aligned");
   const size_t n = 4 * (size_t)B;
-  const struct {
-    const void* p;
-    size_t bytes;
-    const char* name;
-  } arrays[] = {{page_table, n * max_pages, "page_table"}, {kv_len, n, "kv_len"},
-                {new_len, n, "new_len"},                   {refs, 4 * (size_t)num_pages, "refs"},
-                {copies, 2 * n, "copies"},                 {served, n, "served"}};
-  for (int x = 0; x < 6; ++x)
-    for (int y = x + 1; y < 6; ++y)
-      REQUIRE(!overlap(arrays[x].p, arrays[x].bytes, arrays[y].p, arrays[y].bytes), DSPARK_ERR_INVALID,
-              "%s must not overlap %s", arrays[y].name, arrays[x].name);
+  st = apart({{page_table, n * max_pages, "page_table"},
+              {kv_len, n, "kv_len"},
+              {refs, 4 * (size_t)num_pages, "refs"},
+              {copies, 2 * n, "copies"},
+              {served, n, "served"},
+              {new_len, n, "new_len"}},
+             5);
+  if (st != DSPARK_OK) return st;
   dspark::ResizeArgs a;
   a.page_table = page_table;
   a.kv_len = kv_len;

@@ -543,7 +543,7 @@ dspark_status dspark_prompt_attention_window(const uint16_t* q, int64_t q_stride
  *   dspark_kv_append's rotation.  NULL: not wanted.
  *   parent, positions [T] int32; mask [T, 4] 32-bit words, 16-byte aligned; kv_len, cu_q,
  *   max_q, B, T as dspark_paged_attention's.  Rows of tokens beyond max_q or behind
- *   cu_q[B] are left as they were.
+ *   cu_q[B] are left as they were.  mask and positions overlap no other array.
  *
  * dspark_tree_attention, once a layer, after the nodes' keys and values are in the cache:
  * dspark_paged_attention with the rule that node j of request b sees every key of the
@@ -566,8 +566,8 @@ dspark_status dspark_tree_attention(const uint16_t* q, int64_t q_stride, const u
  *   for i < accepted[b]; new_len[b] = kv_len[b] - n_b + accepted[b] (NULL: not wanted).
  *   path [B, max_path] int32, the accepted nodes from the first on: ascending, each in
  *   0 .. n_b - 1.  It ends before the first entry that is not (accepted counts as many then).
- *   accepted [B] int32, taken as at most max_path and at least 0; new_len [B] int32, another
- *   array than kv_len.
+ *   accepted [B] int32, taken as at most max_path and at least 0; new_len [B] int32.  The
+ *   caches and new_len overlap no other array, kv_len neither.
  *   k_cache, v_cache [L, num_pages * page_size, nkv, hd] bf16, 16-byte aligned, every layer
  *   under the same page_table; page_table, kv_len, cu_q as dspark_paged_attention's.  A row
  *   whose place, old or new, has no page is left out.  Pages that are written must belong to
@@ -598,21 +598,22 @@ dspark_status dspark_kv_compact(uint16_t* k_cache, uint16_t* v_cache, const int3
  *   If they run out, that request and all behind it that need a page, or grow into a shared
  *   one, are not served: their rows and lengths stay (served[b] = 0).
  *   copies [B, 2] int32, (-1, -1) where nothing is to be copied, or NULL; served [B] int32, 0
- *   or 1, or NULL; refs 16-byte aligned, copies 8-byte aligned; no array may overlap another.
+ *   or 1, or NULL; refs 16-byte aligned, copies 8-byte aligned; no array may overlap another;
+ *   B * max_pages < 2^31.
  *
  * dspark_pages_select makes a new table out of rows of the old: row r of new_table is row
  * src[r] of page_table, new_len[r] its length; a row number outside [0, B) gives an empty
  * row.  Afterwards refs count the new table in place of the old one, whose rows mean nothing
  * any more.  A row taken twice is a fork, a row not taken is freed, a permutation reorders:
  * beams, samples, a batch closed up.
- *   page_table [B, max_pages], new_table [rows, max_pages], not overlapping; kv_len [B],
- *   new_len [rows], src [rows].  1 <= rows <= DSPARK_MAX_SEQS.
+ *   page_table [B, max_pages], new_table [rows, max_pages]; kv_len [B], new_len [rows], src
+ *   [rows].  new_table, new_len and refs overlap no other array.  1 <= rows <= DSPARK_MAX_SEQS.
  *
  * dspark_kv_copy_pages copies pages of every layer: page copies[i, 0] to copies[i, 1], for
  * both caches.  A pair with a side outside [0, num_pages) is passed over.  A page may be the
  * source of several pairs, the destination of one; no page may be both.
- *   copies [n, 2] int32, 8-byte aligned; caches as dspark_kv_compact's; n == 0 enqueues
- *   nothing.  n <= 2^20.
+ *   copies [n, 2] int32, 8-byte aligned; caches as dspark_kv_compact's, apart from each
+ *   other and from copies; n == 0 enqueues nothing.  n <= 2^20.
  *   page_size a power of two, num_pages * page_size < 2^31, max_pages * page_size <= 2^30. */
 dspark_status dspark_pages_resize(int32_t* page_table, int32_t* kv_len, const int32_t* new_len, int32_t* refs,
                                   int32_t* copies, int32_t* served, int B, int page_size, int max_pages,

@@ -74,7 +74,7 @@ def test_prompt_window_validation(dspark_lib):
 
 
 def _mask(**kw):
-    a = dict(parent=FAKE, kv_len=FAKE, cu_q=FAKE, mask=FAKE, positions=FAKE, T=4, B=2, max_q=3, stream=None)
+    a = dict(parent=FAKE, kv_len=2 * FAKE, cu_q=3 * FAKE, mask=4 * FAKE, positions=5 * FAKE, T=4, B=2, max_q=3, stream=None)
     a.update(kw)
     return dsl.load().dspark_tree_mask(*a.values())
 
@@ -86,11 +86,13 @@ def test_tree_mask_validation(dspark_lib):
     for name in ("parent", "kv_len", "cu_q", "mask"):
         assert _mask(**{name: None}) == INVALID and name in _err()
     assert _mask(mask=FAKE_ODD) == INVALID and "aligned" in _err()
+    assert _mask(positions=FAKE + 12) == INVALID and "overlap" in _err()
+    assert _mask(mask=5 * FAKE - 48) == INVALID and _mask(mask=2 * FAKE) == INVALID
 
 
 def _compact(**kw):
-    a = dict(k_cache=FAKE, v_cache=FAKE, page_table=FAKE, kv_len=FAKE, cu_q=FAKE, path=FAKE, accepted=FAKE,
-             new_len=2 * FAKE, B=2, L=3, nkv=2, hd=128, page_size=16, max_pages=8, num_pages=32, max_path=5, stream=None)
+    a = dict(k_cache=FAKE, v_cache=2 * FAKE, page_table=3 * FAKE, kv_len=4 * FAKE, cu_q=5 * FAKE, path=6 * FAKE,
+             accepted=7 * FAKE, new_len=8 * FAKE, B=2, L=3, nkv=2, hd=128, page_size=16, max_pages=8, num_pages=32, max_path=5, stream=None)
     a.update(kw)
     return dsl.load().dspark_kv_compact(*a.values())
 
@@ -105,12 +107,14 @@ def test_compact_validation(dspark_lib):
     for name in ("k_cache", "v_cache", "page_table", "kv_len", "cu_q", "path", "accepted"):
         assert _compact(**{name: None}) == INVALID and name in _err()
     assert _compact(k_cache=FAKE_ODD) == INVALID and _compact(v_cache=FAKE_ODD) == INVALID
-    assert _compact(new_len=FAKE) == INVALID and "kv_len" in _err()
-    assert _compact(new_len=FAKE + 4) == INVALID
+    assert _compact(new_len=4 * FAKE) == INVALID and "kv_len" in _err()
+    assert _compact(new_len=4 * FAKE + 4) == INVALID and _compact(new_len=6 * FAKE + 36) == INVALID
+    assert _compact(v_cache=FAKE) == INVALID and "v_cache" in _err()
+    assert _compact(v_cache=FAKE + 3 * 512 * 256 * 2 - 16) == INVALID and _compact(path=FAKE + 16) == INVALID
 
 
 def _copy(**kw):
-    a = dict(k_cache=FAKE, v_cache=FAKE, copies=FAKE, n=2, L=3, nkv=2, hd=128, page_size=16, num_pages=32, stream=None)
+    a = dict(k_cache=FAKE, v_cache=2 * FAKE, copies=3 * FAKE, n=2, L=3, nkv=2, hd=128, page_size=16, num_pages=32, stream=None)
     a.update(kw)
     return dsl.load().dspark_kv_copy_pages(*a.values())
 
@@ -121,6 +125,7 @@ def test_copy_pages_validation(dspark_lib):
     assert _copy(num_pages=0) == INVALID
     assert _copy(k_cache=None) == INVALID and _copy(v_cache=FAKE_ODD) == INVALID
     assert _copy(copies=None) == INVALID and _copy(copies=FAKE_ODD) == INVALID and "aligned" in _err()
+    assert _copy(v_cache=FAKE) == INVALID and "overlap" in _err() and _copy(copies=2 * FAKE + 8) == INVALID
 
 
 def _resize(**kw):
@@ -138,6 +143,7 @@ def test_resize_validation(dspark_lib):
     assert _resize(refs=FAKE_ODD) == INVALID and _resize(copies=5 * FAKE + 4) == INVALID
     assert _resize(new_len=2 * FAKE) == INVALID and "overlap" in _err()
     assert _resize(served=FAKE + 32) == INVALID and _resize(copies=4 * FAKE) == INVALID
+    assert _resize(B=4096, max_pages=1 << 19, page_size=1) == UNSUPPORTED and "2^31" in _err()
 
 
 def _select(**kw):
@@ -154,6 +160,7 @@ def test_select_validation(dspark_lib):
         assert _select(**{name: None}) == INVALID and name in _err()
     assert _select(new_table=FAKE) == INVALID and _select(new_table=FAKE + 60) == INVALID and "overlap" in _err()
     assert _select(new_len=2 * FAKE) == INVALID and _select(new_len=3 * FAKE) == INVALID
+    assert _select(refs=FAKE) == INVALID and _select(refs=5 * FAKE + 8) == INVALID
 
 
 def test_binding_refusals(dspark_lib):

@@ -227,6 +227,42 @@ def test_tree_rows_left_alone_hidden_pages_and_two_streams():
     assert all(torch.equal(o, out) for o in outs)
 
 
+def test_trees_in_a_graph_follow_the_lengths():
+    """Masks, and attention by workgroups of 256 rows, captured once; lengths and trees change."""
+    g = np.random.default_rng(31)
+    B, n, page = 2, 40, 16
+    c = widen(paged_case(g, 8, 2, 128, page, [n] * B, [900] * B))
+    q = dev(np.concatenate([c["q"].reshape(B * n, -1), c["q"].reshape(B * n, -1)], 1)).unflatten(1, (-1, 128))[:, :8]   # strided
+    args = [q] + [dev(c[k]) for k in ("kc", "vc", "table", "kv", "cu")]
+    parent = dev(np.array(tree_of(g, n) * B, np.int32))
+    mask, pos = torch.empty((B * n, 4), dtype=torch.int32, device="cuda"), torch.empty(B * n, dtype=torch.int32, device="cuda")
+    out = torch.empty((B * n, 8, 128), dtype=torch.int16, device="cuda")
+    ws = torch.empty(dsl.paged_attention_workspace_size(B * n, B, n, 8, 2, 128), dtype=torch.uint8, device="cuda")
+
+    def body():
+        dsl.tree_mask(parent, args[4], args[5], n, mask=mask, positions=pos)
+        dsl.tree_attention(*args, mask, n, page, out=out, workspace=ws)
+
+    body()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        body()
+    for kv in ([900, 41], [300, 899], [40, 640]):
+        trees = tree_of(g, n) + tree_of(g, n, 1)
+        parent.copy_(torch.tensor(trees, dtype=torch.int32))
+        args[4].copy_(torch.tensor(kv, dtype=torch.int32))
+        graph.replay()
+        got = out.clone()
+        out.fill_(SENT)
+        body()
+        assert torch.equal(got, out)
+        c["kv"] = np.array(kv, np.int32)
+        want, places = oa.tree_mask(trees, kv, c["cu"])
+        assert np.array_equal(host(mask).view(np.uint32), want) and np.array_equal(host(pos), places)
+        check_rows(got, None, ref(c, want), 128, str(kv))
+
+
 # ---------------------------------------------------------------- accepted paths
 
 def compact_case(g, L, nkv, hd, page, blocks, ctxs):

@@ -266,6 +266,42 @@ def test_prompt_window_unseen_tokens_do_not_matter():
         assert not np.isfinite(a[sees]).any() and np.isfinite(a[~sees]).all(), hd
 
 
+@pytest.mark.parametrize("hd,n,window", [(64, 2300, 1300), (128, 1700, 700), (256, 400, 150)])
+def test_prompt_window_unseen_tokens_of_long_windows(hd, n, window):
+    """The same where eight waves share a workgroup, at the edges of a row's window and its sinks."""
+    g = np.random.default_rng(hd)
+    sinks, at = 20, (5, 19, 20, 900 if n > 900 else 200)
+    q, k, v = bits(g, n, 4, hd, std=2.0), bits(g, n, 1, hd), bits(g, n, 1, hd)
+    for bad in at:
+        k1, v1 = k.copy(), v.copy()
+        k1[bad], v1[bad] = NAN, INF
+        out, lse = run_prompt(q, k1, v1, np.array([0, n], np.int32), window, sinks)
+        rows = sorted({bad - 1, bad, bad + 1, bad + window - 1, bad + window, bad + window + 1, n - 1})
+        for t in (t for t in rows if 0 <= t < n):
+            seen = np.flatnonzero((np.arange(t + 1) > t - window) | (np.arange(t + 1) < sinks))
+            if bad in seen:
+                assert np.isnan(value(out)[t]).all(), (bad, t)
+            else:
+                r = oa.paged(q[t:t + 1], k[seen], v[seen], np.arange(len(seen))[None], [len(seen)], [0, 1], 1, True, hd ** -0.5)
+                check_rows(out[t:t + 1], lse[t:t + 1], r, hd, f"{bad} {t}")
+
+
+def test_windows_read_column_ranges():
+    """q, k and v as column ranges of one product, under a window; both forms."""
+    g = np.random.default_rng(21)
+    n, nh, nkv, hd = 150, 8, 2, 128
+    q, k, v = bits(g, n, nh, hd, std=2.0), bits(g, n, nkv, hd), bits(g, n, nkv, hd)
+    wide = dev(np.concatenate([x.reshape(n, -1) for x in (q, k, v)], 1))
+    a, b = nh * hd, nkv * hd
+    dq, dk, dv = (wide[:, lo:hi].unflatten(1, (-1, hd)) for lo, hi in ((0, a), (a, a + b), (a + b, a + 2 * b)))
+    cu = dev(np.array([0, 100, n], np.int32))
+    want = dsl.prompt_attention(dev(q), dev(k), dev(v), cu, window=30, sinks=2)
+    assert torch.equal(dsl.prompt_attention(dq, dk, dv, cu, window=30, sinks=2), want)
+    table, kv, cq = dev(np.arange(n, dtype=np.int32)[None]), dev(np.array([n], np.int32)), dev(np.array([0, 9], np.int32))
+    want = dsl.paged_attention(dev(q[-9:]), dev(k), dev(v), table, kv, cq, 9, 1, window=30, sinks=2)
+    assert torch.equal(dsl.paged_attention(dq[-9:], dev(k), dev(v), table, kv, cq, 9, 1, window=30, sinks=2), want)
+
+
 def test_windows_in_a_graph_follow_the_lengths():
     """A captured paged call under a window, replayed as the cache grows past it."""
     g = np.random.default_rng(13)
