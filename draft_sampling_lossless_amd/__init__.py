@@ -548,19 +548,19 @@ def _arg(t: Optional[torch.Tensor], name: str, dtypes, dev: int, shape) -> Optio
     return _ptr(t, name, dtypes, torch.device("cuda", dev), shape)
 
 
-def _device_of(t: torch.Tensor, name: str, dims: str = "[tokens, heads, hd]") -> int:
+def _device_of(t: torch.Tensor, name: str, dim: int = 3, dims: str = "[tokens, heads, hd]") -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device (cuda/hip) tensor")
-    if t.dim() != dims.count(",") + 1:
+    if t.dim() != dim:
         raise ValueError(f"{name} must be {dims}, got shape {tuple(t.shape)}")
     return t.get_device()
 
 
 def _on(dev: int, name: str, call, *args) -> None:
     """call(*args, stream) on dev's current stream, with dev the current device."""
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         status = call(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -701,7 +701,7 @@ def tree_mask(parent: torch.Tensor, kv_len: torch.Tensor, cu_q: torch.Tensor, ma
     parent among its request's nodes cu_q[b] .. cu_q[b+1] - 1 (-1: it hangs on the context).
     Returns mask [T, 4] int32, what each node sees of the block, and positions [T] int32, for
     kv_append."""
-    dev = _device_of(parent, "parent", "[nodes]")
+    dev = _device_of(parent, "parent", 1, "[nodes]")
     T = parent.shape[0]
     if not isinstance(kv_len, torch.Tensor):
         raise TypeError("kv_len must be a torch.Tensor")
@@ -768,7 +768,7 @@ def _layers(k_cache: torch.Tensor, v_cache: torch.Tensor, dev: int, page_size: i
 
 
 def _table(page_table: torch.Tensor) -> Tuple[int, int, int]:
-    return _device_of(page_table, "page_table", "[B, max_pages]"), page_table.shape[0], page_table.shape[1]
+    return _device_of(page_table, "page_table", 2, "[B, max_pages]"), page_table.shape[0], page_table.shape[1]
 
 
 def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
@@ -796,7 +796,7 @@ def kv_copy_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, copies: torch.Te
     """Page copies[i, 0] copied to page copies[i, 1] in every layer of both caches
     (dspark_kv_copy_pages); a pair with a negative side is passed over, as pages_resize
     writes them."""
-    dev = _device_of(copies, "copies", "[n, 2]")
+    dev = _device_of(copies, "copies", 2, "[n, 2]")
     kp, vp, L, nkv, hd, pages = _layers(k_cache, v_cache, dev, page_size)
     n = copies.shape[0]
     _on(dev, "dspark_kv_copy_pages", load().dspark_kv_copy_pages,
@@ -811,11 +811,11 @@ def pages_resize(page_table: torch.Tensor, kv_len: torch.Tensor, new_len: torch.
     page, int32, are updated.  Returns copies [B, 2], the pages to copy by kv_copy_pages before
     anything is appended, and served [B], 0 where the free pages did not last."""
     dev, B, width = _table(page_table)
-    _device_of(refs, "refs", "[num_pages]")
+    _device_of(refs, "refs", 1, "[num_pages]")
     if copies is None:
         copies = torch.empty((B, 2), dtype=torch.int32, device=page_table.device)
     if served is None:
-        served = torch.empty(B, dtype=torch.int32, device=page_table.device)
+        served = torch.empty_like(kv_len)
     _on(dev, "dspark_pages_resize", load().dspark_pages_resize,
         _arg(page_table, "page_table", _I32, dev, (B, width)), _arg(kv_len, "kv_len", _I32, dev, (B,)),
         _arg(new_len, "new_len", _I32, dev, (B,)), _arg(refs, "refs", _I32, dev, (refs.numel(),)),
@@ -832,8 +832,8 @@ def pages_select(page_table: torch.Tensor, kv_len: torch.Tensor, src: torch.Tens
     table afterwards; the old one is done with.  Returns new_table [rows, max_pages] and
     new_len [rows]."""
     dev, B, width = _table(page_table)
-    _device_of(src, "src", "[rows]")
-    _device_of(refs, "refs", "[num_pages]")
+    _device_of(src, "src", 1, "[rows]")
+    _device_of(refs, "refs", 1, "[num_pages]")
     rows = src.numel()
     if new_table is None:
         new_table = torch.empty((rows, width), dtype=torch.int32, device=page_table.device)

@@ -1489,7 +1489,7 @@ Shape shape_of(int B, int max_q, int nh, int nkv, int hd, int64_t keys) {
   // even out: 64 blocks of 16 x 4 rows over 100..4000 keys take 145 us so, 150 at twice
   // and 163 us at four times as many; one token over 131071 keys 104, 110 and 118 us
   s.target = kCus * (hd > 128 ? 1 : 2);
-  if (s.wide) s.target = kCus;
+  if (s.wide) s.target = kCus;                    // (twice as many: 388 us for the 64 ragged trees' 355)
   // A shorter range costs more to start and join than it takes.  A tile of 32 keys takes a
   // workgroup of shared tiles about 0.9 us alone, four tiles the waves of paged_rows; the
   // joining pass, about 5 us.  Calls that leave most of the card idle cut finer: 9 tokens
