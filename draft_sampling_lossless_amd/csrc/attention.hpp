@@ -1,4 +1,4 @@
-// Building blocks of the two attention kernels: bf16 packing, loads into LDS, transposing
+// Building blocks of the attention kernels: bf16 packing, loads into LDS, transposing
 // LDS reads, wave-uniform values.
 #pragma once
 

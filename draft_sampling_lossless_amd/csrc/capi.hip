@@ -902,6 +902,7 @@ dspark_status dspark_pages_resize(int32_t* page_table, int32_t* kv_len, const in
   REQUIRE_PTR(page_table, "page_table");
   REQUIRE_PTR(kv_len, "kv_len");
   REQUIRE((int64_t)B * max_pages < ((int64_t)1 << 31), DSPARK_ERR_UNSUPPORTED, "B * max_pages must be < 2^31");
+  REQUIRE(num_pages <= (1 << 30), DSPARK_ERR_UNSUPPORTED, "num_pages must be <= 2^30 (got %d)", num_pages);
   REQUIRE_PTR(new_len, "new_len");
   REQUIRE_PTR16(refs, "refs");
   REQUIRE((reinterpret_cast<uintptr_t>(copies) & 7u) == 0, DSPARK_ERR_INVALID, "copies must be 8-byte aligned");

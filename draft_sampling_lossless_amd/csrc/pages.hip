@@ -120,8 +120,12 @@ __global__ __launch_bounds__(256) void pages_select_rows(SelectArgs a) {
 // ------------------------------------------------------------------ lengths
 // One workgroup for the whole call, its four steps told apart by barriers: pages given back,
 // needs counted, free pages found and dealt, lengths set.  A thread has up to kEach requests in
-// a row; the r-th need of all requests gets the r-th free page.
+// a row; the r-th need of all requests gets the r-th free page.  A call is a chain of dependent
+// loads and barriers: 64 requests that grow by two pages 7 us, that shrink 7; 256 in groups of four
+// on a page 12, 4096 of them 31, and 137 where all share one page, whose count is one after the
+// other's.
 constexpr int kThreads = 1024, kEach = 4;
+constexpr int kSpan = 4, kPass = kSpan * 4 * kThreads;   // counts looked through at once
 static_assert(kThreads * kEach >= 4096, "DSPARK_MAX_SEQS requests");
 
 // exclusive sum over the workgroup; `part` is LDS of its waves
@@ -148,10 +152,10 @@ __device__ __forceinline__ int block_sum_before(int v, int* part, int& total) {
 }
 
 __global__ __launch_bounds__(kThreads) void pages_resize_all(ResizeArgs a) {
-  // offs: first item of each request; col0: the column of a request's first item; list: pages
-  // that growing requests write in but share, then free pages in their order
+  // offs: first item of each request; col0: the column of a request's first item; list: free
+  // pages in their order
   __shared__ int offs[kThreads * kEach + 1], col0[kThreads * kEach];
-  __shared__ __attribute__((aligned(16))) int list[kThreads * kEach];
+  __shared__ int list[4 * kThreads];
   __shared__ int part[kThreads / 64], torn;
   const int tid = threadIdx.x, each = (a.B + kThreads - 1) / kThreads, b0 = tid * each;
   const int size = 1 << a.page_shift, most = a.width << a.page_shift;
@@ -194,7 +198,19 @@ __global__ __launch_bounds__(kThreads) void pages_resize_all(ResizeArgs a) {
   };
 
   // The counts to look through first are asked for at once, and hold if no page is given back.
-  int4 next = counts_at(4 * tid);
+  int4 next[kSpan];
+  auto first_counts = [&]() {
+#pragma unroll
+    for (int k = 0; k < kSpan; ++k) next[k] = counts_at(k * 4 * kThreads + 4 * tid);
+  };
+  first_counts();
+
+  // Everyone's atomics are done.  (They are carried out by the second-level cache, which this
+  // workgroup alone writes to: a fence for the whole device, some 3 us, is more than is needed.)
+  auto everyone = [&]() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+  };
 
   // pages given back
   int items[kEach];
@@ -225,43 +241,46 @@ __global__ __launch_bounds__(kThreads) void pages_resize_all(ResizeArgs a) {
       *entry = -1;
       if (page >= 0 && page < a.num_pages) atomicSub(a.refs + page, 1);
     }
-    __threadfence();
-    __syncthreads();
+    everyone();
     // (the atomics went to the second-level cache, and the first may hold what was asked for before)
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-    next = counts_at(4 * tid);
+    first_counts();
   }
 
   // A growing request whose last page is not full writes into it.  If others share the page the
-  // request takes a copy, in the requests' order, until one is left that keeps it.
-  int shared[kEach], count[kEach];
+  // request takes a copy; if all who share it do, the last of them keeps it.  All are counted off
+  // at once: where none is left, the count serves to find the last, which counts itself again.
+  int shared[kEach];
+  bool copied[kEach] = {};
   bool any = false;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
-    const int b = b0 + e;
-    shared[e] = -1;
-    count[e] = 0;
-    if (end[e] >= 0 && end[e] < a.num_pages) {
-      count[e] = a.refs[end[e]];
-      if (count[e] > 1) shared[e] = end[e];
-    }
-    any |= shared[e] >= 0;
-    if (e < each && b < a.B) list[b] = shared[e];
+    shared[e] = end[e] >= 0 && end[e] < a.num_pages && a.refs[end[e]] > 1 ? end[e] : -1;
+    copied[e] = shared[e] >= 0;
+    any |= copied[e];
   }
-  bool copied[kEach] = {};
   if (__syncthreads_or(any)) {
+    auto count_of = [&](int page) { return __hip_atomic_load(a.refs + page, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      if (shared[e] < 0) continue;
-      const int b = b0 + e;
-      int earlier = 0, x = 0;
-      for (; x + 4 <= b; x += 4) {
-        const int4 v = *reinterpret_cast<const int4*>(list + x);
-        earlier += (v.x == shared[e]) + (v.y == shared[e]) + (v.z == shared[e]) + (v.w == shared[e]);
-      }
-      for (; x < b; ++x) earlier += list[x] == shared[e];
-      copied[e] = count[e] - earlier > 1;
-    }
+    for (int e = 0; e < kEach; ++e)
+      if (copied[e]) atomicSub(a.refs + shared[e], 1);
+    everyone();
+    bool left[kEach];                             // nobody has it any more
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) left[e] = copied[e] && count_of(shared[e]) == 0;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if (left[e]) atomicMax(a.refs + shared[e], b0 + e + 1);
+    everyone();
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if (left[e] && count_of(shared[e]) == b0 + e + 1) copied[e] = false;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if (left[e] && !copied[e]) __hip_atomic_store(a.refs + shared[e], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    everyone();
   }
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
@@ -271,21 +290,33 @@ __global__ __launch_bounds__(kThreads) void pages_resize_all(ResizeArgs a) {
   if (tid == 0) torn = -1;
   publish(items);
 
-  // The lowest free pages, dealt in order: 4 kThreads counts a pass, the next pass's on their way.
+  // The lowest free pages, dealt in order: kSpan times 4 kThreads counts a pass, the next pass's on
+  // their way.  Spans without a free page, which most are where a pool is nearly full, take no more
+  // than the pass's barrier: with the free pages at the end of 131072 a call takes 16 us, 35 with a pass
+  // for every 4096.
   int found = 0;
   const int needed = total;
-  if (needed > 0) {
-    for (int base = 0; base < a.num_pages && found < needed; base += 4 * kThreads) {
-      const int first = base + 4 * tid;
-      const int4 v = next;
-      if (base + 4 * kThreads < a.num_pages) next = counts_at(first + 4 * kThreads);
+  for (int base = 0; base < a.num_pages && found < needed; base += kPass) {
+    int4 v[kSpan];
+    bool some = false;
+#pragma unroll
+    for (int k = 0; k < kSpan; ++k) {
+      v[k] = next[k];
+      some |= v[k].x == 0 || v[k].y == 0 || v[k].z == 0 || v[k].w == 0;
+      next[k] = counts_at(base + kPass + k * 4 * kThreads + 4 * tid);
+    }
+    if (!__syncthreads_or(some)) continue;
+#pragma unroll
+    for (int k = 0; k < kSpan; ++k) {
+      if (found >= needed) break;
+      const int first = base + k * 4 * kThreads + 4 * tid;
       int here;
-      const int mine = (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
+      const int mine = (v[k].x == 0) + (v[k].y == 0) + (v[k].z == 0) + (v[k].w == 0);
       int at = block_sum_before(mine, part, here);
-      if (v.x == 0) list[at++] = first;
-      if (v.y == 0) list[at++] = first + 1;
-      if (v.z == 0) list[at++] = first + 2;
-      if (v.w == 0) list[at++] = first + 3;
+      if (v[k].x == 0) list[at++] = first;
+      if (v[k].y == 0) list[at++] = first + 1;
+      if (v[k].z == 0) list[at++] = first + 2;
+      if (v[k].w == 0) list[at++] = first + 3;
       __syncthreads();
       const int use = min(here, needed - found);
       for (int x = tid; x < use; x += kThreads) {
@@ -308,10 +339,8 @@ __global__ __launch_bounds__(kThreads) void pages_resize_all(ResizeArgs a) {
       const bool ok = !waits || at + items[e] <= found;
       int32_t* last = a.page_table + (size_t)b * a.width + hold[e] - 1;
       int2 copy = make_int2(-1, -1);
-      if (copied[e] && ok) {
-        copy = make_int2(shared[e], *last);
-        atomicSub(a.refs + shared[e], 1);
-      }
+      if (copied[e] && ok) copy = make_int2(shared[e], *last);
+      if (copied[e] && !ok) atomicAdd(a.refs + shared[e], 1);   // (it still has the page)
       if (!ok && at < found) torn = b;            // (one at most: the needs lie in a row)
       a.kv_len[b] = ok ? now[e] : was[e];
       if (a.copies) reinterpret_cast<int2*>(a.copies)[b] = copy;

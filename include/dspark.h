@@ -599,7 +599,7 @@ dspark_status dspark_kv_compact(uint16_t* k_cache, uint16_t* v_cache, const int3
  *   one, are not served: their rows and lengths stay (served[b] = 0).
  *   copies [B, 2] int32, (-1, -1) where nothing is to be copied, or NULL; served [B] int32, 0
  *   or 1, or NULL; refs 16-byte aligned, copies 8-byte aligned; no array may overlap another;
- *   B * max_pages < 2^31.
+ *   B * max_pages < 2^31, num_pages <= 2^30.
  *
  * dspark_pages_select makes a new table out of rows of the old: row r of new_table is row
  * src[r] of page_table, new_len[r] its length; a row number outside [0, B) gives an empty

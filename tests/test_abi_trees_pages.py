@@ -144,6 +144,7 @@ def test_resize_validation(dspark_lib):
     assert _resize(new_len=2 * FAKE) == INVALID and "overlap" in _err()
     assert _resize(served=FAKE + 32) == INVALID and _resize(copies=4 * FAKE) == INVALID
     assert _resize(B=4096, max_pages=1 << 19, page_size=1) == UNSUPPORTED and "2^31" in _err()
+    assert _resize(num_pages=(1 << 30) + 1, page_size=1) == UNSUPPORTED and "num_pages" in _err()
 
 
 def _select(**kw):

@@ -93,6 +93,27 @@ def test_everyone_shares_one_page():
         assert (copies[:-1, 0] == 77).all() and t[-1, 0] == 77 and r[77] == 1 and served.all()
 
 
+@pytest.mark.parametrize("free", [0, 5, 900, 1400, 3000])
+def test_groups_that_share_and_a_pool_that_may_not_last(free):
+    """1500 requests in groups of 1 to 7 on a page each, most of which grow; 40000 pages, the free ones
+    far behind each other."""
+    g = np.random.default_rng(free)
+    B, P, page = 1500, 40000, 16
+    group = np.repeat(np.arange(B), g.integers(1, 8, B))[:B]
+    table, refs = np.full((B, 4), -1), np.ones(P, np.int64)
+    table[:, 0] = 3 * group
+    refs[:] = 1
+    for p in set(table[:, 0].tolist()):
+        refs[p] = (table[:, 0] == p).sum()
+    refs[g.permutation(np.arange(3 * B, P))[:free]] = 0
+    order = g.permutation(B)                               # groups lie among each other
+    table = table[order]
+    kv = np.full(B, 9)
+    for grows in (1.0, 0.9, 0.3):
+        new = np.where(g.random(B) < grows, g.integers(10, 40, B), g.integers(0, 10, B))
+        check_resize(table, kv, new, refs, page)
+
+
 def test_pages_that_are_not_there_are_passed_over():
     table = np.array([[-1, 3, 99, -7], [5, -1, -1, -1], [2, 1 << 30, -1, -1]])
     refs = np.array([0, 0, 1, 1, 0, 1])
