@@ -44,7 +44,8 @@ __global__ __launch_bounds__(64 * NW, HD > 128 ? 1 : 2) void window_rows(Work w)
   const int at_edge = min((a.sinks + KT - 1) / KT, first_edge);
   const int nt = uniform((ghigh + KT - 1) / KT + at_edge - first_edge);
   const int wfirst = uniform(w0 / w.G - a.window + 1), wlast = uniform(min(n - 1, (w0 + 31) / w.G) - a.window + 1);
-  int my_first = a.sinks > first_edge * KT ? at_edge : at_edge + max(wfirst, 0) / KT - first_edge;
+  // (with sinks, from their tile on: taking it alone and leaving out those between gave -3 to +3%)
+  const int my_first = a.sinks > 0 ? 0 : max(wfirst, 0) / KT - first_edge;
   const int my_end = uniform(whigh > 0 ? at_edge + (whigh + KT - 1) / KT - first_edge : my_first);
   auto tile_at = [&](int t) { return uniform(t < at_edge ? t : t - at_edge + first_edge); };
 
@@ -358,9 +359,7 @@ __global__ __launch_bounds__(64 * NW, HD > 128 ? 1 : 2) void window_rows(Work w)
       ++t;
     }
   };
-  // a few sinks are a fraction of a tile: by themselves; more of them with the others
-  int alone = a.sinks <= 16 ? at_edge : 0;
-  if (a.sinks > 16) my_first = my_end > my_first ? 0 : my_first;
+  int alone = 0;                            // tiles to go over by themselves: none at first, then all
   while (true) {
     while (t < alone) one_tile();
     if (t == nt) break;
