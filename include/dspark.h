@@ -572,7 +572,8 @@ dspark_status dspark_tree_attention(const uint16_t* q, int64_t q_stride, const u
  *   under the same page_table; page_table, kv_len, cu_q as dspark_paged_attention's.  A row
  *   whose place, old or new, has no page is left out.  Pages that are written must belong to
  *   one request (dspark_pages_resize sees to that).  Other rows keep their values.
- *   nkv * hd % 8 == 0 and <= 2^18; 1 <= L <= 1024; 1 <= max_path <= DSPARK_MAX_BLOCK. */
+ *   nkv * hd % 8 == 0 and <= 2^18; 1 <= L <= 1024; 1 <= max_path <= DSPARK_MAX_BLOCK;
+ *   1 <= B <= DSPARK_MAX_SEQS. */
 dspark_status dspark_kv_compact(uint16_t* k_cache, uint16_t* v_cache, const int32_t* page_table,
                                 const int32_t* kv_len, const int32_t* cu_q, const int32_t* path,
                                 const int32_t* accepted, int32_t* new_len, int B, int L, int nkv, int hd,
@@ -614,7 +615,8 @@ dspark_status dspark_kv_compact(uint16_t* k_cache, uint16_t* v_cache, const int3
  * source of several pairs, the destination of one; no page may be both.
  *   copies [n, 2] int32, 8-byte aligned; caches as dspark_kv_compact's, apart from each
  *   other and from copies; n == 0 enqueues nothing.  n <= 2^20.
- *   page_size a power of two, num_pages * page_size < 2^31, max_pages * page_size <= 2^30. */
+ *   All: page_size a power of two, num_pages * page_size < 2^31, max_pages * page_size <= 2^30,
+ *   1 <= B <= DSPARK_MAX_SEQS. */
 dspark_status dspark_pages_resize(int32_t* page_table, int32_t* kv_len, const int32_t* new_len, int32_t* refs,
                                   int32_t* copies, int32_t* served, int B, int page_size, int max_pages,
                                   int num_pages, void* stream);

@@ -202,6 +202,9 @@ def run_prompt(q, k, v, cu, window, sinks, lse=True):
     (4, 2, 64, [90], MOST, MOST),
     (4, 2, 64, [90], 5, MOST),
     (16, 1, 128, [150], 32, 32),
+    (512, 1, 64, [20, 3], 7, 2),                  # more heads on one than a workgroup has rows
+    (2, 1, 64, [3, 0, 17, 40] * 18, 9, 3),        # more sequences than lanes
+    (2, 1, 128, [5, 33, 0] * 70, 20, 1),
 ])
 def test_prompt_window(nh, nkv, hd, lens, window, sinks):
     say(f"prompt window nh={nh} nkv={nkv} hd={hd} lens={lens} window={window} sinks={sinks}")
