@@ -205,7 +205,7 @@ __global__ __launch_bounds__(kThreads) void pages_resize_all(ResizeArgs a) {
   };
   first_counts();
 
-  // Everyone's atomics are done.  (They are carried out by the second-level cache, which this
+  // Everyone's atomics, and loads of what they change, are done.  (They are carried out by the second-level cache, which this
   // workgroup alone writes to: a fence for the whole device, some 3 us, is more than is needed.)
   auto everyone = [&]() {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -268,7 +268,7 @@ __global__ __launch_bounds__(kThreads) void pages_resize_all(ResizeArgs a) {
     bool left[kEach];                             // nobody has it any more
 #pragma unroll
     for (int e = 0; e < kEach; ++e) left[e] = copied[e] && count_of(shared[e]) == 0;
-    __syncthreads();
+    everyone();
 #pragma unroll
     for (int e = 0; e < kEach; ++e)
       if (left[e]) atomicMax(a.refs + shared[e], b0 + e + 1);
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(kThreads) void pages_resize_all(ResizeArgs a) {
 #pragma unroll
     for (int e = 0; e < kEach; ++e)
       if (left[e] && count_of(shared[e]) == b0 + e + 1) copied[e] = false;
-    __syncthreads();
+    everyone();
 #pragma unroll
     for (int e = 0; e < kEach; ++e)
       if (left[e] && !copied[e]) __hip_atomic_store(a.refs + shared[e], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
