@@ -69,11 +69,12 @@ __global__ __launch_bounds__(kCopyThreads) void kv_compact_rows(CompactArgs a) {
         dst[u] = (int64_t)to[first + r] * pieces + p;
       }
     }
+    // every load of the batch has returned, everyone's: its rows may be written
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kFlight; ++u)
       if (dst[u] >= 0) store_streaming(cache + dst[u], v[u]);
-    __syncthreads();
   }
 }
 
@@ -205,8 +206,9 @@ __global__ __launch_bounds__(kThreads) void pages_resize_all(ResizeArgs a) {
   };
   first_counts();
 
-  // Everyone's atomics, and loads of what they change, are done.  (They are carried out by the second-level cache, which this
-  // workgroup alone writes to: a fence for the whole device, some 3 us, is more than is needed.)
+  // Everyone's atomics, and loads of what they change, are done.  (They are carried out by the
+  // second-level cache, which this workgroup alone writes to: a fence for the whole device, some
+  // 3 us, is more than is needed.)
   auto everyone = [&]() {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
