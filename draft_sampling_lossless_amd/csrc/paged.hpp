@@ -95,7 +95,8 @@ template <int kSeen>
 __device__ __forceinline__ int span_of(const PagedArgs& a, int n, int kv, int& skip) {
   skip = 0;
   if constexpr (kSeen == kRecent) {
-    const int low = (kv - n - a.window + 1) & -min(1 << a.page_shift, 16);
+    // (not below 0: the difference of the two is then within 32 bits, whatever the lengths)
+    const int low = max(kv - n - a.window + 1, 0) & -min(1 << a.page_shift, 16);
     skip = max(low - a.sink_keys, 0);
   }
   return kv - skip;

@@ -175,6 +175,28 @@ def test_a_block_longer_than_max_q_and_the_window():
         assert (host(out)[8:120] == SENT).all()
 
 
+@pytest.mark.parametrize("page", [1, 16])
+@pytest.mark.parametrize("width", [0, 2000])
+@pytest.mark.parametrize("nh,qlen,kvlen", [
+    (4, [2], [0]),
+    (4, [4], [1]),
+    (8, [20], [7]),
+    (8, [20, 3, 1, 4], [7, 1, 400, 0]),
+])
+def test_fewer_keys_than_tokens_under_the_longest_window(nh, qlen, kvlen, width, page):
+    """Places before the first key, a window and sinks that pass every length: the begin of the first
+    window lies further below 0 than 32 bits less the sinks hold.  width: keys that the table has
+    room for, so that requests are cut."""
+    say(f"longest window nh={nh} q={qlen} kv={kvlen} width={width} page={page}")
+    c = paged_case(np.random.default_rng(sum(qlen)), nh, 2, 128, page, qlen, kvlen)
+    B, have = c["table"].shape
+    c["table"] = np.concatenate([c["table"], np.full((B, max(0, width // page - have)), -1, np.int32)], 1)
+    for window, sinks in ((MOST, MOST), (MOST, 2 ** 30 - 31), (2 ** 30, 2 ** 30), (3, MOST), (MOST, 1)):
+        for causal in (True, False):
+            out, lse = run(c, causal, window, sinks)
+            check_rows(out, lse, ref(c, causal, window, sinks), 128, f"{window} {sinks} {causal}")
+
+
 # ---------------------------------------------------------------- prompts
 
 def run_prompt(q, k, v, cu, window, sinks, lse=True):
