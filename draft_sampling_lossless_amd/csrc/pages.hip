@@ -262,6 +262,7 @@ __global__ __launch_bounds__(kThreads) void pages_resize_all(ResizeArgs a) {
     any |= copied[e];
   }
   if (__syncthreads_or(any)) {
+    everyone();                                   // (the first counts too: some of them pass through 0 here)
     auto count_of = [&](int page) { return __hip_atomic_load(a.refs + page, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
 #pragma unroll
     for (int e = 0; e < kEach; ++e)

@@ -93,6 +93,27 @@ def test_everyone_shares_one_page():
         assert (copies[:-1, 0] == 77).all() and t[-1, 0] == 77 and r[77] == 1 and served.all()
 
 
+@pytest.mark.parametrize("B", [2, 64, 130])
+@pytest.mark.parametrize("gives_back", [False, True])
+def test_shared_pages_that_all_leave_are_not_free(B, gives_back):
+    """Pairs share a page and both grow, so that its count is 0 for a while; waves without a request
+    look through these counts, and the free pages lie behind them."""
+    page, P = 16, 20000
+    pairs = B // 2
+    for first in (256, 4000, 8192 + 256):
+        table, refs = np.full((B + 1, 3), -1), np.ones(P, np.int64)
+        at = first + 61 * np.arange(pairs) % 3000
+        table[:B, 0] = np.repeat(at, 2)
+        refs[at], refs[P - 2 * B:] = 2, 0
+        kv, new = np.full(B + 1, 7), np.full(B + 1, 20)
+        table[B, :2], kv[B], new[B] = [1, 2], 30, 30
+        if gives_back:
+            new[B] = 10
+        t, k, r, copies, served = check_resize(table, kv, new, refs, page)
+        assert (copies[0:B:2, 0] == at).all() and (copies[1:B:2, 0] == -1).all() and served.all()
+        assert (r[at] == 1).all() and t[0, 0] == (2 if gives_back else P - 2 * B)
+
+
 @pytest.mark.parametrize("free", [0, 5, 900, 1400, 3000])
 def test_groups_that_share_and_a_pool_that_may_not_last(free):
     """1500 requests in groups of 1 to 7 on a page each, most of which grow; 40000 pages, the free ones
