@@ -175,6 +175,49 @@ def test_a_block_longer_than_max_q_and_the_window():
         assert (host(out)[8:120] == SENT).all()
 
 
+@pytest.mark.parametrize("nh,nkv,hd,page,qlen,kvlen,causal,window,sinks,max_q", [
+    # several requests planned, rows straight into registers
+    (8, 2, 128, 16, [1, 1, 1], [5000, 4100, 5003], True, 2000, 4, None),
+    (8, 2, 128, 1, [1, 3, 1], [5000, 30, 4007], True, 2003, 0, None),
+    (16, 2, 64, 64, [2, 2], [6001, 3500], False, 2500, 33, None),
+    (4, 2, 256, 32, [4, 1], [5001, 2700], True, 2100, 65, None),
+    # several requests planned, tiles shared by eight waves, by four, by several row blocks
+    (32, 8, 128, 16, [17, 17], [4000, 3001], True, 1500, 40, None),
+    (32, 8, 128, 16, [17, 9], [4000, 3001], True, 1501, 0, None),
+    (32, 8, 128, 1, [17, 17], [4000, 3001], True, 1500, 40, None),
+    (32, 8, 128, 1, [17, 5], [4000, 3001], True, 1503, 0, None),
+    (8, 2, 128, 16, [9, 3], [3000, 2903], True, 1300, 7, None),
+    (8, 2, 256, 16, [17, 17], [3000, 2500], True, 1400, 20, None),
+    (16, 1, 64, 8, [17, 17], [3000, 2500], False, 1400, 20, None),    # 272 rows
+    # one request, cut without a plan
+    (32, 8, 128, 16, [17], [9000], True, 1500, 40, None),
+    (32, 8, 128, 1, [17], [5000], True, 1500, 0, None),
+    (8, 2, 128, 64, [1], [9001], True, 3500, 0, None),
+    (8, 2, 64, 16, [33], [5000], False, 1111, 64, None),
+    # blocks longer than max_q: their spans pass what the host counts with
+    (2, 1, 64, 16, [120], [4000], True, 1500, 4, 8),
+    (2, 1, 64, 16, [120, 4], [4000, 2300], True, 1500, 4, 8),
+    (8, 2, 128, 16, [700], [4000], True, 1500, 40, 9),
+    (8, 2, 128, 1, [700, 12], [4000, 2500], True, 1500, 0, 9),
+    # whole, as enough workgroups come without a cut: more slots than are looked up at once
+    (64, 64, 64, 1, [17] * 8, [2600, 40, 40, 1900, 17, 40, 40, 40], True, 1500, 40, None),
+    (64, 64, 64, 1, [17] * 8, [2600, 40, 40, 1900, 17, 40, 40, 40], True, 1500, 0, None),
+])
+def test_windows_cut_into_ranges(nh, nkv, hd, page, qlen, kvlen, causal, window, sinks, max_q):
+    """Ranges that begin behind the keys left out, and their join."""
+    say(f"cut nh={nh} nkv={nkv} hd={hd} page={page} q={qlen} kv={kvlen} causal={causal} window={window} sinks={sinks}")
+    c = drop(paged_case(np.random.default_rng(nh + hd + page), nh, nkv, hd, page, qlen, kvlen), window, sinks)
+    out, lse = run(c, causal, window, sinks, max_q=max_q)
+    w = ref(c, causal, window, sinks)
+    for b, n in enumerate(qlen):
+        w["written"][int(c["cu"][b]) + min(n, max_q or n):int(c["cu"][b + 1])] = False
+    r = check_rows(out, lse, w, hd, "cut")
+    say(f"  worst error at {r:.2f} of its bound")
+    assert (host(out)[~w["written"]] == SENT).all()
+    assert torch.equal(out, run(c, causal, window, sinks, max_q=max_q)[0])
+    assert torch.equal(out, run(c, causal, window, sinks, lse=False, max_q=max_q)[0])
+
+
 @pytest.mark.parametrize("page", [1, 16])
 @pytest.mark.parametrize("width", [0, 2000])
 @pytest.mark.parametrize("nh,qlen,kvlen", [
@@ -238,6 +281,29 @@ def test_prompt_window(nh, nkv, hd, lens, window, sinks):
     r = check_rows(out, lse, oa.prompt(q, k, v, cu, True, hd ** -0.5, window, sinks), hd, "prompt window")
     say(f"  worst error at {r:.2f} of its bound")
     assert (host(out)[-2:] == SENT).all() and (host(lse)[-2:] == 7.0).all()
+    assert torch.equal(out, run_prompt(q, k, v, cu, window, sinks, lse=False)[0])
+
+
+@pytest.mark.parametrize("nh,nkv,hd,lens,window", [
+    (2, 2, 64, [1300], 1100),                     # 256 tokens a workgroup: its last waves see later first tiles
+    (4, 1, 64, [1700, 1203], 1090),
+    (5, 1, 64, [1250], 1101),                     # a group that no row block divides
+    (4, 4, 128, [900, 700], 600),
+    (2, 1, 128, [1100, 0, 803], 531),
+    (5, 1, 128, [900], 577),
+])
+@pytest.mark.parametrize("sinks", [0, 37])
+def test_prompt_window_of_eight_waves(nh, nkv, hd, lens, window, sinks):
+    """Windows and sequences above 1024 with heads of 64, above 512 with 128; every row."""
+    say(f"eight waves nh={nh} nkv={nkv} hd={hd} lens={lens} window={window} sinks={sinks}")
+    assert min(window, sum(lens) // len(lens)) > (1024 if hd == 64 else 512)
+    g = np.random.default_rng(nh + hd + sum(lens))
+    T = sum(lens)
+    q, k, v = bits(g, T, nh, hd, std=2.0), bits(g, T, nkv, hd), bits(g, T, nkv, hd)
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    out, lse = run_prompt(q, k, v, cu, window, sinks)
+    r = check_rows(out, lse, oa.prompt(q, k, v, cu, True, hd ** -0.5, window, sinks), hd, "eight waves")
+    say(f"  worst error at {r:.2f} of its bound")
     assert torch.equal(out, run_prompt(q, k, v, cu, window, sinks, lse=False)[0])
 
 
