@@ -637,7 +637,8 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                    lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """paged_attention for blocks that are drafted trees (dspark_tree_attention): a query token
     sees the context before the block, and the block's tokens that its mask [T, 4] int32 (128
-    bits, as tree_mask writes them) names.  The workspace is paged_attention's."""
+    bits, as tree_mask writes them) names.  The workspace is paged_attention's.  Large trees over
+    short contexts go faster under a table that is not wider than they need."""
     if mask is None:
         raise ValueError("mask must be a tensor [T, 4]")
     return _paged(q, k_cache, v_cache, page_table, kv_len, cu_q, max_q, page_size, True, scale, out, lse, workspace,

@@ -511,10 +511,13 @@ dspark_status dspark_prompt_attention(const uint16_t* q, int64_t q_stride, const
  * sees there, the one at place p = kv_len[b] - n_b + j (of a prompt: its token's place) sees
  * those with s > p - window, and those with s < sinks (the first tokens, which keep drawing
  * weight however far the window has moved).  Everything else, errors, layouts, arithmetic,
- * workspace and lse included, is as dspark_paged_attention and dspark_prompt_attention say; a
- * window that reaches past the beginning gives their results.
+ * workspace and lse included, is as dspark_paged_attention and dspark_prompt_attention say.  A
+ * window that reaches past the beginning gives their results within their rounding, not bit
+ * for bit: prompts under a window run a kernel of their own, and a paged call may cut its
+ * requests elsewhere, so that sums are taken in another order.
  *   Only the keys that some row of a request sees are read.  The pages behind the windows,
- *   but for the sinks', may have been given back: their table entries may be -1.
+ *   but for the sinks', may have been given back: their table entries may be -1.  No call finds
+ *   such pages: the caller sets the entries to -1 and counts the pages off (pages, below).
  *   causal 0: keys behind the row's place are seen as before, the window limits those before
  *   it.  Prompts under a window are causal.
  *   window >= 1; sinks >= 0 (both may pass the length). */
@@ -549,7 +552,11 @@ dspark_status dspark_prompt_attention_window(const uint16_t* q, int64_t q_stride
  * dspark_paged_attention with the rule that node j of request b sees every key of the
  * context, s < kv_len[b] - n_b, and of the block's keys kv_len[b] - n_b + i those whose bit
  * i of mask is set (any 128 bits, trees or not; bits of nodes that do not exist count for
- * nothing).  The workspace is dspark_paged_attention's. */
+ * nothing).  The workspace is dspark_paged_attention's.  There is no window over a tree.
+ *   With max_q * nh / nkv > 128 and hd <= 128 the kernel follows the keys that the tables have
+ *   room for, B * max_pages * page_size * nkv, as the lengths are on the device: a wide table over short
+ *   contexts takes the kernel for long ones, at up to one and a half times the other's time.  Results
+ *   of the two are the same within their rounding, not bit for bit. */
 dspark_status dspark_tree_mask(const int32_t* parent, const int32_t* kv_len, const int32_t* cu_q, uint32_t* mask,
                                int32_t* positions, int T, int B, int max_q, void* stream);
 dspark_status dspark_tree_attention(const uint16_t* q, int64_t q_stride, const uint16_t* k_cache,
