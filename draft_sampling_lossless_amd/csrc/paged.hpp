@@ -924,9 +924,10 @@ __global__ __launch_bounds__(64 * RT, HD > 128 ? RT / 4 : RT == 8 ? 4 : 3) void 
 // beside the exponentials of this one.  K is read one tile ahead of V; four LDS buffers of K and
 // three of V are filled straight from memory, two tiles ahead of their use.  The tiles of the
 // context, which every row sees whole, come first; the tree's own, masked, last.
-// 64 trees of 64 nodes over 4096 keys each, 32/8 heads of 128: 400 us, 0.68 PFLOP/s, 500 by shared
-// tiles; the matrix units are busy a third of the time, a third of the waves' goes by at barriers
-// and loads, a third waiting for the product before.
+// 64 trees of 64 nodes over 4096 keys each, 32/8 heads of 128: 350 us, 0.77 PFLOP/s, 485 by shared
+// tiles; the matrix units are busy 0.39 of the time, a third of the waves' goes by at barriers
+// and loads, 0.30 waiting for the product before.  Smaller trees leave waves idle: of 64 trees of 9
+// to 64 nodes over up to 8192 keys (291 us) 39% of the waves' tiles are only loaded.
 template <int HD>
 __device__ __forceinline__ int swizzle32(int r) {
   if constexpr (HD == 64) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
@@ -1477,10 +1478,12 @@ Shape shape_of(int B, int max_q, int nh, int nkv, int hd, int64_t keys) {
   s.RT = rows <= 16 ? 1 : rows <= 64 ? 4 : 8;
   // Large trees: workgroups of 256 rows (paged_wide) where there may be 2048 keys for every
   // compute unit.  They take longer to start and to end, and go faster in between.  Against shared
-  // tiles, 32/8 heads of 128, in us: trees of 64 nodes, 64 requests of 4096 keys 422 and 504, of 2048
-  // 236 and 281, of 1024 150 and 154, of 512 100 and 78; one request of 65536 keys 122 and 140, of
-  // 8192 48 and 35.  Trees of 32 nodes (128 rows) gained 6% at most by them.  Heads of 256 leave no
-  // registers.
+  // tiles, 32/8 heads of 128, in us in a captured graph: trees of 64 nodes, 64 requests of 4096 keys
+  // 350 and 485, of 2048 205 and 244, of 1024 137 and 136; one request of 65536 keys 111 and 129.
+  // Trees of 32 nodes (128 rows) gained 6% at most by them.  Heads of 256 leave no registers.
+  // The host knows what the tables have room for, not the lengths: short contexts under wide tables
+  // pay.  64 requests of 512 keys under a table of 32768, 105 and 86 us, one of 8192 keys under one of
+  // 131072, 52 and 39, one of 613 33 and 21.
   s.wide = kSeen == kTree && hd <= 128 && rows > 128 && keys * nkv >= (int64_t)2048 * kCus;
   if (s.wide) s.RT = 16;
   s.RB = (rows + 16 * s.RT - 1) / (16 * s.RT);
@@ -1490,7 +1493,7 @@ Shape shape_of(int B, int max_q, int nh, int nkv, int hd, int64_t keys) {
   // even out: 64 blocks of 16 x 4 rows over 100..4000 keys take 145 us so, 150 at twice
   // and 163 us at four times as many; one token over 131071 keys 104, 110 and 118 us
   s.target = kCus * (hd > 128 ? 1 : 2);
-  if (s.wide) s.target = kCus;                    // (twice as many: 388 us for the 64 ragged trees' 355)
+  if (s.wide) s.target = kCus;                    // (twice as many: 345 us for the 64 ragged trees' 291)
   // A shorter range costs more to start and join than it takes.  A tile of 32 keys takes a
   // workgroup of shared tiles about 0.9 us alone, four tiles the waves of paged_rows; the
   // joining pass, about 5 us.  Calls that leave most of the card idle cut finer: 9 tokens
@@ -1595,9 +1598,12 @@ hipError_t launch_seen(const PagedArgs& a, int hd, void* workspace, hipStream_t 
   if (kSeen == kRecent) {
     // Under a window requests are about as long as each other, and where they alone fill the card,
     // cutting them costs the plan and the join for nothing: 16 requests of one token under a window of
-    // 2048, 32/8 heads of 128, 26 us whole and 32 cut, 64 of 17 tokens under one of 512 40 and 44, of 2048
-    // 133 and 138; but 4 of one token under 2048 23 and 17, 32 of 17 tokens under 2048 101 and 80,
-    // 16 of one token under 8192 128 and 108, and 256 of 17 tokens under 4096 941 and 902 (lengths from 1 on).
+    // 2048, 32/8 heads of 128, in us in a captured graph, 39.6 whole and 41.7 cut, 64 of 17 tokens under one
+    // of 512 46 and 52, of 2048 129 and 135; but 4 of one token under 2048 27 and 20, 32 of 17 tokens under
+    // 2048 107 and 85, 16 of one token under 8192 130 and 110.  Large calls even out by the cut what their
+    // uneven ends cost: 256 of 1 to 17 tokens under 1024 247 and 267, 1500 337 and 339, 2048 440 and
+    // 440, 2600 543 and 541, 3500 713 and 702, 4096 820 and 813, 8192 1570 and 1486.  The last condition's
+    // bound lies at about 2500 of these, where the two are within a hundredth.
     const int64_t groups = (int64_t)a.B * s.unit, span = bound(a.max_q);
     const bool fill = s.RT == 1 ? span <= 32 * groups : span <= 2 * groups || groups >= 2 * kCus;
     if (fill && groups * span <= (5 << 20)) w.cut = 0;

@@ -18,17 +18,19 @@ __device__ __forceinline__ void store_streaming(uint4* p, const uint4& v) {
 }
 
 // ------------------------------------------------------------------ rows and pages
-// Bytes copied, nothing else: memory's rate is the bound, 4.98 TB/s for a copy of 2 GiB.  A thread
+// Bytes copied, nothing else: memory's rate is the bound, 4.9 TB/s for a copy of 2 GiB.  A thread
 // has kFlight pieces of 16 bytes on their way, and stores them past the caches' order of
-// replacement: 192 pages of 32 KB in five layers, keys and values, 23 us so and 52 with plain stores.
+// replacement: 192 pages of 32 KB in five layers, keys and values, 29 us so (4.3 TB/s) and 33 with plain
+// stores; 19 and 28 for the same pages again and again, which the last-level cache holds in part.
 constexpr int kCopyThreads = 256, kFlight = 4;
 
 // Path entry i of request b moves from place ctx + path[i] to ctx + i, for one layer of keys or
 // values a workgroup.  Paths ascend, so path[i] >= i and no row is written that a later one
 // still reads: batches of rows in their order, each read whole before it is written.  256 trees of
-// 64 nodes with paths of up to 17, five layers of 8 x 128, 90 MB: 16 us, 5.5 TB/s (34 with plain
-// stores, 17 with a thread for every piece of a row and no barriers, which leaves short rows to
-// few threads); 3 us without a row to move.
+// 64 nodes with paths of up to 17, five layers of 8 x 128, 90 MB: 27 us, 3.3 TB/s, and 35 with plain
+// stores; in the same caches again and again, of which the last-level cache holds a part, 17 and 28
+// (there a thread for every piece of a row and no barriers, which leaves short rows to few threads,
+// gained nothing).  3 us without a row to move.
 __global__ __launch_bounds__(kCopyThreads) void kv_compact_rows(CompactArgs a) {
   __shared__ int from[kMaxPath], to[kMaxPath], valid, lead;
   const int b = blockIdx.x, tid = threadIdx.x;
@@ -123,7 +125,7 @@ __global__ __launch_bounds__(256) void pages_select_rows(SelectArgs a) {
 // needs counted, free pages found and dealt, lengths set.  A thread has up to kEach requests in
 // a row; the r-th need of all requests gets the r-th free page.  A call is a chain of dependent
 // loads and barriers: 64 requests that grow by two pages 7 us, that shrink 7; 256 in groups of four
-// on a page 12, 4096 of them 31, and 137 where all share one page, whose count is one after the
+// on a page 12, 4096 of them 32, and 144 where all share one page, whose count is one after the
 // other's.
 constexpr int kThreads = 1024, kEach = 4;
 constexpr int kSpan = 4, kPass = kSpan * 4 * kThreads;   // counts looked through at once

@@ -1,7 +1,7 @@
 // Causal prompt attention under a window with sinks.
 //
-// 32/8 heads of 128: 16384 tokens under a window of 4096 1000 us, 0.97 PFLOP/s; four sequences of 4096
-// under one of 256 190 us, where a workgroup has about twelve tiles of 32 keys and its loads and
+// 32/8 heads of 128: 16384 tokens under a window of 4096 985 us, 0.98 PFLOP/s; four sequences of 4096
+// under one of 256 164 us, where a workgroup has about twelve tiles of 32 keys and its loads and
 // stores count.
 #include "prompt.hpp"
 
@@ -451,9 +451,9 @@ hipError_t launch_prompt_window(const PromptArgs& a, int hd, hipStream_t stream)
   const Work w = work_of(a);
   // As in prompt_attention.hip, four waves where a workgroup has few tiles and eight where it has
   // many; under a window it is the window that ends them.  Four sequences of 4096, four waves and
-  // eight: 32/8 heads of 128, a window of 64 129 and 155 us, of 256 190 and 206, of 512 259 and 265,
-  // of 1024 385 and 369, of 4096 693 and 617; 16/2 heads of 64, 46 and 48, 65 and 64, 85 and 87, 117
-  // and 126, 205 and 202.
+  // eight: 32/8 heads of 128, a window of 64 116 and 152 us, of 256 163 and 197, of 512 230 and 251,
+  // of 1024 353 and 353, of 2048 544 and 507, of 4096 681 and 613; 16/2 heads of 64, 49 and 50, 64 and
+  // 65, 81 and 85, 114 and 121, 163 and 164, 201 and 198.
   const int64_t reach = std::min<int64_t>(a.window, a.T / a.B);
   switch (hd) {
     case 64: return reach <= 1024 ? launch<64, 4, 64>(w, stream) : launch<64, 8, 64>(w, stream);
